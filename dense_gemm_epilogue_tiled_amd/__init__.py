@@ -54,6 +54,10 @@ GR_ACT_TANH = 6
 GR_FMT_F16 = 0
 GR_FMT_BF16 = 1
 
+GR_OUT_16 = 0
+GR_OUT_MXFP8 = 1
+GR_OUT_MXFP4 = 2
+
 ACT_CODES = {"none": GR_ACT_NONE, "relu": GR_ACT_RELU, "gelu": GR_ACT_GELU, "gelu_tanh": GR_ACT_GELU_TANH,
              "silu": GR_ACT_SILU, "sigmoid": GR_ACT_SIGMOID, "tanh": GR_ACT_TANH}
 
@@ -191,6 +195,14 @@ def lib() -> ctypes.CDLL:
             l.gemm_mxfp8_bt_plan.restype = i32
             for nm in ("gemm_mxfp4_bt", "gemm_mxfp4_bt_forced", "gemm_mxfp4_bt_plan"):
                 getattr(l, nm).argtypes = getattr(l, nm.replace("mxfp4", "mxfp8")).argtypes
+                getattr(l, nm).restype = i32
+            l.rms_norm_mx.argtypes = [i64, i64, p, i64, p, i64, p, f32, p, i64, p, i64, p, i64, i32, i32, p]
+            l.gated_act_mx.argtypes = [i64, i64, p, i64, p, i64, i32, p, i64, p, i64, i32, i32, p]
+            l.gemm_w4_bt.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, p, i32, p, i64, i32, p]
+            l.moe_route.argtypes = [i64, i64, i64, i64, p, i64, p, i64, p, i32, p, p, i32, p]
+            l.moe_w4_workspace_size.argtypes = [i64, i64, i64, i64, i64, ctypes.POINTER(ctypes.c_int64)]
+            l.moe_w4.argtypes = [i64, i64, i64, i64, i64, p, i64, p, p, p, p, p, p, p, p, i32, p, i64, i32, p, i64, p]
+            for nm in ("rms_norm_mx", "gated_act_mx", "gemm_w4_bt", "moe_route", "moe_w4_workspace_size", "moe_w4"):
                 getattr(l, nm).restype = i32
             l.gemm_relu_status_string.argtypes = [i32]
             l.gemm_relu_status_string.restype = ctypes.c_char_p
@@ -725,3 +737,7 @@ def linear(x, weight, bias=None, act="none", out=None, stream=None, path=None):
     if st != GR_OK:
         raise GemmReluError(st, "gemm_bias_act_bt")
     return out
+
+
+from .mx_ops import (gated_act, gated_act_mx, gemm_mxfp4, gemm_w4_bt, linear_mxfp4, moe_mxfp4,  # noqa: E402,F401
+                     moe_route, moe_route_raw, moe_w4, moe_w4_workspace_size, mx_quantize, rms_norm, rms_norm_mx)

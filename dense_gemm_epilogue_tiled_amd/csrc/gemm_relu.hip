@@ -15,6 +15,7 @@
 
 #include "../../include/gemm_relu.h"
 #include "fp8_kernel.hpp"
+#include "host.hpp"
 #include "pack_kernel.hpp"
 #include "probe_kernel.hpp"
 #include "smallm_kernel.hpp"
@@ -34,13 +35,10 @@ static __device__ __align__(256) uint8_t scratch[GR_NOALLOC_SCRATCH_BYTES];
 namespace {
 
 constexpr int kVersion = 200;  // 0.2.0: gr_plan_t.plain_order
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxSpanBytes = int64_t(1) << 62;
 constexpr int kGroupM = 4;          // tile rows per workgroup-order group
 constexpr int kSmallMThreshold = 16;  // rows of A handled by the small-M split and Bt kernels
 constexpr int kSmallMMaxRows = 64;    // rows the single-pass small-M kernel handles (4 blocks of 16)
 constexpr int64_t kPackMinMacs = int64_t(1) << 30;  // smallest M*N*K the planner packs for
-constexpr int64_t kWorkspaceAlign = 256;            // required alignment of a workspace (bytes)
 #ifndef GR_SMALLM_WAVES
 #define GR_SMALLM_WAVES 8
 #endif
@@ -49,21 +47,6 @@ constexpr int64_t kWorkspaceAlign = 256;            // required alignment of a w
 #endif
 constexpr int kSmallMWaves = GR_SMALLM_WAVES;    // waves per small-M workgroup
 constexpr int kSmallMUnroll = GR_SMALLM_UNROLL;  // 32-deep K steps per load group
-
-// Number of bytes spanned by a rows x cols matrix with pitch ld (0 if empty);
-// -1 when it does not fit the library's limits.
-int64_t span_bytes(int64_t rows, int64_t cols, int64_t ld) {
-    if (rows == 0 || cols == 0) return 0;
-    // (rows - 1) * ld + cols elements, checked against 2^62 bytes.
-    const int64_t limit = kMaxSpanBytes / 2;
-    if (rows - 1 > 0 && ld > (limit - cols) / (rows - 1)) return -1;
-    return ((rows - 1) * ld + cols) * 2;
-}
-
-bool overlaps(uintptr_t a, int64_t alen, uintptr_t b, int64_t blen) {
-    if (alen <= 0 || blen <= 0) return false;
-    return a < b + (uintptr_t)blen && b < a + (uintptr_t)alen;
-}
 
 // Widest fp16 vector (8, 2 or 1 elements) every row start of a pitched matrix
 // is aligned to.
@@ -551,25 +534,6 @@ int choose_path(int64_t M, int64_t N, int64_t K, uintptr_t A, int64_t lda, uintp
 }
 
 
-// ---- device check (once per device) ------------------------------------------
-
-constexpr int kMaxDevices = 64;
-std::atomic<int> g_device_state[kMaxDevices];  // 0 unknown, 1 gfx950, 2 other
-
-int check_device() {
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0) return GR_ERR_NO_DEVICE;
-    if (dev >= kMaxDevices) return GR_ERR_UNSUPPORTED_DEVICE;
-    int state = g_device_state[dev].load(std::memory_order_acquire);
-    if (state == 0) {
-        hipDeviceProp_t prop;
-        if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return GR_ERR_NO_DEVICE;
-        state = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 2;
-        g_device_state[dev].store(state, std::memory_order_release);
-    }
-    return state == 1 ? GR_OK : GR_ERR_UNSUPPORTED_DEVICE;
-}
-
 // Device address of the current device's copy of `scratch`, looked up once
 // per device (thread-safe) and kept for later calls.
 std::atomic<uintptr_t> g_scratch_ptr[kMaxDevices];
@@ -595,14 +559,6 @@ int scratch_on_current_device(uint8_t** out) {
 }
 
 // ---- launches ----------------------------------------------------------------
-
-template <typename... Args>
-int launch(void (*kernel)(Args...), int64_t grid, int threads, hipStream_t stream, Args... args) {
-    void* argv[] = {static_cast<void*>(&args)...};
-    hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3((uint32_t)grid), dim3(threads), argv,
-                                   0, stream);
-    return e == hipSuccess ? GR_OK : GR_ERR_LAUNCH;
-}
 
 // The order word the tile kernels take (tile_of_workgroup): the group of tile
 // rows, bit 31 set for the plain order (tile order follows the workgroup id).
@@ -1373,14 +1329,6 @@ int entry_ta(int64_t M, int64_t N, int64_t K, const uint16_t* At, int64_t ldat, 
 }
 
 // ---- fp8 (e4m3) operands, B given transposed -----------------------------------
-
-// Bytes spanned by a rows x cols matrix of 1-byte elements with pitch ld.
-int64_t span_bytes8(int64_t rows, int64_t cols, int64_t ld) {
-    if (rows == 0 || cols == 0) return 0;
-    const int64_t limit = kMaxSpanBytes;
-    if (rows - 1 > 0 && ld > (limit - cols) / (rows - 1)) return -1;
-    return (rows - 1) * ld + cols;
-}
 
 // Argument checks of the fp8 calls; the workspace (ws, ws_bytes) as in
 // validate(), and it must not overlap the bias either.

@@ -1,0 +1,346 @@
+// Host side of the operators around the MX products: RMS norm and gated
+// activation with MX outputs, 16-bit activations times MX fp4 weights, the router
+// and the experts of a mixture-of-experts layer.  See include/gemm_relu.h.
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/gemm_relu.h"
+#include "host.hpp"
+#include "norm_kernel.hpp"
+#include "w4_kernel.hpp"
+
+namespace {
+
+static_assert(GR_OUT_16 == gr::mx::kOut16 && GR_OUT_MXFP8 == gr::mx::kOutMx8 && GR_OUT_MXFP4 == gr::mx::kOutMx4,
+              "output format codes");
+
+bool known_fmt(int fmt) { return fmt == GR_FMT_F16 || fmt == GR_FMT_BF16; }
+bool known_act(int act) { return act >= 0 && act < gr::kActCount; }
+bool known_out(int out) { return out == GR_OUT_16 || out == GR_OUT_MXFP8 || out == GR_OUT_MXFP4; }
+
+struct Region {
+    uintptr_t at;
+    int64_t bytes;
+};
+
+bool overlaps(const Region& a, const Region& b) { return overlaps(a.at, a.bytes, b.at, b.bytes); }
+
+// A rows x cols matrix of 16-bit elements (bytes < 0: too large).
+Region matrix16(const void* p, int64_t rows, int64_t cols, int64_t ld) {
+    return {reinterpret_cast<uintptr_t>(p), p ? span_bytes(rows, cols, ld) : 0};
+}
+Region matrix8(const void* p, int64_t rows, int64_t cols, int64_t ld) {
+    return {reinterpret_cast<uintptr_t>(p), p ? span_bytes8(rows, cols, ld) : 0};
+}
+
+// Columns of one row of an output in `out_fmt`, in the units of its pitch
+// (16-bit elements, or bytes).
+int64_t out_cols(int64_t N, int out_fmt) { return out_fmt == GR_OUT_MXFP4 ? N / 2 : N; }
+
+// Checks shared by rms_norm_mx and gated_act_mx on the output and its scales.
+int validate_out(int64_t M, int64_t N, const void* Y, int64_t ldy, const uint8_t* SY, int64_t ld_sy, int out_fmt,
+                 Region* y, Region* e) {
+    if (!known_out(out_fmt)) return GR_ERR_INVALID_ARG;
+    const bool mx = out_fmt != GR_OUT_16;
+    if (mx && N % 32 != 0) return GR_ERR_INVALID_DIM;
+    const int64_t cols = out_cols(N, out_fmt), blocks = N / 32;
+    if (ldy < (cols > 1 ? cols : 1)) return GR_ERR_INVALID_LD;
+    if (mx && ld_sy < (blocks > 1 ? blocks : 1)) return GR_ERR_INVALID_LD;
+    const bool used = M > 0 && N > 0;
+    if (used && (!Y || (mx && !SY))) return GR_ERR_NULL_PTR;
+    *y = mx ? matrix8(Y, M, cols, ldy) : matrix16(Y, M, cols, ldy);
+    *e = mx ? matrix8(SY, M, blocks, ld_sy) : Region{0, 0};
+    if (y->bytes < 0 || e->bytes < 0) return GR_ERR_TOO_LARGE;
+    return overlaps(*y, *e) ? GR_ERR_ALIAS : GR_OK;
+}
+
+// ---- RMS norm ----------------------------------------------------------------------
+
+// Rows in registers: 64, 256 or 1024 threads with up to 4 chunks of 8
+// columns, the fewest threads that hold the row.
+template <typename E, int OUT, int TPR>
+int launch_norm_tpr(const gr::mx::NormArgs& a, int64_t chunks, hipStream_t stream) {
+    const int threads = TPR < 256 ? 256 : TPR, rows = threads / TPR;
+    const int64_t grid = (a.M + rows - 1) / rows;
+    if (chunks <= TPR) return launch(gr::mx::rms_norm_kernel<E, OUT, TPR, 1>, grid, threads, stream, a);
+    if (chunks <= 2 * TPR) return launch(gr::mx::rms_norm_kernel<E, OUT, TPR, 2>, grid, threads, stream, a);
+    return launch(gr::mx::rms_norm_kernel<E, OUT, TPR, 4>, grid, threads, stream, a);
+}
+
+template <typename E, int OUT>
+int launch_norm(const gr::mx::NormArgs& a, hipStream_t stream) {
+    const int64_t chunks = (a.N + 7) / 8;
+    if (chunks <= 4 * 64) return launch_norm_tpr<E, OUT, 64>(a, chunks, stream);
+    if (chunks <= 4 * 256) return launch_norm_tpr<E, OUT, 256>(a, chunks, stream);
+    if (chunks <= 4 * 1024) return launch_norm_tpr<E, OUT, 1024>(a, chunks, stream);
+    return launch(gr::mx::rms_norm_long_kernel<E, OUT>, a.M, 1024, stream, a);
+}
+
+template <typename E>
+int run_norm(const gr::mx::NormArgs& a, int out_fmt, hipStream_t stream) {
+    if (out_fmt == GR_OUT_MXFP8) return launch_norm<E, gr::mx::kOutMx8>(a, stream);
+    if (out_fmt == GR_OUT_MXFP4) return launch_norm<E, gr::mx::kOutMx4>(a, stream);
+    return launch_norm<E, gr::mx::kOut16>(a, stream);
+}
+
+// ---- gated activation ------------------------------------------------------------
+
+template <typename E>
+int run_gated(const gr::mx::GatedArgs& a, int out_fmt, hipStream_t stream) {
+    using namespace gr::mx;
+    const int64_t per = kGatedThreads * kGatedChunks, chunks = (a.N + 7) / 8;
+    const dim3 grid((uint32_t)((chunks + per - 1) / per), (uint32_t)(a.M < 65535 ? a.M : 65535));
+    if (out_fmt == GR_OUT_MXFP8) return launch_grid(gated_act_kernel<E, kOutMx8>, grid, kGatedThreads, stream, a);
+    if (out_fmt == GR_OUT_MXFP4) return launch_grid(gated_act_kernel<E, kOutMx4>, grid, kGatedThreads, stream, a);
+    return launch_grid(gated_act_kernel<E, kOut16>, grid, kGatedThreads, stream, a);
+}
+
+// ---- 16-bit activations, MX fp4 weights ------------------------------------------
+
+int validate_w4(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* Bt, int64_t ldbt,
+                const void* SB, int64_t ld_sb, const void* bias, int act, const void* C, int64_t ldc, int fmt) {
+    if (M < 0 || N < 0 || K < 0 || K % 32 != 0) return GR_ERR_INVALID_DIM;
+    if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return GR_ERR_TOO_LARGE;
+    if (lda < (K > 1 ? K : 1) || ldbt < (K > 1 ? K / 2 : 1) || ld_sb < (K > 1 ? K / 32 : 1) || ldc < (N > 1 ? N : 1))
+        return GR_ERR_INVALID_LD;
+    if (!known_act(act) || !known_fmt(fmt)) return GR_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return GR_OK;
+    if (!C || (K > 0 && (!A || !Bt || !SB))) return GR_ERR_NULL_PTR;
+    const Region c = matrix16(C, M, N, ldc), a = matrix16(A, M, K, lda), b = matrix8(Bt, N, K / 2, ldbt),
+                 s = matrix8(SB, N, K / 32, ld_sb), v = matrix16(bias, 1, N, N);
+    if (c.bytes < 0 || a.bytes < 0 || b.bytes < 0 || s.bytes < 0) return GR_ERR_TOO_LARGE;
+    if (overlaps(c, a) || overlaps(c, b) || overlaps(c, s) || overlaps(c, v)) return GR_ERR_ALIAS;
+    return GR_OK;
+}
+
+template <typename E, int MT, int NT, int D>
+int launch_w4(gr::w4::LinearArgs a, hipStream_t stream) {
+    using namespace gr::w4;
+    a.n_tiles = (a.N + 16 * NT - 1) / (16 * NT);
+    a.items = a.n_tiles * ((a.M + 16 * MT - 1) / (16 * MT));
+    const int64_t steps = (a.K + 127) / 128;
+    a.kw = 1;
+    while (a.kw < kWaves && a.items * a.kw < 2048 && a.kw * 2 <= steps) a.kw *= 2;
+    const int64_t per = kWaves / a.kw, grid = (a.items + per - 1) / per;
+    if (grid > kMaxDim) return GR_ERR_TOO_LARGE;
+    if (a.K < 128) return launch(linear_w4_kernel<E, MT, NT, D, true>, grid, kThreads, stream, a);
+    return launch(linear_w4_kernel<E, MT, NT, D, false>, grid, kThreads, stream, a);
+}
+
+template <typename E>
+int run_w4(const gr::w4::LinearArgs& a, hipStream_t stream) {
+    const bool wide = a.N >= 16384;
+    if (a.M <= 16) return wide ? launch_w4<E, 1, 2, 3>(a, stream) : launch_w4<E, 1, 1, 4>(a, stream);
+    if (a.M <= 32) return wide ? launch_w4<E, 2, 2, 2>(a, stream) : launch_w4<E, 2, 1, 3>(a, stream);
+    return wide ? launch_w4<E, 4, 2, 2>(a, stream) : launch_w4<E, 4, 1, 2>(a, stream);
+}
+
+// ---- mixture of experts ------------------------------------------------------------
+
+constexpr int64_t kMoeMaxDim = int64_t(1) << 20;  // H and I: the kernels count steps of 128 in 32 bits
+
+int64_t moe_workspace(int64_t T, int64_t I, int64_t topk) {
+    const int64_t bytes = T * topk * I * 4;  // two bfloat16 planes
+    return (bytes + kWorkspaceAlign - 1) / kWorkspaceAlign * kWorkspaceAlign;
+}
+
+int validate_moe_dims(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk) {
+    if (T < 0 || H < 0 || I < 0 || E < 1 || H % 32 != 0 || I % 32 != 0) return GR_ERR_INVALID_DIM;
+    if (topk < 1) return GR_ERR_INVALID_ARG;
+    if (T > 64 * 65535 || H > kMoeMaxDim || I > kMoeMaxDim || E > gr::w4::kMaxExperts || topk > gr::w4::kMaxTopK)
+        return GR_ERR_TOO_LARGE;
+    return GR_OK;
+}
+
+template <typename E>
+int run_moe(const gr::w4::MoeArgs& args, hipStream_t stream) {
+    using namespace gr::w4;
+    MoeArgs a = args;
+    const uint32_t chunks = (uint32_t)((a.T + kChunk - 1) / kChunk);
+    const int64_t n_tok = a.T < kChunk ? a.T : kChunk;
+    if (a.I > 0) {
+        // at most this many experts and tiles of 16 pairs are reached
+        const int64_t pairs = n_tok * a.topk, most = pairs < a.E ? pairs : a.E;
+        const int64_t items = (most + (n_tok > 16 ? pairs / 16 : 0)) * ((a.I + 15) / 16);
+        const int64_t steps = (a.H + 127) / 128;
+        a.kw = 1;
+        while (a.kw < kWaves && items * a.kw < 4096 && a.kw * 2 <= steps) a.kw *= 2;
+        int64_t grid = (items + kWaves / a.kw - 1) / (kWaves / a.kw);
+        if (grid > 512) grid = 512;
+        const dim3 g((uint32_t)grid, chunks);
+        const int st = a.H < 128 ? launch_grid(moe_gate_up_kernel<E, 3, true>, g, kThreads, stream, a)
+                                 : launch_grid(moe_gate_up_kernel<E, 3, false>, g, kThreads, stream, a);
+        if (st != GR_OK) return st;
+    }
+    const dim3 g((uint32_t)((a.H + 15) / 16), chunks);
+    return a.I < 128 ? launch_grid(moe_down_kernel<E, 3, true>, g, kThreads, stream, a)
+                     : launch_grid(moe_down_kernel<E, 3, false>, g, kThreads, stream, a);
+}
+
+template <typename E>
+int run_route(const gr::w4::RouteArgs& a, hipStream_t stream) {
+    using namespace gr::w4;
+    const int64_t grid = (a.T + 15) / 16;
+    if (a.E <= 64) return launch(moe_route_kernel<E, 1>, grid, kRouteThreads, stream, a);
+    if (a.E <= 256) return launch(moe_route_kernel<E, 4>, grid, kRouteThreads, stream, a);
+    return launch(moe_route_kernel<E, 16>, grid, kRouteThreads, stream, a);
+}
+
+}  // namespace
+
+extern "C" {
+
+int rms_norm_mx(int64_t M, int64_t N, const uint16_t* X, int64_t ldx, const uint16_t* R, int64_t ldr,
+                const uint16_t* weight, float eps, uint16_t* S, int64_t lds, void* Y, int64_t ldy, uint8_t* SY,
+                int64_t ld_sy, int fmt, int out_fmt, void* stream) {
+    if (M < 0 || N < 0) return GR_ERR_INVALID_DIM;
+    if (M > kMaxDim || N > kMaxDim) return GR_ERR_TOO_LARGE;
+    const int64_t nmin = N > 1 ? N : 1;
+    if (ldx < nmin || (R && ldr < nmin) || (S && lds < nmin)) return GR_ERR_INVALID_LD;
+    if (!known_fmt(fmt) || !(eps >= 0.0f) || !std::isfinite(eps) || (S && !R)) return GR_ERR_INVALID_ARG;
+    Region y, e;
+    int st = validate_out(M, N, Y, ldy, SY, ld_sy, out_fmt, &y, &e);
+    if (st != GR_OK) return st;
+    if (M == 0 || N == 0) return GR_OK;
+    if (!X) return GR_ERR_NULL_PTR;
+    const Region x = matrix16(X, M, N, ldx), r = matrix16(R, M, N, ldr), s = matrix16(S, M, N, lds),
+                 w = matrix16(weight, 1, N, N);
+    if (x.bytes < 0 || r.bytes < 0 || s.bytes < 0) return GR_ERR_TOO_LARGE;
+    // S may be X or R itself and a 16-bit Y may be X itself: each thread has
+    // read what it overwrites
+    const bool s_is_x = S == X && lds == ldx, s_is_r = S == R && lds == ldr;
+    const bool y_is_x = Y == static_cast<const void*>(X) && ldy == ldx && out_fmt == GR_OUT_16;
+    if ((overlaps(s, x) && !s_is_x) || (overlaps(s, r) && !s_is_r) || overlaps(s, w) || overlaps(s, y) ||
+        overlaps(s, e) || (overlaps(y, x) && !y_is_x) || overlaps(y, r) || overlaps(y, w) || overlaps(e, x) ||
+        overlaps(e, r) || overlaps(e, w))
+        return GR_ERR_ALIAS;
+    // X and R may be the same matrix or overlap, as they are only read; but a
+    // write into one of them must not reach the other
+    if ((s_is_x && overlaps(s, r) && !s_is_r) || (s_is_r && overlaps(s, x) && !s_is_x)) return GR_ERR_ALIAS;
+    st = check_device();
+    if (st != GR_OK) return st;
+    const gr::mx::NormArgs a{X,   R,   weight, S,  static_cast<uint8_t*>(Y),           SY,    M,  N,
+                             ldx, ldr, lds,    out_fmt == GR_OUT_16 ? ldy * 2 : ldy, ld_sy, eps};
+    hipStream_t h = static_cast<hipStream_t>(stream);
+    return fmt == GR_FMT_BF16 ? run_norm<gr::ElemBF16>(a, out_fmt, h) : run_norm<gr::ElemF16>(a, out_fmt, h);
+}
+
+int gated_act_mx(int64_t M, int64_t N, const uint16_t* G, int64_t ldg, const uint16_t* U, int64_t ldu, int act,
+                 void* Y, int64_t ldy, uint8_t* SY, int64_t ld_sy, int fmt, int out_fmt, void* stream) {
+    if (M < 0 || N < 0) return GR_ERR_INVALID_DIM;
+    if (M > kMaxDim || N > kMaxDim) return GR_ERR_TOO_LARGE;
+    const int64_t nmin = N > 1 ? N : 1;
+    if (ldg < nmin || (U && ldu < nmin)) return GR_ERR_INVALID_LD;
+    if (!known_fmt(fmt) || !known_act(act)) return GR_ERR_INVALID_ARG;
+    Region y, e;
+    int st = validate_out(M, N, Y, ldy, SY, ld_sy, out_fmt, &y, &e);
+    if (st != GR_OK) return st;
+    if (M == 0 || N == 0) return GR_OK;
+    if (!G) return GR_ERR_NULL_PTR;
+    const Region g = matrix16(G, M, N, ldg), u = matrix16(U, M, N, ldu);
+    if (g.bytes < 0 || u.bytes < 0) return GR_ERR_TOO_LARGE;
+    // a 16-bit Y may be G or U itself
+    const bool y_is_g = Y == static_cast<const void*>(G) && ldy == ldg && out_fmt == GR_OUT_16;
+    const bool y_is_u = Y == static_cast<const void*>(U) && ldy == ldu && out_fmt == GR_OUT_16;
+    if ((overlaps(y, g) && !y_is_g) || (overlaps(y, u) && !y_is_u) || overlaps(e, g) || overlaps(e, u))
+        return GR_ERR_ALIAS;
+    st = check_device();
+    if (st != GR_OK) return st;
+    gr::mx::GatedArgs a{G, U, static_cast<uint8_t*>(Y), SY, M, N, ldg, ldu, ldy, ld_sy, act};
+    // rows without padding are one long row (blocks of 32 stay within rows)
+    const int64_t cols = out_cols(N, out_fmt);
+    if (N % 32 == 0 && ldg == N && (!U || ldu == N) && ldy == cols && (out_fmt == GR_OUT_16 || ld_sy == N / 32)) {
+        a.N = M * N;
+        a.M = 1;
+    }
+    if (out_fmt == GR_OUT_16) a.ldy_bytes = ldy * 2;
+    hipStream_t h = static_cast<hipStream_t>(stream);
+    return fmt == GR_FMT_BF16 ? run_gated<gr::ElemBF16>(a, out_fmt, h) : run_gated<gr::ElemF16>(a, out_fmt, h);
+}
+
+int gemm_w4_bt(int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, const uint8_t* Bt, int64_t ldbt,
+               const uint8_t* scale_b, int64_t ld_sb, const uint16_t* bias, int act, uint16_t* C, int64_t ldc,
+               int fmt, void* stream) {
+    int st = validate_w4(M, N, K, A, lda, Bt, ldbt, scale_b, ld_sb, bias, act, C, ldc, fmt);
+    if (st != GR_OK) return st;
+    if (M == 0 || N == 0) return GR_OK;
+    st = check_device();
+    if (st != GR_OK) return st;
+    const gr::w4::LinearArgs a{A, Bt, scale_b, bias, C, M, N, K, lda, ldbt, ld_sb, ldc, 0, 0, act, 1};
+    hipStream_t h = static_cast<hipStream_t>(stream);
+    return fmt == GR_FMT_BF16 ? run_w4<gr::ElemBF16>(a, h) : run_w4<gr::ElemF16>(a, h);
+}
+
+int moe_route(int64_t T, int64_t H, int64_t E, int64_t topk, const uint16_t* X, int64_t ldx, const uint16_t* Wr,
+              int64_t ldwr, const float* bias, int renorm, int32_t* ids, float* weights, int fmt, void* stream) {
+    if (T < 0 || H < 0 || E < 1) return GR_ERR_INVALID_DIM;
+    if (topk < 1 || topk > E || !known_fmt(fmt) || (renorm != 0 && renorm != 1)) return GR_ERR_INVALID_ARG;
+    if (T > kMaxDim || H > kMaxDim || E > gr::w4::kMaxExperts || topk > gr::w4::kMaxTopK) return GR_ERR_TOO_LARGE;
+    const int64_t hmin = H > 1 ? H : 1;
+    if (ldx < hmin || ldwr < hmin) return GR_ERR_INVALID_LD;
+    if (T == 0) return GR_OK;
+    if (!ids || !weights || (H > 0 && (!X || !Wr))) return GR_ERR_NULL_PTR;
+    const Region x = matrix16(X, T, H, ldx), w = matrix16(Wr, E, H, ldwr),
+                 b{reinterpret_cast<uintptr_t>(bias), bias ? E * 4 : 0}, i{reinterpret_cast<uintptr_t>(ids), T * topk * 4},
+                 v{reinterpret_cast<uintptr_t>(weights), T * topk * 4};
+    if (x.bytes < 0 || w.bytes < 0) return GR_ERR_TOO_LARGE;
+    if (overlaps(i, v) || overlaps(i, x) || overlaps(i, w) || overlaps(i, b) || overlaps(v, x) || overlaps(v, w) ||
+        overlaps(v, b))
+        return GR_ERR_ALIAS;
+    int st = check_device();
+    if (st != GR_OK) return st;
+    const gr::w4::RouteArgs a{X, Wr, bias, ids, weights, T, H, ldx, ldwr, (int)E, (int)topk, renorm};
+    hipStream_t h = static_cast<hipStream_t>(stream);
+    return fmt == GR_FMT_BF16 ? run_route<gr::ElemBF16>(a, h) : run_route<gr::ElemF16>(a, h);
+}
+
+int moe_w4_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, int64_t* bytes) {
+    if (!bytes) return GR_ERR_INVALID_ARG;
+    const int st = validate_moe_dims(T, H, I, E, topk);
+    if (st != GR_OK) return st;
+    *bytes = moe_workspace(T, I, topk);
+    return GR_OK;
+}
+
+int moe_w4(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, const uint16_t* X, int64_t ldx,
+           const int32_t* ids, const float* weights, const uint8_t* W13, const uint8_t* S13, const uint16_t* b13,
+           const uint8_t* W2, const uint8_t* S2, const uint16_t* b2, int act, uint16_t* C, int64_t ldc, int fmt,
+           void* workspace, int64_t workspace_bytes, void* stream) {
+    int st = validate_moe_dims(T, H, I, E, topk);
+    if (st != GR_OK) return st;
+    const int64_t hmin = H > 1 ? H : 1;
+    if (ldx < hmin || ldc < hmin) return GR_ERR_INVALID_LD;
+    if (!known_act(act) || !known_fmt(fmt) || workspace_bytes < 0) return GR_ERR_INVALID_ARG;
+    if (T == 0 || H == 0) return GR_OK;
+    if (!C || !ids || !weights || (I > 0 && (!X || !W13 || !S13 || !W2 || !S2))) return GR_ERR_NULL_PTR;
+    const int64_t need = moe_workspace(T, I, topk);
+    if (need > 0 && !workspace) return GR_ERR_NULL_PTR;
+    if (reinterpret_cast<uintptr_t>(workspace) % kWorkspaceAlign != 0) return GR_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return GR_ERR_SCRATCH;
+    const Region x = matrix16(X, T, H, ldx), c = matrix16(C, T, H, ldc),
+                 ws{reinterpret_cast<uintptr_t>(workspace), need};
+    if (x.bytes < 0 || c.bytes < 0) return GR_ERR_TOO_LARGE;
+    const Region in[] = {x,
+                         {reinterpret_cast<uintptr_t>(ids), T * topk * 4},
+                         {reinterpret_cast<uintptr_t>(weights), T * topk * 4},
+                         {reinterpret_cast<uintptr_t>(W13), E * I * H},
+                         {reinterpret_cast<uintptr_t>(S13), E * I * H / 16},
+                         {reinterpret_cast<uintptr_t>(W2), E * I * H / 2},
+                         {reinterpret_cast<uintptr_t>(S2), E * I * H / 32},
+                         {reinterpret_cast<uintptr_t>(b13), b13 ? E * I * 4 : 0},
+                         {reinterpret_cast<uintptr_t>(b2), b2 ? E * H * 2 : 0}};
+    if (overlaps(c, ws)) return GR_ERR_ALIAS;
+    for (const Region& r : in)
+        if (overlaps(c, r) || overlaps(ws, r)) return GR_ERR_ALIAS;
+    st = check_device();
+    if (st != GR_OK) return st;
+    const gr::w4::MoeArgs a{X,  ids, weights, W13, S13, W2, S2,  b13,    b2,        static_cast<uint16_t*>(workspace),
+                            C,  T,   H,       I,   ldx, ldc, (int)E, (int)topk, act, 1};
+    hipStream_t h = static_cast<hipStream_t>(stream);
+    return fmt == GR_FMT_BF16 ? run_moe<gr::ElemBF16>(a, h) : run_moe<gr::ElemF16>(a, h);
+}
+
+}  // extern "C"

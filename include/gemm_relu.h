@@ -82,12 +82,17 @@ extern "C" {
 #define GR_ERR_LAUNCH               -8 /* the kernel launch was rejected by the runtime    */
 #define GR_ERR_INVALID_PATH         -9 /* forced path unknown or not applicable            */
 #define GR_ERR_INVALID_ARG         -10 /* a NULL output struct or other bad argument        */
-#define GR_ERR_SCRATCH             -11 /* gemm_relu_f16_noalloc: the problem needs more      */
+#define GR_ERR_SCRATCH             -11 /* gemm_relu_f16_noalloc, moe_w4: the problem needs more      */
                                        /* scratch than the library's static buffer holds   */
 
 /* ---- element formats (fmt / out_fmt arguments) ----------------------------- */
 #define GR_FMT_F16         0 /* IEEE binary16                                        */
 #define GR_FMT_BF16        1 /* bfloat16                                             */
+
+/* Output formats of rms_norm_mx and gated_act_mx. */
+#define GR_OUT_16          0 /* the inputs' 16-bit format                            */
+#define GR_OUT_MXFP8       1 /* E4M3 bytes and one E8M0 scale byte per 32 columns    */
+#define GR_OUT_MXFP4       2 /* E2M1 pairs (low nibble first) and E8M0 scale bytes   */
 
 /* ---- execution paths chosen by the planner --------------------------------- */
 #define GR_PATH_NONE       0 /* empty output: nothing to launch                            */
@@ -823,6 +828,126 @@ int gemm_relu_f16_noalloc(int64_t M, int64_t N, int64_t K,
 #define GR_READ_CONTIGUOUS 0
 #define GR_READ_ROW_PIECES 1
 int gemm_relu_stream_read(const void* src, int64_t bytes, int pattern, uint64_t* sink, void* stream);
+
+/*
+ * ---- the feed-forward block around the MX products --------------------------------
+ * Operators that make the operands of the products above and use MX fp4
+ * weights where there are few rows.  The conventions of gemm_relu_f16 hold:
+ * device pointers, pitches in elements (bytes for MX data), any size including
+ * zero, nothing allocated, one stream, a status code; rows may start at any
+ * address their element type allows.  Outputs outside their M x N window
+ * are never written.
+ *
+ * MX rounding of a row, for each 32 consecutive columns (N % 32 == 0, else
+ * GR_ERR_INVALID_DIM): with a the largest magnitude of the 32 fp32 values,
+ *   e = floor(log2 a) - emax, held to [-127, 127], -127 for a = 0
+ *       (emax: 8 for E4M3, 2 for E2M1),
+ *   scale byte e + 127, element = value * 2^-e rounded to the nearest
+ *   element, ties to even, held to +-448 (E4M3) or +-6 (E2M1).
+ * A block that holds an infinity or a NaN gets the scale 255 (NaN) and zero
+ * elements, so that products with it are NaN.  These are the operands of
+ * gemm_mxfp8_bt and gemm_mxfp4_bt.
+ */
+
+/*
+ * rms_norm_mx -- root-mean-square norm of the rows of X + R:
+ *   s = round16(x + r)            (R NULL: s = x)
+ *   y = s * weight / sqrt(mean over the row of s^2 + eps)
+ * in fp32 from the 16-bit values of s, rounded once to the output format.
+ * The squares are summed in fp32, so a row whose sum of squares passes
+ * 3.4e38 gives zeros.
+ *   X, R, S    M x N in fmt (GR_FMT_*), pitches ldx, ldr, lds; S (the next
+ *              residual) may be NULL; R NULL needs S NULL (GR_ERR_INVALID_ARG)
+ *   weight     N values in fmt, NULL for ones
+ *   Y, ldy     the output in out_fmt (GR_OUT_*): pitch in 16-bit elements, or in
+ *              bytes for the MX formats (N bytes, N / 2 for GR_OUT_MXFP4)
+ *   SY, ld_sy  scale bytes, M x N / 32 (MX formats; ignored for GR_OUT_16)
+ * S may be X or R itself (same pitch), and a GR_OUT_16 Y may be X itself;
+ * any other overlap of what is written is GR_ERR_ALIAS.  eps negative or not
+ * finite: GR_ERR_INVALID_ARG.
+ */
+int rms_norm_mx(int64_t M, int64_t N,
+                const uint16_t* X, int64_t ldx,
+                const uint16_t* R, int64_t ldr,
+                const uint16_t* weight, float eps,
+                uint16_t* S, int64_t lds,
+                void* Y, int64_t ldy, uint8_t* SY, int64_t ld_sy,
+                int fmt, int out_fmt, void* stream);
+
+/*
+ * gated_act_mx -- y = act(g) * u (U NULL: y = act(g); with act GR_ACT_NONE
+ * the rounding of G itself to MX fp8 or fp4) in fp32, rounded once to the
+ * output format.  Arguments as for rms_norm_mx; G and U in fmt; a GR_OUT_16 Y
+ * may be G or U itself.
+ */
+int gated_act_mx(int64_t M, int64_t N,
+                 const uint16_t* G, int64_t ldg,
+                 const uint16_t* U, int64_t ldu, int act,
+                 void* Y, int64_t ldy, uint8_t* SY, int64_t ld_sy,
+                 int fmt, int out_fmt, void* stream);
+
+/*
+ * gemm_w4_bt -- C := act(A * Bt~^T + bias) with A (M x K), bias and C in fmt and
+ * Bt (N x K) in MX fp4 as for gemm_mxfp4_bt (E2M1 pairs, pitch ldbt in bytes;
+ * scale_b N x K / 32 E8M0 bytes, pitch ld_sb).  Made for few rows of A: the
+ * weights are read once per 64 rows.  Weights are widened exactly, products
+ * accumulate in fp32 per block of 32 k, and the block's scale multiplies the fp32
+ * sum: every scale 2^-127 .. 2^127 is exact, scale byte 255 gives NaN.  K % 32
+ * != 0 is GR_ERR_INVALID_DIM; K == 0 gives act(bias).
+ */
+int gemm_w4_bt(int64_t M, int64_t N, int64_t K,
+               const uint16_t* A, int64_t lda,
+               const uint8_t* Bt, int64_t ldbt,
+               const uint8_t* scale_b, int64_t ld_sb,
+               const uint16_t* bias, int act,
+               uint16_t* C, int64_t ldc, int fmt,
+               void* stream);
+
+/*
+ * moe_route -- the router of a mixture-of-experts layer: logits[t][e] = sum_k
+ * X[t][k] * Wr[e][k] + bias[e] in fp32, the topk largest of each token in
+ * descending order (equal logits: the lower index first; NaN counts as the
+ * largest), and their softmax: weights = exp(logit - max) over its sum, taken
+ * over the chosen experts (renorm 1) or over all E (renorm 0).
+ *   X, Wr         T x H and E x H in fmt, pitches ldx, ldwr; any H
+ *   bias          E floats or NULL
+ *   ids, weights  T x topk, contiguous
+ * E <= 1024, topk <= 32 (GR_ERR_TOO_LARGE), 1 <= topk <= E
+ * (GR_ERR_INVALID_ARG).
+ */
+int moe_route(int64_t T, int64_t H, int64_t E, int64_t topk,
+              const uint16_t* X, int64_t ldx,
+              const uint16_t* Wr, int64_t ldwr, const float* bias, int renorm,
+              int32_t* ids, float* weights, int fmt, void* stream);
+
+/*
+ * moe_w4 -- the experts of a mixture-of-experts layer with MX fp4 weights:
+ *   out[t] = sum_j weights[t][j] * (W2[e]~ h + b2[e]),  e = ids[t][j],
+ *   h = act(g) * u,  (g, u) = W13[e]~ x[t] + b13[e]
+ * Made for few tokens: the weights of an expert that a token of a chunk of 64
+ * chose are read once for the chunk, others not at all.  An id outside [0, E) is
+ * passed over (an expert held elsewhere); a token with no expert gives zeros.  The
+ * sums over k, over experts and h are held to 16 bits or more (fp32 sums, h in
+ * two bfloat16 parts); the result is rounded once.
+ *   X, C       T x H in fmt, pitches ldx, ldc
+ *   ids, weights  T x topk, contiguous
+ *   W13, S13   E x 2I x H / 2 and E x 2I x H / 32 bytes, contiguous; the rows of an
+ *              expert are its I gate rows, then its I up rows
+ *   W2, S2     E x H x I / 2 and E x H x I / 32 bytes, contiguous
+ *   b13, b2    E x 2I and E x H values in fmt, or NULL
+ * H and I are multiples of 32 (GR_ERR_INVALID_DIM); E <= 1024, topk <= 32, H and I
+ * <= 2^20 (GR_ERR_TOO_LARGE).  The workspace (rules as for gemm_relu_f16_ws)
+ * holds at least moe_w4_workspace_size bytes, else GR_ERR_SCRATCH.
+ */
+int moe_w4_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, int64_t* bytes);
+
+int moe_w4(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk,
+           const uint16_t* X, int64_t ldx,
+           const int32_t* ids, const float* weights,
+           const uint8_t* W13, const uint8_t* S13, const uint16_t* b13,
+           const uint8_t* W2, const uint8_t* S2, const uint16_t* b2,
+           int act, uint16_t* C, int64_t ldc, int fmt,
+           void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Static, NUL-terminated name of a status code ("GR_OK", "GR_ERR_ALIAS", ...),
  * so that a refused call can be reported with its cause (the fail-loudly
