@@ -12,7 +12,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 # one translation unit per family of entry points, compiled side by side
-UNITS = [os.path.join(HERE, "csrc", f) for f in ("gemm_relu.hip", "mx_ops.hip")]
+SRC = os.path.join(HERE, "csrc", "gemm_relu.hip")
+UNITS = [SRC, os.path.join(HERE, "csrc", "mx_ops.hip")]
 LIB = os.path.join(HERE, "libgemm_relu.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
