@@ -116,35 +116,90 @@ int validate_w4(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, con
     return GR_OK;
 }
 
-template <typename E, int MT, int NT, int D>
-int launch_w4(gr::w4::LinearArgs a, hipStream_t stream) {
-    using namespace gr::w4;
-    a.n_tiles = (a.N + 16 * NT - 1) / (16 * NT);
-    a.items = a.n_tiles * ((a.M + 16 * MT - 1) / (16 * MT));
-    const int64_t steps = (a.K + 127) / 128;
-    a.kw = 1;
-    while (a.kw < kWaves && a.items * a.kw < 2048 && a.kw * 2 <= steps) a.kw *= 2;
-    const int64_t per = kWaves / a.kw, grid = (a.items + per - 1) / per;
-    if (grid > kMaxDim) return GR_ERR_TOO_LARGE;
-    if (a.K < 128) return launch(linear_w4_kernel<E, MT, NT, D, true>, grid, kThreads, stream, a);
-    return launch(linear_w4_kernel<E, MT, NT, D, false>, grid, kThreads, stream, a);
+constexpr int64_t kMaxGrid = ((int64_t(1) << 32) - 1) / gr::w4::kThreads;  // the runtime counts threads in 32 bits
+constexpr int64_t kCus = 256;
+
+// How a K is divided: steps of 128 per wave (a power of two, at most `most`), the
+// waves that share a unit, and whether the waves pass over the units more
+// than once.
+struct Division {
+    int steps, kw;
+    bool passes;
+};
+
+Division divide(int64_t K, int most) {
+    const int64_t steps = (K + 127) / 128;
+    Division d{1, 1, false};
+    while (d.steps < most && d.steps * gr::w4::kWaves < steps) d.steps *= 2;
+    while (d.kw < gr::w4::kWaves && d.steps * d.kw < steps) d.kw *= 2;
+    d.passes = (int64_t)d.steps * d.kw < steps;
+    return d;
+}
+
+// Workgroups along the units: enough to fill the chip, and for several passes
+// no more units each than their sums have room for.
+int64_t grid_of(int64_t units, const Division& d, int MT) {
+    const int groups = gr::w4::kWaves / d.kw;
+    const int64_t most = kCus * (d.steps * MT > 4 ? 1 : 2);
+    int64_t grid = (units + groups - 1) / groups;
+    if (grid > most) grid = most;
+    const int64_t room = gr::w4::kSumTiles / MT;
+    if (d.passes && grid * room < units) grid = (units + room - 1) / room;
+    return grid;
+}
+
+template <typename E, int MT, int ST, bool PASSES>
+int launch_w4(const gr::w4::LinearArgs& a, dim3 grid, hipStream_t stream) {
+    return launch_grid(gr::w4::linear_w4_kernel<E, MT, ST, PASSES>, grid, gr::w4::kThreads, stream, a);
+}
+
+template <typename E, int MT>
+int run_w4_rows(gr::w4::LinearArgs a, hipStream_t stream) {
+    constexpr int most = 8 / MT;
+    const Division d = divide(a.K, most);
+    a.kw = d.kw;
+    const int64_t gx = grid_of((a.N + 15) / 16, d, MT), gy = (a.M + 16 * MT - 1) / (16 * MT);
+    // rows beyond the grid's y limit go in further launches
+    for (int64_t y = 0; y < gy; y += 65535) {
+        gr::w4::LinearArgs b = a;
+        b.x += y * 16 * MT * a.ldx;
+        b.c += y * 16 * MT * a.ldc;
+        b.M -= y * 16 * MT;
+        const dim3 grid((uint32_t)gx, (uint32_t)(gy - y < 65535 ? gy - y : 65535));
+        int st = GR_OK;
+        if (d.passes)
+            st = launch_w4<E, MT, most, true>(b, grid, stream);
+        else if (d.steps == most)
+            st = launch_w4<E, MT, most, false>(b, grid, stream);
+        else if (d.steps == 1)
+            st = launch_w4<E, MT, 1, false>(b, grid, stream);
+        else if (MT < 4 && d.steps == 2)
+            st = launch_w4<E, MT, MT < 4 ? 2 : 1, false>(b, grid, stream);
+        else
+            st = launch_w4<E, MT, MT < 2 ? 4 : 1, false>(b, grid, stream);
+        if (st != GR_OK) return st;
+    }
+    return GR_OK;
 }
 
 template <typename E>
 int run_w4(const gr::w4::LinearArgs& a, hipStream_t stream) {
-    const bool wide = a.N >= 16384;
-    if (a.M <= 16) return wide ? launch_w4<E, 1, 2, 3>(a, stream) : launch_w4<E, 1, 1, 4>(a, stream);
-    if (a.M <= 32) return wide ? launch_w4<E, 2, 2, 2>(a, stream) : launch_w4<E, 2, 1, 3>(a, stream);
-    return wide ? launch_w4<E, 4, 2, 2>(a, stream) : launch_w4<E, 4, 1, 2>(a, stream);
+    if (a.M <= 16) return run_w4_rows<E, 1>(a, stream);
+    if (a.M <= 32) return run_w4_rows<E, 2>(a, stream);
+    return run_w4_rows<E, 4>(a, stream);
 }
 
 // ---- mixture of experts ------------------------------------------------------------
 
 constexpr int64_t kMoeMaxDim = int64_t(1) << 20;  // H and I: the kernels count steps of 128 in 32 bits
 
-int64_t moe_workspace(int64_t T, int64_t I, int64_t topk) {
-    const int64_t bytes = T * topk * I * 4;  // two bfloat16 planes
-    return (bytes + kWorkspaceAlign - 1) / kWorkspaceAlign * kWorkspaceAlign;
+int64_t aligned(int64_t bytes) { return (bytes + kWorkspaceAlign - 1) / kWorkspaceAlign * kWorkspaceAlign; }
+
+// The workspace: h (two bfloat16 planes), y (fp32), the pairs' rows.
+int64_t moe_h_bytes(int64_t T, int64_t I, int64_t topk) { return aligned(T * topk * I * 4); }
+int64_t moe_y_bytes(int64_t T, int64_t H, int64_t topk) { return aligned(T * topk * H * 4); }
+int64_t moe_workspace(int64_t T, int64_t H, int64_t I, int64_t topk) {
+    return I > 0 ? moe_h_bytes(T, I, topk) + moe_y_bytes(T, H, topk) + aligned(T * topk * 4) : 0;
 }
 
 int validate_moe_dims(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk) {
@@ -156,28 +211,45 @@ int validate_moe_dims(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk) 
 }
 
 template <typename E>
-int run_moe(const gr::w4::MoeArgs& args, hipStream_t stream) {
+int run_moe(gr::w4::MoeArgs a, hipStream_t stream) {
     using namespace gr::w4;
-    MoeArgs a = args;
     const uint32_t chunks = (uint32_t)((a.T + kChunk - 1) / kChunk);
-    const int64_t n_tok = a.T < kChunk ? a.T : kChunk;
     if (a.I > 0) {
-        // at most this many experts and tiles of 16 pairs are reached
-        const int64_t pairs = n_tok * a.topk, most = pairs < a.E ? pairs : a.E;
-        const int64_t items = (most + (n_tok > 16 ? pairs / 16 : 0)) * ((a.I + 15) / 16);
-        const int64_t steps = (a.H + 127) / 128;
-        a.kw = 1;
-        while (a.kw < kWaves && items * a.kw < 4096 && a.kw * 2 <= steps) a.kw *= 2;
-        int64_t grid = (items + kWaves / a.kw - 1) / (kWaves / a.kw);
-        if (grid > 512) grid = 512;
-        const dim3 g((uint32_t)grid, chunks);
-        const int st = a.H < 128 ? launch_grid(moe_gate_up_kernel<E, 3, true>, g, kThreads, stream, a)
-                                 : launch_grid(moe_gate_up_kernel<E, 3, false>, g, kThreads, stream, a);
+        // at most this many tiles of 16 pairs of one expert are in a chunk
+        const int64_t n_tok = a.T < kChunk ? a.T : kChunk, pairs = n_tok * a.topk;
+        const int64_t tiles = (pairs < a.E ? pairs : a.E) + (n_tok > 16 ? pairs / 16 : 0);
+        const Division d13 = divide(a.H, 8), d2 = divide(a.I, 4);
+        a.kw13 = d13.kw;
+        a.kw2 = d2.kw;
+        // (a workgroup's room for sums counts both products of a pair)
+        const int64_t items = tiles * ((a.I + 15) / 16);
+        const dim3 g13((uint32_t)grid_of(items, d13, 2), chunks);
+        int st = GR_OK;
+        if (d13.passes)
+            st = launch_grid(moe_gate_up_kernel<E, 8, true>, g13, kThreads, stream, a);
+        else if (d13.steps == 8)
+            st = launch_grid(moe_gate_up_kernel<E, 8, false>, g13, kThreads, stream, a);
+        else if (d13.steps == 4)
+            st = launch_grid(moe_gate_up_kernel<E, 4, false>, g13, kThreads, stream, a);
+        else if (d13.steps == 2)
+            st = launch_grid(moe_gate_up_kernel<E, 2, false>, g13, kThreads, stream, a);
+        else
+            st = launch_grid(moe_gate_up_kernel<E, 1, false>, g13, kThreads, stream, a);
+        if (st != GR_OK) return st;
+        const dim3 g2((uint32_t)grid_of(tiles * (a.H / 16), d2, 1), chunks);
+        if (d2.passes)
+            st = launch_grid(moe_down_kernel<4, true>, g2, kThreads, stream, a);
+        else if (d2.steps == 4)
+            st = launch_grid(moe_down_kernel<4, false>, g2, kThreads, stream, a);
+        else if (d2.steps == 2)
+            st = launch_grid(moe_down_kernel<2, false>, g2, kThreads, stream, a);
+        else
+            st = launch_grid(moe_down_kernel<1, false>, g2, kThreads, stream, a);
         if (st != GR_OK) return st;
     }
-    const dim3 g((uint32_t)((a.H + 15) / 16), chunks);
-    return a.I < 128 ? launch_grid(moe_down_kernel<E, 3, true>, g, kThreads, stream, a)
-                     : launch_grid(moe_down_kernel<E, 3, false>, g, kThreads, stream, a);
+    const int64_t per = kCombineThreads * 4;
+    const dim3 g((uint32_t)((a.H + per - 1) / per), (uint32_t)(a.T < 65535 ? a.T : 65535));
+    return launch_grid(moe_combine_kernel<E>, g, kCombineThreads, stream, a);
 }
 
 template <typename E>
@@ -269,7 +341,7 @@ int gemm_w4_bt(int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, 
     if (M == 0 || N == 0) return GR_OK;
     st = check_device();
     if (st != GR_OK) return st;
-    const gr::w4::LinearArgs a{A, Bt, scale_b, bias, C, M, N, K, lda, ldbt, ld_sb, ldc, 0, 0, act, 1};
+    const gr::w4::LinearArgs a{A, Bt, scale_b, bias, C, M, N, K, lda, ldbt, ld_sb, ldc, act, 1};
     hipStream_t h = static_cast<hipStream_t>(stream);
     return fmt == GR_FMT_BF16 ? run_w4<gr::ElemBF16>(a, h) : run_w4<gr::ElemF16>(a, h);
 }
@@ -301,7 +373,7 @@ int moe_w4_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t to
     if (!bytes) return GR_ERR_INVALID_ARG;
     const int st = validate_moe_dims(T, H, I, E, topk);
     if (st != GR_OK) return st;
-    *bytes = moe_workspace(T, I, topk);
+    *bytes = moe_workspace(T, H, I, topk);
     return GR_OK;
 }
 
@@ -316,7 +388,7 @@ int moe_w4(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, const uint1
     if (!known_act(act) || !known_fmt(fmt) || workspace_bytes < 0) return GR_ERR_INVALID_ARG;
     if (T == 0 || H == 0) return GR_OK;
     if (!C || !ids || !weights || (I > 0 && (!X || !W13 || !S13 || !W2 || !S2))) return GR_ERR_NULL_PTR;
-    const int64_t need = moe_workspace(T, I, topk);
+    const int64_t need = moe_workspace(T, H, I, topk);
     if (need > 0 && !workspace) return GR_ERR_NULL_PTR;
     if (reinterpret_cast<uintptr_t>(workspace) % kWorkspaceAlign != 0) return GR_ERR_INVALID_ARG;
     if (workspace_bytes < need) return GR_ERR_SCRATCH;
@@ -337,8 +409,30 @@ int moe_w4(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, const uint1
         if (overlaps(c, r) || overlaps(ws, r)) return GR_ERR_ALIAS;
     st = check_device();
     if (st != GR_OK) return st;
-    const gr::w4::MoeArgs a{X,  ids, weights, W13, S13, W2, S2,  b13,    b2,        static_cast<uint16_t*>(workspace),
-                            C,  T,   H,       I,   ldx, ldc, (int)E, (int)topk, act, 1};
+    uint8_t* const at = static_cast<uint8_t*>(workspace);
+    const gr::w4::MoeArgs a{X,
+                            ids,
+                            weights,
+                            W13,
+                            S13,
+                            W2,
+                            S2,
+                            b13,
+                            b2,
+                            reinterpret_cast<uint16_t*>(at),
+                            reinterpret_cast<float*>(at + moe_h_bytes(T, I, topk)),
+                            reinterpret_cast<int32_t*>(at + moe_h_bytes(T, I, topk) + moe_y_bytes(T, H, topk)),
+                            C,
+                            T,
+                            H,
+                            I,
+                            ldx,
+                            ldc,
+                            (int)E,
+                            (int)topk,
+                            act,
+                            1,
+                            1};
     hipStream_t h = static_cast<hipStream_t>(stream);
     return fmt == GR_FMT_BF16 ? run_moe<gr::ElemBF16>(a, h) : run_moe<gr::ElemF16>(a, h);
 }

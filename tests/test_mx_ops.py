@@ -33,7 +33,7 @@ def route(T=4, H=64, E=8, k=2, x=X, ldx=64, w=W, ldw=64, bias=None, renorm=1, id
 def moe(T=4, H=64, I_=96, E=8, k=2, x=X, ldx=64, ids=I, weights=R, w13=W, s13=S, b13=None, w2=B, s2=SY, b2=None,
         act=gr.GR_ACT_SILU, c=Y, ldc=64, fmt=BF, ws=0x900000000000, size=None):
     if size is None:
-        size = 4 * max(T, 0) * max(I_, 0) * max(k, 0) + 256
+        size = 4 * max(T, 0) * (max(I_, 0) + max(H, 0) + 1) * max(k, 0) + 768
     return gr.moe_w4(T, H, I_, E, k, x, ldx, ids, weights, w13, s13, b13, w2, s2, b2, act, c, ldc, fmt, ws, size)
 
 
