@@ -59,10 +59,16 @@ int check_device() {
 }
 
 template <typename... Args>
-int launch_grid(void (*kernel)(Args...), dim3 grid, int threads, hipStream_t stream, Args... args) {
+int launch_lds(void (*kernel)(Args...), dim3 grid, int threads, int dynamic_lds, hipStream_t stream, Args... args) {
     void* argv[] = {static_cast<void*>(&args)...};
-    hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), argv, 0, stream);
+    hipError_t e =
+        hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), argv, dynamic_lds, stream);
     return e == hipSuccess ? GR_OK : GR_ERR_LAUNCH;
+}
+
+template <typename... Args>
+int launch_grid(void (*kernel)(Args...), dim3 grid, int threads, hipStream_t stream, Args... args) {
+    return launch_lds(kernel, grid, threads, 0, stream, args...);
 }
 
 template <typename... Args>

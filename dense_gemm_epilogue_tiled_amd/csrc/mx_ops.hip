@@ -116,49 +116,59 @@ int validate_w4(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, con
     return GR_OK;
 }
 
-constexpr int64_t kMaxGrid = ((int64_t(1) << 32) - 1) / gr::w4::kThreads;  // the runtime counts threads in 32 bits
 constexpr int64_t kCus = 256;
 
 // How a K is divided: steps of 128 per wave (a power of two, at most `most`), the
-// waves that share a unit, and whether the waves pass over the units more
-// than once.
+// waves of a workgroup, those of them that share a unit, and whether they pass
+// over the units more than once.  Workgroups of 8 waves, two per CU; of 16 where
+// 8 waves do not hold the K at once.
 struct Division {
-    int steps, kw;
+    int steps, waves, kw;
     bool passes;
 };
 
-Division divide(int64_t K, int most) {
+Division divide(int64_t K, int most, bool wide) {
     const int64_t steps = (K + 127) / 128;
-    Division d{1, 1, false};
-    while (d.steps < most && d.steps * gr::w4::kWaves < steps) d.steps *= 2;
-    while (d.kw < gr::w4::kWaves && d.steps * d.kw < steps) d.kw *= 2;
+    Division d{1, wide && most * 8 < steps ? 16 : 8, 1, false};
+    while (d.steps < most && d.steps * d.waves < steps) d.steps *= 2;
+    while (d.kw < d.waves && d.steps * d.kw < steps) d.kw *= 2;
     d.passes = (int64_t)d.steps * d.kw < steps;
     return d;
 }
 
-// Workgroups along the units: enough to fill the chip, and for several passes
-// no more units each than their sums have room for.
-int64_t grid_of(int64_t units, const Division& d, int MT) {
-    const int groups = gr::w4::kWaves / d.kw;
-    const int64_t most = kCus * (d.steps * MT > 4 ? 1 : 2);
+// Workgroups along the units (`per` of them go together): enough to fill the chip, and
+// for several passes no more units each than their sums have room for.
+int64_t grid_of(int64_t units, const Division& d, int64_t wgs_per_cu, int64_t room) {
+    const int groups = d.waves / d.kw;
     int64_t grid = (units + groups - 1) / groups;
-    if (grid > most) grid = most;
-    const int64_t room = gr::w4::kSumTiles / MT;
+    if (grid > kCus * wgs_per_cu) grid = kCus * wgs_per_cu;
     if (d.passes && grid * room < units) grid = (units + room - 1) / room;
     return grid;
 }
 
-template <typename E, int MT, int ST, bool PASSES>
+template <typename E, int NW, int MT, int ST, bool PASSES>
 int launch_w4(const gr::w4::LinearArgs& a, dim3 grid, hipStream_t stream) {
-    return launch_grid(gr::w4::linear_w4_kernel<E, MT, ST, PASSES>, grid, gr::w4::kThreads, stream, a);
+    return launch_grid(gr::w4::linear_w4_kernel<E, NW, MT, ST, PASSES>, grid, 64 * NW, stream, a);
+}
+
+template <typename E, int MT>
+int launch_w4_rows(const gr::w4::LinearArgs& a, const Division& d, dim3 grid, hipStream_t stream) {
+    constexpr int most = MT == 1 ? 4 : 8 / MT;
+    if (d.passes) return launch_w4<E, MT == 1 ? 16 : 8, MT, most, true>(a, grid, stream);
+    if constexpr (MT == 1)
+        if (d.waves == 16) return launch_w4<E, 16, 1, 4, false>(a, grid, stream);
+    if (d.steps == most) return launch_w4<E, 8, MT, most, false>(a, grid, stream);
+    if constexpr (MT < 4)
+        if (d.steps == 2) return launch_w4<E, 8, MT, 2, false>(a, grid, stream);
+    return launch_w4<E, 8, MT, 1, false>(a, grid, stream);
 }
 
 template <typename E, int MT>
 int run_w4_rows(gr::w4::LinearArgs a, hipStream_t stream) {
-    constexpr int most = 8 / MT;
-    const Division d = divide(a.K, most);
+    const Division d = divide(a.K, MT == 1 ? 4 : 8 / MT, MT == 1);
     a.kw = d.kw;
-    const int64_t gx = grid_of((a.N + 15) / 16, d, MT), gy = (a.M + 16 * MT - 1) / (16 * MT);
+    const int64_t gx = grid_of((a.N + 15) / 16, d, d.waves * d.steps * MT > 32 ? 1 : 2, gr::w4::kSumTiles / MT);
+    const int64_t gy = (a.M + 16 * MT - 1) / (16 * MT);
     // rows beyond the grid's y limit go in further launches
     for (int64_t y = 0; y < gy; y += 65535) {
         gr::w4::LinearArgs b = a;
@@ -166,17 +176,7 @@ int run_w4_rows(gr::w4::LinearArgs a, hipStream_t stream) {
         b.c += y * 16 * MT * a.ldc;
         b.M -= y * 16 * MT;
         const dim3 grid((uint32_t)gx, (uint32_t)(gy - y < 65535 ? gy - y : 65535));
-        int st = GR_OK;
-        if (d.passes)
-            st = launch_w4<E, MT, most, true>(b, grid, stream);
-        else if (d.steps == most)
-            st = launch_w4<E, MT, most, false>(b, grid, stream);
-        else if (d.steps == 1)
-            st = launch_w4<E, MT, 1, false>(b, grid, stream);
-        else if (MT < 4 && d.steps == 2)
-            st = launch_w4<E, MT, MT < 4 ? 2 : 1, false>(b, grid, stream);
-        else
-            st = launch_w4<E, MT, MT < 2 ? 4 : 1, false>(b, grid, stream);
+        const int st = launch_w4_rows<E, MT>(b, d, grid, stream);
         if (st != GR_OK) return st;
     }
     return GR_OK;
@@ -218,33 +218,23 @@ int run_moe(gr::w4::MoeArgs a, hipStream_t stream) {
         // at most this many tiles of 16 pairs of one expert are in a chunk
         const int64_t n_tok = a.T < kChunk ? a.T : kChunk, pairs = n_tok * a.topk;
         const int64_t tiles = (pairs < a.E ? pairs : a.E) + (n_tok > 16 ? pairs / 16 : 0);
-        const Division d13 = divide(a.H, 8), d2 = divide(a.I, 4);
+        const Division d13 = divide(a.H, 4, true), d2 = divide(a.I, 2, true);
         a.kw13 = d13.kw;
         a.kw2 = d2.kw;
-        // (a workgroup's room for sums counts both products of a pair)
-        const int64_t items = tiles * ((a.I + 15) / 16);
-        const dim3 g13((uint32_t)grid_of(items, d13, 2), chunks);
-        int st = GR_OK;
-        if (d13.passes)
-            st = launch_grid(moe_gate_up_kernel<E, 8, true>, g13, kThreads, stream, a);
-        else if (d13.steps == 8)
-            st = launch_grid(moe_gate_up_kernel<E, 8, false>, g13, kThreads, stream, a);
-        else if (d13.steps == 4)
-            st = launch_grid(moe_gate_up_kernel<E, 4, false>, g13, kThreads, stream, a);
-        else if (d13.steps == 2)
-            st = launch_grid(moe_gate_up_kernel<E, 2, false>, g13, kThreads, stream, a);
-        else
-            st = launch_grid(moe_gate_up_kernel<E, 1, false>, g13, kThreads, stream, a);
+        // an item of the first product is two units
+        const dim3 g13((uint32_t)grid_of(tiles * (a.I / 16), d13, 16 / d13.waves, kSumTiles / 2), chunks);
+        const dim3 g2((uint32_t)grid_of(tiles * (a.H / 16), d2, 16 / d2.waves, kSumTiles), chunks);
+        const int lds = routing_bytes(a.E, a.topk);
+        int st = d13.passes        ? launch_lds(moe_gate_up_kernel<E, 16, 4, true>, g13, 1024, lds, stream, a)
+                 : d13.waves == 16 ? launch_lds(moe_gate_up_kernel<E, 16, 4, false>, g13, 1024, lds, stream, a)
+                 : d13.steps == 4  ? launch_lds(moe_gate_up_kernel<E, 8, 4, false>, g13, 512, lds, stream, a)
+                 : d13.steps == 2  ? launch_lds(moe_gate_up_kernel<E, 8, 2, false>, g13, 512, lds, stream, a)
+                                   : launch_lds(moe_gate_up_kernel<E, 8, 1, false>, g13, 512, lds, stream, a);
         if (st != GR_OK) return st;
-        const dim3 g2((uint32_t)grid_of(tiles * (a.H / 16), d2, 1), chunks);
-        if (d2.passes)
-            st = launch_grid(moe_down_kernel<4, true>, g2, kThreads, stream, a);
-        else if (d2.steps == 4)
-            st = launch_grid(moe_down_kernel<4, false>, g2, kThreads, stream, a);
-        else if (d2.steps == 2)
-            st = launch_grid(moe_down_kernel<2, false>, g2, kThreads, stream, a);
-        else
-            st = launch_grid(moe_down_kernel<1, false>, g2, kThreads, stream, a);
+        st = d2.passes        ? launch_lds(moe_down_kernel<16, 2, true>, g2, 1024, lds, stream, a)
+             : d2.waves == 16 ? launch_lds(moe_down_kernel<16, 2, false>, g2, 1024, lds, stream, a)
+             : d2.steps == 2  ? launch_lds(moe_down_kernel<8, 2, false>, g2, 512, lds, stream, a)
+                              : launch_lds(moe_down_kernel<8, 1, false>, g2, 512, lds, stream, a);
         if (st != GR_OK) return st;
     }
     const int64_t per = kCombineThreads * 4;

@@ -29,34 +29,40 @@ struct LinearUnits {
     const LinearArgs& a;
     const uint8_t *w, *s;
     int64_t K, ldw, lds, m0;
-    __device__ __forceinline__ int key(int) const { return 0; }
-    __device__ __forceinline__ const uint16_t* x(int, int, int m) const {
+    struct Run {
+        int from, end;
+    };
+    __device__ __forceinline__ Run run(int u) const { return {u, 0x7FFFFFFF}; }
+    __device__ __forceinline__ const uint16_t* x(const Run&, int, int m) const {
         return m0 + m < a.M ? a.x + (m0 + m) * a.ldx : nullptr;
     }
-    __device__ __forceinline__ int64_t row(int u, int r) const {
-        const int64_t n = (int64_t)u * 16 + r;
-        return n < a.N ? n : a.N - 1;
+    __device__ __forceinline__ Tile tile(const Run& run, int i) const {
+        const int64_t n = (int64_t)(run.from + i) * 16, rows = a.N - n < 16 ? a.N - n : 16;
+        return {w + n * ldw, s + n * lds, (uint32_t)((rows - 1) * ldw + K / 2), (uint32_t)((rows - 1) * lds + K / 32)};
     }
-    __device__ __forceinline__ bool wanted(int u, int m, int n) const {
-        return m0 + m < a.M && (int64_t)u * 16 + n < a.N;
+    __device__ __forceinline__ bool wanted(const Run& run, int i, int m, int n) const {
+        return m0 + m < a.M && (int64_t)(run.from + i) * 16 + n < a.N;
     }
-    __device__ __forceinline__ void finish(int u, int m, int n, float v) const {
-        const int64_t col = (int64_t)u * 16 + n;
+    __device__ __forceinline__ void finish(const Run& run, int i, int m, int n, float v) const {
+        const int64_t col = (int64_t)(run.from + i) * 16 + n;
         if (a.bias != nullptr) v += E::widen(a.bias[col]);
         a.c[(m0 + m) * a.ldc + col] = E::round(mx::exact_activate(v, a.act));
     }
 };
 
-// Units per wave between two barriers.
-constexpr int batch_of(int MT) { return MT == 1 ? 4 : 2; }
+// Registers for two workgroups of 8 waves, or one of 16, per CU while X takes 64 of
+// them.
+constexpr int waves_per_simd(int MT, int PL, int ST) { return MT * PL * ST <= 4 ? 4 : 2; }
 
-template <typename E, int MT, int ST, bool PASSES>
-__global__ void __launch_bounds__(kThreads) linear_w4_kernel(LinearArgs a) {
-    __shared__ Lds<MT, batch_of(MT), PASSES> lds;
+template <typename E, int NW, int MT, int ST, bool PASSES>
+__global__ void __launch_bounds__(64 * NW, waves_per_simd(MT, 1, ST)) linear_w4_kernel(LinearArgs a) {
+    // 16 waves: one batch of 8 units, as many as a workgroup has where N is below 2^15
+    constexpr int TB = MT == 1 ? (NW == 16 && !PASSES ? 8 : 4) : 2, BUFS = NW == 16 ? 1 : 2;
+    __shared__ Lds<NW, MT, TB, BUFS, PASSES> lds;
     const int64_t units = (a.N + 15) / 16;
     const LinearUnits<E> p{a, a.w, a.s, a.K, a.ldw, a.lds, (int64_t)blockIdx.y * (16 * MT)};
-    stream_units<E, MT, 1, ST, batch_of(MT), PASSES>(p, lds, (int)(units * blockIdx.x / gridDim.x),
-                                                     (int)(units * (blockIdx.x + 1) / gridDim.x), a.kw);
+    stream_units<E, 1, ST>(p, lds, (int)(units * blockIdx.x / gridDim.x), (int)(units * (blockIdx.x + 1) / gridDim.x),
+                           a.kw);
 }
 
 // ---- mixture of experts -----------------------------------------------------------
@@ -76,19 +82,23 @@ __global__ void __launch_bounds__(kThreads) linear_w4_kernel(LinearArgs a) {
 constexpr int kChunk = 64;         // tokens per chunk
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
-// sum over the experts of ceil(pairs / 16) < experts + pairs / 16
-constexpr int kMaxTiles = kMaxExperts + kChunk * kMaxTopK / 16;
-
-// Which tokens chose which expert, for one chunk (LDS).
+// Which tokens chose which expert, for one chunk, in dynamic LDS: as much as E
+// experts and topk choices need.
 struct Routing {
-    unsigned long long tokens[kMaxExperts];
-    uint16_t expert[kMaxExperts + 1];  // the chosen experts, ascending
-    uint16_t row[kMaxExperts + 1];     // first pair of each; [count]: pairs in all
-    uint16_t row_of[kMaxExperts];      // the same by expert number
-    uint16_t tile[kMaxTiles];          // tiles of 16 pairs: slot in `expert` * 4 + tile of that expert
-    uint8_t token[kChunk * kMaxTopK];  // a pair's token
-    int count, tiles;
+    unsigned long long* tokens;  // of each expert
+    uint16_t* expert;            // the chosen experts, ascending
+    uint16_t* row;               // first pair of each; [chosen]: pairs in all
+    uint16_t* row_of;            // the same by expert number
+    uint16_t* tile;              // tiles of 16 pairs: slot in `expert` * 4 + tile of that expert
+    uint8_t* token;              // a pair's token
+    int tiles;
 };
+
+// sum over the experts of ceil(pairs / 16) < experts + pairs / 16
+__host__ __device__ constexpr int max_tiles(int E, int topk) { return E + kChunk * topk / 16; }
+__host__ __device__ constexpr int routing_bytes(int E, int topk) {
+    return 8 * E + 8 + 2 * (3 * E + 2 + max_tiles(E, topk)) + kChunk * topk;
+}
 
 // The token's earlier slot with the same expert, or -1.
 __device__ __forceinline__ int earlier(const int32_t* ids, int j, int32_t e) {
@@ -97,10 +107,19 @@ __device__ __forceinline__ int earlier(const int32_t* ids, int j, int32_t e) {
     return -1;
 }
 
-// Fill r from the chunk's ids (n tokens x topk); called by the whole
+// The routing of the chunk's ids (n tokens x topk); called by the whole
 // workgroup.  Ids outside [0, E) choose nothing, and a token that names an
 // expert twice is one pair.
-__device__ __forceinline__ void route(Routing& r, const int32_t* ids, int n, int topk, int E) {
+__device__ __forceinline__ Routing route(const int32_t* ids, int n, int topk, int E) {
+    extern __shared__ unsigned long long routing_lds[];
+    Routing r;
+    r.tokens = routing_lds;
+    int* const tiles_of_all = reinterpret_cast<int*>(r.tokens + E);
+    r.expert = reinterpret_cast<uint16_t*>(tiles_of_all + 2);
+    r.row = r.expert + E + 1;
+    r.row_of = r.row + E + 1;
+    r.tile = r.row_of + E;
+    r.token = reinterpret_cast<uint8_t*>(r.tile + max_tiles(E, topk));
     for (int e = threadIdx.x; e < E; e += blockDim.x) r.tokens[e] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < n * topk; i += blockDim.x) {
@@ -138,9 +157,8 @@ __device__ __forceinline__ void route(Routing& r, const int32_t* ids, int n, int
             tiles += all >> 16;
         }
         if (lane == 0) {
-            r.count = count;
-            r.tiles = tiles;
             r.row[count] = (uint16_t)rows;
+            *tiles_of_all = tiles;
         }
     }
     __syncthreads();
@@ -150,7 +168,9 @@ __device__ __forceinline__ void route(Routing& r, const int32_t* ids, int n, int
         // (tokens that name e twice write the same value)
         if (e < (uint32_t)E) r.token[r.row_of[e] + __popcll(r.tokens[e] & ((1ull << t) - 1))] = (uint8_t)t;
     }
+    r.tiles = __builtin_amdgcn_readfirstlane(*tiles_of_all);
     __syncthreads();
+    return r;
 }
 
 struct MoeArgs {
@@ -168,60 +188,70 @@ struct MoeArgs {
     int kw13, kw2;             // waves that share a unit's K in the two products
 };
 
-// Units of the first product: tile of 16 pairs, columns of h, gate and up.
+// Units with the same X: a tile of pairs of one expert.
+struct MoeRun {
+    int end, expert, row, pairs, col;  // row: the tile's first pair; pairs: from there to the expert's end
+};
+
+// item: 16 columns for a tile of pairs, `tiles` for each.
+__device__ __forceinline__ MoeRun moe_run(const Routing& r, int item, int tiles) {
+    const int tile = item / tiles;
+    const int at = __builtin_amdgcn_readfirstlane(r.tile[tile]);
+    const int row = __builtin_amdgcn_readfirstlane(r.row[at / 4]) + at % 4 * 16;
+    return {(tile + 1) * tiles, __builtin_amdgcn_readfirstlane(r.expert[at / 4]), row,
+            __builtin_amdgcn_readfirstlane(r.row[at / 4 + 1]) - row, (item - tile * tiles) * 16};
+}
+
+// Units of the first product: 16 columns of h for a tile of pairs, gate and up.
 template <typename E>
 struct GateUpUnits {
     static constexpr bool kPair = true;
     const MoeArgs& a;
     const Routing& r;
-    const uint8_t *w, *s;
     int64_t K, ldw, lds, t0;
     int tiles;  // of 16 columns of h
-    __device__ __forceinline__ int key(int u) const { return u / 2 / tiles; }
-    __device__ __forceinline__ const uint16_t* x(int u, int, int m) const {
-        const int at = r.tile[key(u)], row = r.row[at / 4] + at % 4 * 16 + m;
-        return row < r.row[at / 4 + 1] ? a.x + (t0 + r.token[row]) * a.ldx : nullptr;
+    __device__ __forceinline__ MoeRun run(int u) const {
+        MoeRun run = moe_run(r, u / 2, tiles);
+        run.end *= 2;
+        return run;
     }
-    __device__ __forceinline__ int64_t row(int u, int q) const {
-        const int e = r.expert[r.tile[key(u)] / 4];
-        const int64_t n = (int64_t)(u / 2 % tiles) * 16 + q;
-        return (2 * (int64_t)e + u % 2) * a.I + (n < a.I ? n : a.I - 1);
+    __device__ __forceinline__ const uint16_t* x(const MoeRun& run, int, int m) const {
+        return m < run.pairs ? a.x + (t0 + r.token[run.row + m]) * a.ldx : nullptr;
     }
-    __device__ __forceinline__ bool wanted(int u, int m, int n) const {
-        const int at = r.tile[key(u)];
-        return r.row[at / 4] + at % 4 * 16 + m < r.row[at / 4 + 1] && (int64_t)(u / 2 % tiles) * 16 + n < a.I;
+    __device__ __forceinline__ Tile tile(const MoeRun& run, int i) const {
+        const int64_t n = (2 * (int64_t)run.expert + i % 2) * a.I + run.col + i / 2 * 16;
+        return {a.w13 + n * ldw, a.s13 + n * lds, (uint32_t)(16 * ldw), (uint32_t)(16 * lds)};
     }
-    __device__ __forceinline__ void finish(int u, int m, int n, float g, float v) const {
-        const int at = r.tile[key(u)], e = r.expert[at / 4], row = r.row[at / 4] + at % 4 * 16 + m;
-        const int64_t col = (int64_t)(u / 2 % tiles) * 16 + n;
+    __device__ __forceinline__ bool wanted(const MoeRun& run, int, int m, int) const { return m < run.pairs; }
+    __device__ __forceinline__ void finish(const MoeRun& run, int i, int m, int n, float g, float v) const {
+        const int64_t col = run.col + i / 2 * 16 + n;
         if (a.b13 != nullptr) {
-            g += E::widen(a.b13[2 * (int64_t)e * a.I + col]);
-            v += E::widen(a.b13[(2 * (int64_t)e + 1) * a.I + col]);
+            g += E::widen(a.b13[2 * (int64_t)run.expert * a.I + col]);
+            v += E::widen(a.b13[(2 * (int64_t)run.expert + 1) * a.I + col]);
         }
-        const int64_t t = t0 + r.token[row];
+        const int64_t t = t0 + r.token[run.row + m];
         float weight = 0.0f;
         for (int j = 0; j < a.topk; ++j)
-            if (a.ids[t * a.topk + j] == e) weight += a.weights[t * a.topk + j];
+            if (a.ids[t * a.topk + j] == run.expert) weight += a.weights[t * a.topk + j];
         const float h = mx::exact_activate(g, a.act) * v * weight;
         const uint16_t high = to_bf16(h);
-        const int64_t to = (t0 * a.topk + row) * a.I + col;
+        const int64_t to = (t0 * a.topk + run.row + m) * a.I + col;
         a.h[to] = high;
         a.h[a.T * a.topk * a.I + to] = to_bf16(h - ElemBF16::widen(high));
     }
 };
 
-constexpr int kMoeBatch = 2;
+constexpr int kMoeBatch = 4;
 
-template <typename E, int ST, bool PASSES>
-__global__ void __launch_bounds__(kThreads) moe_gate_up_kernel(MoeArgs a) {
-    __shared__ Routing r;
-    __shared__ Lds<1, kMoeBatch, PASSES> lds;
+template <typename E, int NW, int ST, bool PASSES>
+__global__ void __launch_bounds__(64 * NW, waves_per_simd(1, 1, ST)) moe_gate_up_kernel(MoeArgs a) {
+    __shared__ Lds<NW, 1, kMoeBatch, NW == 16 ? 1 : 2, PASSES> lds;
     const int64_t t0 = (int64_t)blockIdx.y * kChunk;
     const int n_tok = (int)(a.T - t0 < kChunk ? a.T - t0 : kChunk);
     const int32_t* const ids = a.ids + t0 * a.topk;
-    route(r, ids, n_tok, a.topk, a.E);
+    const Routing r = route(ids, n_tok, a.topk, a.E);
     if (blockIdx.x == 0) {
-        for (int i = threadIdx.x; i < n_tok * a.topk; i += kThreads) {
+        for (int i = threadIdx.x; i < n_tok * a.topk; i += 64 * NW) {
             const int32_t e = ids[i];
             const int t = i / a.topk;
             int row = -1;
@@ -230,52 +260,45 @@ __global__ void __launch_bounds__(kThreads) moe_gate_up_kernel(MoeArgs a) {
             a.pair[t0 * a.topk + i] = row;
         }
     }
-    const int tiles = (int)((a.I + 15) / 16);
-    const GateUpUnits<E> p{a, r, a.w13, a.s13, a.H, a.H / 2, a.H / 32, t0, tiles};
+    const int tiles = (int)(a.I / 16);
+    const GateUpUnits<E> p{a, r, a.H, a.H / 2, a.H / 32, t0, tiles};
     const int64_t items = (int64_t)r.tiles * tiles;
-    stream_units<E, 1, 1, ST, kMoeBatch, PASSES>(p, lds, (int)(items * blockIdx.x / gridDim.x) * 2,
-                                                 (int)(items * (blockIdx.x + 1) / gridDim.x) * 2, a.kw13);
+    stream_units<E, 1, ST>(p, lds, (int)(items * blockIdx.x / gridDim.x) * 2,
+                           (int)(items * (blockIdx.x + 1) / gridDim.x) * 2, a.kw13);
 }
 
-// Units of the second product: tile of 16 pairs, columns of the output.
+// Units of the second product: 16 columns of the output for a tile of pairs.
 struct DownUnits {
     static constexpr bool kPair = false;
     const MoeArgs& a;
     const Routing& r;
-    const uint8_t *w, *s;
     int64_t K, ldw, lds, first;  // first: the chunk's first row of h and y
     int tiles;                   // of 16 columns
-    __device__ __forceinline__ int key(int u) const { return u / tiles; }
-    __device__ __forceinline__ const uint16_t* x(int u, int plane, int m) const {
-        const int at = r.tile[key(u)], row = r.row[at / 4] + at % 4 * 16 + m;
-        return row < r.row[at / 4 + 1] ? a.h + (plane * (a.T * a.topk) + first + row) * a.I : nullptr;
+    __device__ __forceinline__ MoeRun run(int u) const { return moe_run(r, u, tiles); }
+    __device__ __forceinline__ const uint16_t* x(const MoeRun& run, int plane, int m) const {
+        return m < run.pairs ? a.h + (plane * (a.T * a.topk) + first + run.row + m) * a.I : nullptr;
     }
-    __device__ __forceinline__ int64_t row(int u, int q) const {
-        const int e = r.expert[r.tile[key(u)] / 4];
-        return (int64_t)e * a.H + u % tiles * 16 + q;  // H is a multiple of 16
+    __device__ __forceinline__ Tile tile(const MoeRun& run, int i) const {
+        const int64_t n = (int64_t)run.expert * a.H + run.col + i * 16;
+        return {a.w2 + n * ldw, a.s2 + n * lds, (uint32_t)(16 * ldw), (uint32_t)(16 * lds)};
     }
-    __device__ __forceinline__ bool wanted(int u, int m, int) const {
-        const int at = r.tile[key(u)];
-        return r.row[at / 4] + at % 4 * 16 + m < r.row[at / 4 + 1];
-    }
-    __device__ __forceinline__ void finish(int u, int m, int n, float v) const {
-        const int at = r.tile[key(u)], row = r.row[at / 4] + at % 4 * 16 + m;
-        a.y[(first + row) * a.H + u % tiles * 16 + n] = v;
+    __device__ __forceinline__ bool wanted(const MoeRun& run, int, int m, int) const { return m < run.pairs; }
+    __device__ __forceinline__ void finish(const MoeRun& run, int i, int m, int n, float v) const {
+        a.y[(first + run.row + m) * a.H + run.col + i * 16 + n] = v;
     }
 };
 
-template <int ST, bool PASSES>
-__global__ void __launch_bounds__(kThreads) moe_down_kernel(MoeArgs a) {
-    __shared__ Routing r;
-    __shared__ Lds<1, kMoeBatch, PASSES> lds;
+template <int NW, int ST, bool PASSES>
+__global__ void __launch_bounds__(64 * NW, waves_per_simd(1, 2, ST)) moe_down_kernel(MoeArgs a) {
+    __shared__ Lds<NW, 1, kMoeBatch, NW == 16 ? 1 : 2, PASSES> lds;
     const int64_t t0 = (int64_t)blockIdx.y * kChunk;
     const int n_tok = (int)(a.T - t0 < kChunk ? a.T - t0 : kChunk);
-    route(r, a.ids + t0 * a.topk, n_tok, a.topk, a.E);
+    const Routing r = route(a.ids + t0 * a.topk, n_tok, a.topk, a.E);
     const int tiles = (int)(a.H / 16);
-    const DownUnits p{a, r, a.w2, a.s2, a.I, a.I / 2, a.I / 32, t0 * a.topk, tiles};
+    const DownUnits p{a, r, a.I, a.I / 2, a.I / 32, t0 * a.topk, tiles};
     const int64_t items = (int64_t)r.tiles * tiles;
-    stream_units<ElemBF16, 1, 2, ST, kMoeBatch, PASSES>(p, lds, (int)(items * blockIdx.x / gridDim.x),
-                                                        (int)(items * (blockIdx.x + 1) / gridDim.x), a.kw2);
+    stream_units<ElemBF16, 2, ST>(p, lds, (int)(items * blockIdx.x / gridDim.x),
+                                  (int)(items * (blockIdx.x + 1) / gridDim.x), a.kw2);
 }
 
 // out: 4 columns per thread; the sum goes through a token's choices in order.

@@ -31,9 +31,6 @@ using mx::u32_any;
 using mx::u32x2_any;
 using mx::u32x4_any;
 
-constexpr int kWaves = 8;
-constexpr int kThreads = 64 * kWaves;
-
 // The widened weights of one dword times 2^k (scale holds 2^k): 8 values, k order.
 template <typename E>
 __device__ __forceinline__ f16x8 widen8(uint32_t d, float scale) {
@@ -52,43 +49,45 @@ __device__ __forceinline__ f16x8 widen8(uint32_t d, float scale) {
     return __builtin_bit_cast(f16x8, r);
 }
 
-// A unit of W in registers: step s holds the lane's block 4s + g, and byte g of
-// c[s] its scale code (byte 0 of c[0]: the code of block 0 in every lane).
-template <int ST>
-struct Weights {
-    u32x4 w[ST];
-    uint32_t c[ST];
+// A matrix tile of up to 16 rows as a buffer: loads beyond its `bytes` give 0 and
+// move nothing.  The pointer and size are the same in all lanes.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* p, uint32_t bytes) {
+    const uint64_t at = reinterpret_cast<uint64_t>(p);
+    const uint64_t low = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)at);
+    const uint64_t high = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(at >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(low | high << 32), 0,
+                                             __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
+}
+
+// A unit: up to 16 rows of W and S.
+struct Tile {
+    const uint8_t *w, *s;
+    uint32_t w_bytes, s_bytes;
 };
 
-// `blocks` whole blocks of the row from w and s on are in the wave's range (at
-// least 1, the same in all lanes).  Absent ones repeat block 0; X is 0 there.
+// The scale codes of a unit, `blocks` whole blocks of whose rows are in the wave's
+// range (at least 1, the same in all lanes): the code of the lane's block 4i + g in
+// byte g of c[i], or in byte 0 if the range is not whole.  Blocks beyond it, where
+// X is 0, repeat the code of block 0.
 template <int ST>
-__device__ __forceinline__ void load_weights(Weights<ST>& b, const uint8_t* w, const uint8_t* s, int g, int blocks) {
+__device__ __forceinline__ void load_codes(uint32_t (&c)[ST], __amdgpu_buffer_rsrc_t s, int at, int g, int blocks) {
     if (blocks >= 4 * ST) {
-#pragma unroll
-        for (int i = 0; i < ST; ++i) b.w[i] = *(const u32x4_any*)(w + 16 * g + 64 * i);
         if constexpr (ST == 1) {
-            b.c[0] = *(const u32_any*)s;
+            c[0] = __builtin_amdgcn_raw_buffer_load_b32(s, at, 0, 0);
         } else if constexpr (ST == 2) {
-            const u32x2 c = *(const u32x2_any*)s;
-            b.c[0] = c[0];
-            b.c[1] = c[1];
+            const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(s, at, 0, 0);
+            c[0] = v[0];
+            c[1] = v[1];
         } else {
+            static_assert(ST == 4, "steps per wave");
+            const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(s, at, 0, 0);
 #pragma unroll
-            for (int i = 0; i < ST; i += 4) {
-                const u32x4 c = *(const u32x4_any*)(s + 4 * i);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) b.c[i + j] = c[j];
-            }
+            for (int i = 0; i < ST; ++i) c[i] = v[i];
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < ST; ++i) {
-            const int at = 4 * i + g < blocks ? 4 * i + g : 0;
-            b.w[i] = *(const u32x4_any*)(w + 16 * at);
-            b.c[i] = (uint32_t)s[at] << (8 * g);
-        }
-        if (g != 0) b.c[0] |= s[0];
+        for (int i = 0; i < ST; ++i)
+            c[i] = __builtin_amdgcn_raw_buffer_load_b8(s, at + (4 * i + g < blocks ? 4 * i + g : 0), 0, 0);
     }
 }
 
@@ -116,23 +115,67 @@ __device__ __forceinline__ void load_rows(Rows<MT, PL, ST>& r, const uint16_t* c
             }
 }
 
-// acc[mt] += sum over the unit's blocks, any scale codes, in units of 2^(ref - 127).
-// Block by block: the groups that hold the other blocks put zeros on both sides.
-template <typename E, int MT, int PL, int ST>
-__device__ __forceinline__ void multiply_any(const Weights<ST>& b, const Rows<MT, PL, ST>& r, f32x4 (&acc)[MT], int g,
-                                             int ref) {
-    const u32x4 zero = {0u, 0u, 0u, 0u};
+// The value that lane % 16 holds, in all four lane groups.
+__device__ __forceinline__ uint32_t from_group_0(uint32_t x) {
+    const auto a = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false)[0];
+}
+
+// What multiplies a unit: the lane's scale codes, relative to ref, and whether the
+// conversion can apply them all.  The row of W whose code a lane holds is also its column
+// of the result (D[i][j] of the MFMA has row i of X in lane / 16 * 4 + register and
+// row j of W in lane % 16).
+template <typename E, int ST>
+struct Scales {
+    int ref;
+    uint32_t code[ST];
+    bool any;
+
+    __device__ __forceinline__ Scales(const uint32_t (&c)[ST], int shift) {
+        ref = 127;
+        if constexpr (E::kIsF16) {
+            ref = (int)(from_group_0(c[0]) & 255u);
+            // far enough for any weights; the fp32 sum keeps its range
+            ref = ref < 127 - 24 ? 127 - 24 : (ref > 127 + 24 ? 127 + 24 : ref);
+        }
+        const uint32_t low = E::kIsF16 ? (uint32_t)(ref - 13) : 2u;
+        constexpr uint32_t kSpan = E::kIsF16 ? 26u : 250u;
+        uint32_t worst = 0;
 #pragma unroll
-    for (int i = 0; i < ST; ++i) {
-        const int own = (int)((b.c[i] >> (8 * g)) & 255u);
+        for (int i = 0; i < ST; ++i) {
+            code[i] = (c[i] >> shift) & 255u;
+            worst = code[i] - low > worst ? code[i] - low : worst;
+        }
+        any = __ballot(worst > kSpan) != 0;
+    }
+};
+
+// acc[mt] += the product of one step: 16 rows of W, 128 k, in units of 2^(ref - 127).
+template <typename E, int MT, int PL, int ST>
+__device__ __forceinline__ void multiply(const u32x4& wi, const Scales<E, ST>& s, int i, const Rows<MT, PL, ST>& r,
+                                         f32x4 (&acc)[MT], int g) {
+    if (__builtin_expect(!s.any, 1)) {
+        const float scale = __builtin_bit_cast(float, (s.code[i] + (uint32_t)(127 - s.ref)) << 23);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const f16x8 w = widen8<E>(wi[j], scale);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int p = 0; p < PL; ++p)
+                    acc[mt] = E::mfma16(__builtin_bit_cast(f16x8, r.x[p][mt][i][j]), w, acc[mt]);
+        }
+    } else {
+        // block by block: the groups that hold the other blocks put zeros on both sides
+        const u32x4 zero = {0u, 0u, 0u, 0u};
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
             const bool mine = g == q;
-            const int code = __shfl(own, 16 * q + (int)(threadIdx.x % 16));
+            const int code = __shfl((int)s.code[i], 16 * q + (int)(threadIdx.x % 16));
             f32x4 t[MT] = {};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const f16x8 w = widen8<E>(mine ? b.w[i][j] : 0u, 1.0f);
+                const f16x8 w = widen8<E>(mine ? wi[j] : 0u, 1.0f);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -143,54 +186,8 @@ __device__ __forceinline__ void multiply_any(const Weights<ST>& b, const Rows<MT
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    acc[mt][k] += code == 255 ? __builtin_nanf("") : __builtin_amdgcn_ldexpf(t[mt][k], code - ref);
+                    acc[mt][k] += code == 255 ? __builtin_nanf("") : __builtin_amdgcn_ldexpf(t[mt][k], code - s.ref);
         }
-    }
-}
-
-// acc[mt] = the unit's product.  D[i][j] of the MFMA has row i of X in (lane /
-// 16) * 4 + register and row j of W in lane % 16, so that a lane's own code 0 is
-// that of its column.
-template <typename E, int MT, int PL, int ST>
-__device__ __forceinline__ void multiply(const Weights<ST>& b, const Rows<MT, PL, ST>& r, f32x4 (&acc)[MT], int g) {
-    int ref = 127;
-    if constexpr (E::kIsF16) {
-        ref = (int)(b.c[0] & 255u);
-        // far enough for any weights; the fp32 sum keeps its range
-        ref = ref < 127 - 24 ? 127 - 24 : (ref > 127 + 24 ? 127 + 24 : ref);
-    }
-    const uint32_t low = E::kIsF16 ? (uint32_t)(ref - 13) : 2u;
-    constexpr uint32_t kSpan = E::kIsF16 ? 26u : 250u;
-    uint32_t code[ST], worst = 0;
-#pragma unroll
-    for (int i = 0; i < ST; ++i) {
-        code[i] = (b.c[i] >> (8 * g)) & 255u;
-        worst = code[i] - low > worst ? code[i] - low : worst;
-    }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) acc[mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (__builtin_expect(__ballot(worst > kSpan) == 0, 1)) {
-#pragma unroll
-        for (int i = 0; i < ST; ++i) {
-            const float scale = __builtin_bit_cast(float, (code[i] + (uint32_t)(127 - ref)) << 23);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const f16x8 w = widen8<E>(b.w[i][j], scale);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int p = 0; p < PL; ++p)
-                        acc[mt] = E::mfma16(__builtin_bit_cast(f16x8, r.x[p][mt][i][j]), w, acc[mt]);
-            }
-        }
-    } else {
-        multiply_any<E, MT, PL, ST>(b, r, acc, g, ref);
-    }
-    if constexpr (E::kIsF16) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) acc[mt][k] = __builtin_amdgcn_ldexpf(acc[mt][k], ref - 127);
     }
 }
 
@@ -201,122 +198,159 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// LDS of a workgroup: the partial sums of two batches of TB units per wave (one
-// is written while the other is read), and for a K of several passes the sums
-// so far of at most kSumTiles 16 x 16 tiles.
+// LDS of a workgroup of NW waves: the partial sums of a batch of TB units per wave,
+// twice (one is written while the other is read) or once, and for a K of several
+// passes the sums so far of at most kSumTiles 16 x 16 tiles.
 constexpr int kSumTiles = 16;
-template <int MT, int TB, bool PASSES>
+template <int NW, int MT, int TB, int BUFS, bool PASSES>
 struct Lds {
-    float part[2][TB * MT][kWaves][256];
+    float part[BUFS][TB * MT][NW][256];
     float sum[PASSES ? kSumTiles * 256 : 1];
 };
 
-// Units [u0, u1) of policy P by one workgroup.  kw of its waves share a unit's
-// K, 128 * ST each; with PASSES the X of the next kw * 128 * ST k is loaded and the
-// units are gone through again, at most kSumTiles / MT of them.
+// Units [u0, u1) of policy P by one workgroup of NW waves.  kw of them share a
+// unit's K, 128 * ST each; with PASSES the X of the next kw * 128 * ST k is loaded
+// and the units are gone through again, at most kSumTiles / MT of them.
 // P gives
-//   key(u)                    units with the same key have the same rows of X
-//   x(u, plane, m)            row m of X, or nullptr
-//   row(u, r)                 the index of row r of unit u in W and S
-//   w, s, ldw, lds, K
-//   kPair                     units 2i and 2i + 1 are finished together
-//   finish(u, m, n, v[, v2])  column n of the unit, row m
-template <typename E, int MT, int PL, int ST, int TB, bool PASSES, typename P>
-__device__ __forceinline__ void stream_units(const P& p, Lds<MT, TB, PASSES>& lds, int u0, int u1, int kw) {
-    constexpr int D = 2;
+//   run(u)                    what the units from u on share: their X and more; run.end
+//                             is the first unit with other rows of X
+//   x(run, plane, m)          row m of X, or nullptr
+//   tile(run, i)              the rows of W and S of the run's i-th unit
+//   K, ldw, lds               in k and bytes
+//   kPair                     a run's units 2i and 2i + 1 are finished together
+//   wanted(run, i, m, n), finish(run, i, m, n, v[, v2])   column n of unit i, row m
+template <typename E, int PL, int ST, int NW, int MT, int TB, int BUFS, bool PASSES, typename P>
+__device__ __forceinline__ void stream_units(const P& p, Lds<NW, MT, TB, BUFS, PASSES>& lds, int u0, int u1, int kw) {
+    // units in flight: 4 steps where a batch has as many units
+    constexpr int D = 4 / ST < TB ? 4 / ST : TB;
+    static_assert(TB % D == 0, "a batch is a whole number of turns of the ring");
     constexpr int kPer = P::kPair ? 2 : 1;
     const int lane = threadIdx.x % 64, g = lane / 16, r16 = lane % 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int groups = kWaves / kw, group = wave / kw, part_of = wave % kw;
-    const int units = u1 - u0;
-    if (units <= 0) return;  // (nothing below may ask P for a unit that does not exist)
-    const int turns = (units + TB * groups - 1) / (TB * groups);
+    const int groups = NW / kw, group = wave / kw, part_of = wave % kw;
     const int64_t span = (int64_t)kw * (128 * ST);
-    // the i-th unit of this wave, relative to u0; finished pairs stay together
-    const auto unit_of = [&](int i) { return (i / kPer * groups + group) * kPer + i % kPer; };
     int parity = 0;
-    for (int64_t pass = 0; pass * span < p.K || pass == 0; ++pass) {
+    for (int64_t pass = 0; pass == 0 || (PASSES && pass * span < p.K); ++pass) {
         const int64_t k0 = pass * span + part_of * (128 * ST);
         const int64_t left = (p.K - k0) / 32;
         const bool active = left > 0;
-        const int blocks = active ? (int)(left < 4 * ST ? left : 4 * ST) : 1;
-        const int64_t kw0 = active ? k0 / 2 : 0, ks0 = active ? k0 / 32 : 0;
-        // waves that hold a part of this pass
-        const int64_t rest = (p.K - pass * span + 128 * ST - 1) / (128 * ST);
-        const int parts = rest < kw ? (int)rest : kw;
-        const bool last_pass = (pass + 1) * span >= p.K;
-        Weights<ST> buf[D];
-        Rows<MT, PL, ST> rows;
-        int key = -1;
-        const auto load = [&](Weights<ST>& b, int i) {
-            const int u = unit_of(i);
-            const bool there = u < units;
-            // (absent units: one line of the last one)
-            const int64_t at = p.row(u0 + (there ? u : units - 1), there ? r16 : 0);
-            load_weights<ST>(b, p.w + at * p.ldw + kw0, p.s + at * p.lds + ks0, g, blocks);
-        };
-        if (active) {
-#pragma unroll
-            for (int d = 0; d < D; ++d) load(buf[d], d);
-        }
-        for (int turn = 0; turn < turns; ++turn) {
+        const int blocks = (int)(left < 4 * ST ? left : 4 * ST), shift = blocks < 4 * ST ? 0 : 8 * g;
+        const int w_at = r16 * (int)p.ldw + (int)(k0 / 2) + 16 * g, s_at = r16 * (int)p.lds + (int)(k0 / 32);
+        const bool last_pass = !PASSES || (pass + 1) * span >= p.K;
+        // runs of units with the same X
+        for (int from = u0, to = 0; from < u1; from = to) {
+            const auto run = p.run(from);
+            to = run.end < u1 ? run.end : u1;
+            const int units = to - from;
+            const int turns = (units + TB * groups - 1) / (TB * groups);
+            // the i-th unit of this wave; units that are finished together stay together
+            const auto unit_of = [&](int i) { return (i / kPer * groups + group) * kPer + i % kPer; };
+            const auto tile_of = [&](int i) {
+                const int u = unit_of(i);
+                Tile t = p.tile(run, u < units ? u : units - 1);
+                if (u >= units) t.w_bytes = t.s_bytes = 0;
+                return t;
+            };
+            u32x4 w[D][ST];
+            uint32_t c[D][ST];
+            Rows<MT, PL, ST> rows;
             if (active) {
 #pragma unroll
-                for (int t = 0; t < TB; ++t) {
-                    const int i = turn * TB + t, u = unit_of(i);
-                    if (u < units) {
-                        const int k = p.key(u0 + u);
-                        if (k != key) {
-                            key = k;
-                            const uint16_t* x[PL][MT];
+                for (int d = 0; d < D; ++d) {
+                    const Tile t = tile_of(d);
+                    load_codes<ST>(c[d], buffer_of(t.s, t.s_bytes), s_at, g, blocks);
 #pragma unroll
-                            for (int pl = 0; pl < PL; ++pl)
+                    for (int i = 0; i < ST; ++i)
+                        w[d][i] = __builtin_amdgcn_raw_buffer_load_b128(buffer_of(t.w, t.w_bytes), w_at + 64 * i, 0, 0);
+                }
+                const uint16_t* x[PL][MT];
 #pragma unroll
-                                for (int mt = 0; mt < MT; ++mt) {
-                                    x[pl][mt] = p.x(u0 + u, pl, mt * 16 + r16);
-                                    if (x[pl][mt] != nullptr) x[pl][mt] += k0;
-                                }
-                            load_rows<MT, PL, ST>(rows, x, g, blocks);
-                            // a wait here, so that none is needed where the X of an
-                            // earlier unit is still there
-                            __builtin_amdgcn_s_waitcnt(0x0F70);
-                        }
+                for (int pl = 0; pl < PL; ++pl)
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        x[pl][mt] = p.x(run, pl, mt * 16 + r16);
+                        if (x[pl][mt] != nullptr) x[pl][mt] += k0;
+                    }
+                load_rows<MT, PL, ST>(rows, x, g, blocks);
+            }
+            for (int turn = 0; turn < turns; ++turn) {
+#pragma unroll 1
+                for (int t0 = 0; t0 < TB; t0 += D) {
+#pragma unroll
+                    for (int d = 0; d < D; ++d) {
+                        const int t = t0 + d;
+                        if (unit_of(turn * TB + t) >= units) break;
                         f32x4 acc[MT];
-                        multiply<E, MT, PL, ST>(buf[t % D], rows, acc, g);
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) *(f32x4*)&lds.part[parity][t * MT + mt][wave][lane * 4] = acc[mt];
+                        for (int mt = 0; mt < MT; ++mt) acc[mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                        if (active) {
+                            const Scales<E, ST> scales(c[d], shift);
+                            const Tile next = tile_of(turn * TB + t + D);
+                            load_codes<ST>(c[d], buffer_of(next.s, next.s_bytes), s_at, g, blocks);
+#pragma unroll
+                            for (int i = 0; i < ST; ++i) {
+                                multiply<E, MT, PL, ST>(w[d][i], scales, i, rows, acc, g);
+                                w[d][i] = __builtin_amdgcn_raw_buffer_load_b128(buffer_of(next.w, next.w_bytes),
+                                                                                w_at + 64 * i, 0, 0);
+                            }
+                            if constexpr (E::kIsF16) {
+#pragma unroll
+                                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k)
+                                        acc[mt][k] = __builtin_amdgcn_ldexpf(acc[mt][k], scales.ref - 127);
+                            }
+                        }
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+                            *(f32x4*)&lds.part[parity][t * MT + mt][wave][lane * 4] = acc[mt];
                     }
-                    load(buf[t % D], i + D);
                 }
-            }
-            lds_barrier();
-            const int total = TB / kPer * groups * MT * 256;
-            for (int at = threadIdx.x; at < total; at += kThreads) {
-                const int e = at % 256, q = at / 256, mt = q % MT, t = q / MT % (TB / kPer), gi = q / MT / (TB / kPer);
-                const int m = mt * 16 + e / 64 * 4 + e % 4, n = e / 4 % 16;
-                const int u = ((turn * (TB / kPer) + t) * groups + gi) * kPer;
-                if (u < units && p.wanted(u0 + u, m, n)) {
-                    float v[kPer];
+                lds_barrier();
+                const int total = TB / kPer * groups * MT * 256;
+                // (a thread number that the compiler takes for new in each turn: what follows
+                // from it is not kept in registers through the loop above)
+                int first = threadIdx.x;
+                asm volatile("" : "+v"(first));
+                for (int at = first; at < total; at += 64 * NW) {
+                    const int e = at % 256, q = at / 256, mt = q % MT, t = q / MT % (TB / kPer);
+                    const int m = mt * 16 + e / 64 * 4 + e % 4, n = e / 4 % 16, gi = q / MT / (TB / kPer);
+                    const int u = ((turn * (TB / kPer) + t) * groups + gi) * kPer;
+                    if (u < units && p.wanted(run, u, m, n)) {
+                        float v[kPer];
 #pragma unroll
-                    for (int h = 0; h < kPer; ++h) {
-                        v[h] = 0.0f;
-                        for (int w = 0; w < parts; ++w)
-                            v[h] += lds.part[parity][(t * kPer + h) * MT + mt][gi * kw + w][e];
-                        if constexpr (PASSES) {
-                            float& sum = lds.sum[((u + h) * MT + mt) * 256 + e];
-                            if (pass > 0) v[h] += sum;
-                            if (!last_pass) sum = v[h];
+                        for (int h = 0; h < kPer; ++h) {
+                            const auto& part = lds.part[parity][(t * kPer + h) * MT + mt];
+                            v[h] = part[gi * kw][e];
+                            if (kw >= 4) {
+#pragma unroll 1
+                                for (int i = 0; i < kw; i += 4) {
+                                    const float a = part[gi * kw + i][e], b = part[gi * kw + i + 1][e],
+                                                y = part[gi * kw + i + 2][e], z = part[gi * kw + i + 3][e];
+                                    v[h] = (i == 0 ? a : v[h] + a) + b + y + z;
+                                }
+                            } else if (kw == 2) {
+                                v[h] += part[gi * kw + 1][e];
+                            }
+                            if constexpr (PASSES) {
+                                float& sum = lds.sum[((from - u0 + u + h) * MT + mt) * 256 + e];
+                                if (pass > 0) v[h] += sum;
+                                if (!last_pass) sum = v[h];
+                            }
+                        }
+                        if (last_pass) {
+                            if constexpr (P::kPair)
+                                p.finish(run, u, m, n, v[0], v[1]);
+                            else
+                                p.finish(run, u, m, n, v[0]);
                         }
                     }
-                    if (!PASSES || last_pass) {
-                        if constexpr (P::kPair)
-                            p.finish(u0 + u, m, n, v[0], v[1]);
-                        else
-                            p.finish(u0 + u, m, n, v[0]);
-                    }
                 }
+                if constexpr (BUFS == 2)
+                    parity ^= 1;
+                else if (PASSES || turn + 1 < turns || to < u1)
+                    lds_barrier();
             }
-            parity ^= 1;
         }
     }
 }
