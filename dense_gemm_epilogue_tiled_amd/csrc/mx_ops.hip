@@ -242,13 +242,46 @@ int run_moe(gr::w4::MoeArgs a, hipStream_t stream) {
     return launch_grid(moe_combine_kernel<E>, g, kCombineThreads, stream, a);
 }
 
+// Two kernels where one CU would read Wr (E * H values) for longer than the second
+// kernel takes, and the tokens do not fill the chip by themselves: 4096 x 64 for one
+// token takes 20 us in one kernel; 2048 x 32 takes 7.7 us either way.
+int64_t route_workspace(int64_t T, int64_t H, int64_t E) {
+    if (T > 512 || E * H <= 65536 || H > (int64_t(1) << 24)) return 0;
+    const int64_t slice = 32 * gr::w4::kSliceSteps, bytes = (H + slice - 1) / slice * T * E * 4;
+    return aligned(bytes);
+}
+
 template <typename E>
 int run_route(const gr::w4::RouteArgs& a, hipStream_t stream) {
     using namespace gr::w4;
-    const int64_t grid = (a.T + 15) / 16;
-    if (a.E <= 64) return launch(moe_route_kernel<E, 1>, grid, kRouteThreads, stream, a);
-    if (a.E <= 256) return launch(moe_route_kernel<E, 4>, grid, kRouteThreads, stream, a);
-    return launch(moe_route_kernel<E, 16>, grid, kRouteThreads, stream, a);
+    const int64_t tiles = (a.T + 15) / 16;
+    if (a.partial != nullptr) {
+        const int64_t slice = 32 * kSliceSteps;
+        const dim3 grid((uint32_t)((a.E + 15) / 16), (uint32_t)((a.H + slice - 1) / slice), (uint32_t)tiles);
+        const int st = launch_grid(moe_logits_kernel<E>, grid, 64 * kSliceWaves, stream, a);
+        if (st != GR_OK) return st;
+        const int64_t picks = (a.T + kPickWaves - 1) / kPickWaves;
+        if (a.E <= 64) return launch(moe_pick_kernel<1>, picks, 64 * kPickWaves, stream, a);
+        if (a.E <= 256) return launch(moe_pick_kernel<4>, picks, 64 * kPickWaves, stream, a);
+        return launch(moe_pick_kernel<16>, picks, 64 * kPickWaves, stream, a);
+    }
+    // tokens beyond what one grid counts (2^32 threads) go in further launches
+    const int64_t most = (int64_t(1) << 31) / kRouteThreads;
+    for (int64_t at = 0; at < tiles; at += most) {
+        RouteArgs b = a;
+        b.x += at * 16 * a.ldx;
+        b.ids += at * 16 * a.topk;
+        b.weights += at * 16 * a.topk;
+        b.T -= at * 16;
+        const int64_t grid = tiles - at < most ? tiles - at : most;
+        const int st = a.E <= 16    ? launch(moe_route_kernel<E, 1, 1>, grid, kRouteThreads, stream, b)
+                       : a.E <= 32  ? launch(moe_route_kernel<E, 2, 1>, grid, kRouteThreads, stream, b)
+                       : a.E <= 64  ? launch(moe_route_kernel<E, 4, 1>, grid, kRouteThreads, stream, b)
+                       : a.E <= 256 ? launch(moe_route_kernel<E, 4, 4>, grid, kRouteThreads, stream, b)
+                                    : launch(moe_route_kernel<E, 4, 16>, grid, kRouteThreads, stream, b);
+        if (st != GR_OK) return st;
+    }
+    return GR_OK;
 }
 
 }  // namespace
@@ -336,25 +369,42 @@ int gemm_w4_bt(int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, 
     return fmt == GR_FMT_BF16 ? run_w4<gr::ElemBF16>(a, h) : run_w4<gr::ElemF16>(a, h);
 }
 
-int moe_route(int64_t T, int64_t H, int64_t E, int64_t topk, const uint16_t* X, int64_t ldx, const uint16_t* Wr,
-              int64_t ldwr, const float* bias, int renorm, int32_t* ids, float* weights, int fmt, void* stream) {
+int moe_route_workspace_size(int64_t T, int64_t H, int64_t E, int64_t* bytes) {
+    if (!bytes) return GR_ERR_INVALID_ARG;
     if (T < 0 || H < 0 || E < 1) return GR_ERR_INVALID_DIM;
-    if (topk < 1 || topk > E || !known_fmt(fmt) || (renorm != 0 && renorm != 1)) return GR_ERR_INVALID_ARG;
+    if (T > kMaxDim || H > kMaxDim || E > gr::w4::kMaxExperts) return GR_ERR_TOO_LARGE;
+    *bytes = route_workspace(T, H, E);
+    return GR_OK;
+}
+
+int moe_route(int64_t T, int64_t H, int64_t E, int64_t topk, const uint16_t* X, int64_t ldx, const uint16_t* Wr,
+              int64_t ldwr, const float* bias, int renorm, int32_t* ids, float* weights, int fmt, void* workspace,
+              int64_t workspace_bytes, void* stream) {
+    if (T < 0 || H < 0 || E < 1) return GR_ERR_INVALID_DIM;
+    if (topk < 1 || topk > E || !known_fmt(fmt) || (renorm != 0 && renorm != 1) || workspace_bytes < 0)
+        return GR_ERR_INVALID_ARG;
     if (T > kMaxDim || H > kMaxDim || E > gr::w4::kMaxExperts || topk > gr::w4::kMaxTopK) return GR_ERR_TOO_LARGE;
     const int64_t hmin = H > 1 ? H : 1;
     if (ldx < hmin || ldwr < hmin) return GR_ERR_INVALID_LD;
     if (T == 0) return GR_OK;
     if (!ids || !weights || (H > 0 && (!X || !Wr))) return GR_ERR_NULL_PTR;
+    if (reinterpret_cast<uintptr_t>(workspace) % kWorkspaceAlign != 0) return GR_ERR_INVALID_ARG;
+    // (too small a workspace is none, as for the products)
+    int64_t need = route_workspace(T, H, E);
+    if (!workspace || workspace_bytes < need) need = 0;
     const Region x = matrix16(X, T, H, ldx), w = matrix16(Wr, E, H, ldwr),
                  b{reinterpret_cast<uintptr_t>(bias), bias ? E * 4 : 0}, i{reinterpret_cast<uintptr_t>(ids), T * topk * 4},
-                 v{reinterpret_cast<uintptr_t>(weights), T * topk * 4};
+                 v{reinterpret_cast<uintptr_t>(weights), T * topk * 4},
+                 s{reinterpret_cast<uintptr_t>(workspace), need};
     if (x.bytes < 0 || w.bytes < 0) return GR_ERR_TOO_LARGE;
     if (overlaps(i, v) || overlaps(i, x) || overlaps(i, w) || overlaps(i, b) || overlaps(v, x) || overlaps(v, w) ||
-        overlaps(v, b))
+        overlaps(v, b) || overlaps(s, x) || overlaps(s, w) || overlaps(s, b) || overlaps(s, i) || overlaps(s, v))
         return GR_ERR_ALIAS;
     int st = check_device();
     if (st != GR_OK) return st;
-    const gr::w4::RouteArgs a{X, Wr, bias, ids, weights, T, H, ldx, ldwr, (int)E, (int)topk, renorm};
+    const gr::w4::RouteArgs a{X,   Wr,  bias,   ids,       weights, T,
+                              H,   ldx, ldwr,   (int)E,    (int)topk, renorm,
+                              need > 0 ? static_cast<float*>(workspace) : nullptr};
     hipStream_t h = static_cast<hipStream_t>(stream);
     return fmt == GR_FMT_BF16 ? run_route<gr::ElemBF16>(a, h) : run_route<gr::ElemF16>(a, h);
 }

@@ -77,15 +77,29 @@ __device__ __forceinline__ float dppf(float x) {
 }
 constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E, kRowHalfMirror = 0x141, kRowMirror = 0x140;
 
+// f over x of this lane and of the lane 16 (32) further, the same in all lanes: the
+// swap of a register with itself gives both halves to every lane.
+template <typename F>
+__device__ __forceinline__ uint32_t over_16(uint32_t x, F f) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return f(r[0], r[1]);
+}
+template <typename F>
+__device__ __forceinline__ uint32_t over_32(uint32_t x, F f) {
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return f(r[0], r[1]);
+}
+
 // The sum over the 64 lanes, the same bits in each (a fixed tree).
 __device__ __forceinline__ float wave_sum(float x) {
     x += dppf<kQuadXor1>(x);
     x += dppf<kQuadXor2>(x);
     x += dppf<kRowHalfMirror>(x);
     x += dppf<kRowMirror>(x);
-    x += __shfl_xor(x, 16);
-    x += __shfl_xor(x, 32);
-    return x;
+    const auto add = [](uint32_t a, uint32_t b) {
+        return __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));
+    };
+    return __builtin_bit_cast(float, over_32(over_16(__builtin_bit_cast(uint32_t, x), add), add));
 }
 
 // Write 8 values of one row: column c8 * 8 on, n of them (n < 8 only for the

@@ -346,9 +346,13 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(MoeArgs a)
 //   the topk largest, in order (ties: lower index first; NaN above infinity),
 //   weight[j] = exp(logit_j - max) / sum over the chosen (renorm) or over all E
 //
-// A workgroup takes 16 tokens and every expert: its waves share the tiles of
-// 16 experts and their K, the logits meet in LDS, and each wave then
-// picks for whole tokens.
+// One kernel: a workgroup takes 16 tokens and every expert.  Its waves share K, each with
+// a few steps of 32 k for NT tiles of 16 experts in flight at once.  The logits meet
+// in LDS, and each wave then picks for one token.  One CU reads some 35 KB a
+// microsecond: 4096 x 64 takes 20 us for one token.
+// Few tokens and a large Wr take two: logits of 16 tokens and 16 experts over slices
+// of 512 k by a workgroup each, partial sums to the workspace; then a wave per token
+// adds the slices in order and picks.
 
 constexpr int kRouteWaves = 16;
 constexpr int kRouteThreads = 64 * kRouteWaves;
@@ -361,6 +365,7 @@ struct RouteArgs {
     float* weights;
     int64_t T, H, ldx, ldw;
     int E, topk, renorm;
+    float* partial;  // two kernels: slices x T x E
 };
 
 // Order-preserving bits of a float, at least 1; NaN above everything.
@@ -373,31 +378,25 @@ __device__ __forceinline__ uint32_t order_bits(float x) {
 }
 
 __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
-    uint32_t o = mx::dpp<mx::kQuadXor1>(x);
-    x = o > x ? o : x;
-    o = mx::dpp<mx::kQuadXor2>(x);
-    x = o > x ? o : x;
-    o = mx::dpp<mx::kRowHalfMirror>(x);
-    x = o > x ? o : x;
-    o = mx::dpp<mx::kRowMirror>(x);
-    x = o > x ? o : x;
-    o = __shfl_xor(x, 16);
-    x = o > x ? o : x;
-    o = __shfl_xor(x, 32);
-    return o > x ? o : x;
+    const auto most = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+    x = most(x, mx::dpp<mx::kQuadXor1>(x));
+    x = most(x, mx::dpp<mx::kQuadXor2>(x));
+    x = most(x, mx::dpp<mx::kRowHalfMirror>(x));
+    x = most(x, mx::dpp<mx::kRowMirror>(x));
+    return mx::over_32(mx::over_16(x, most), most);
 }
 
 // The topk of one token's E logits, by one wave; PER logits per lane (expert
 // = lane + 64 * i).
-template <int PER>
-__device__ __forceinline__ void pick(const float* logits, int E, int topk, int renorm, int32_t* ids, float* weights) {
+template <int PER, typename F>
+__device__ __forceinline__ void pick(F logit_of, int E, int topk, int renorm, int32_t* ids, float* weights) {
     const int lane = threadIdx.x % 64;
     float v[PER];
     uint32_t key[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int e = lane + 64 * i;
-        v[i] = e < E ? logits[e] : 0.0f;
+        v[i] = e < E ? logit_of(e) : 0.0f;
         key[i] = e < E ? order_bits(v[i]) : 0u;
     }
     int my_id = 0;
@@ -406,7 +405,7 @@ __device__ __forceinline__ void pick(const float* logits, int E, int topk, int r
         uint32_t m = key[0];
 #pragma unroll
         for (int i = 1; i < PER; ++i) m = key[i] > m ? key[i] : m;
-        m = wave_max(m);
+        m = (uint32_t)__builtin_amdgcn_readfirstlane((int)wave_max(m));
         int id = 0, owner = -1;
         float logit = 0.0f;
 #pragma unroll
@@ -415,7 +414,7 @@ __device__ __forceinline__ void pick(const float* logits, int E, int topk, int r
             if (owner < 0 && has != 0) {
                 owner = __ffsll(has) - 1;
                 id = owner + 64 * i;
-                logit = __shfl(v[i], owner);
+                logit = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v[i]), owner));
                 if (lane == owner) key[i] = 0;
             }
         }
@@ -441,65 +440,126 @@ __device__ __forceinline__ void pick(const float* logits, int E, int topk, int r
     }
 }
 
-template <typename E, int PER>
+// acc[nt] += X times tile nt of Wr over the steps [first, last) of 32 k, U of them in
+// flight; x and w are the lane's rows.
+template <typename E, int NT, int U>
+__device__ __forceinline__ void route_product(const uint16_t* x, const uint16_t* const (&w)[NT], int64_t H,
+                                              int64_t first, int64_t last, f32x4 (&acc)[NT]) {
+    const int g = threadIdx.x % 64 / 16;
+    const int64_t whole = H / 32, until = last < whole ? last : whole;
+    for (int64_t k = first; k < until; k += U) {
+        u32x4 xv[U], wv[U][NT];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (k + u < until) {
+                xv[u] = *(const u32x4_any*)(x + (k + u) * 32 + g * 8);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) wv[u][nt] = *(const u32x4_any*)(w[nt] + (k + u) * 32 + g * 8);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (k + u < until) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    acc[nt] =
+                        E::mfma16(__builtin_bit_cast(f16x8, xv[u]), __builtin_bit_cast(f16x8, wv[u][nt]), acc[nt]);
+            }
+    }
+    if (whole < last && whole >= first) {  // the tail of H: absent values are 0 on both sides
+        const int left = (int)(H - whole * 32) - g * 8, n = left < 8 ? left : 8;
+        u32x4 xt = {0u, 0u, 0u, 0u};
+        if (n > 0) xt = mx::load8(x + whole * 32 + g * 8, n);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            u32x4 wt = {0u, 0u, 0u, 0u};
+            if (n > 0) wt = mx::load8(w[nt] + whole * 32 + g * 8, n);
+            acc[nt] = E::mfma16(__builtin_bit_cast(f16x8, xt), __builtin_bit_cast(f16x8, wt), acc[nt]);
+        }
+    }
+}
+
+// NT tiles of 16 experts at a time; PER * 64 experts at most.
+template <typename E, int NT, int PER>
 __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(RouteArgs a) {
-    __shared__ float part[kRouteWaves][4][64];
+    __shared__ float part[kRouteWaves][NT][256];
     __shared__ float logits[16][64 * PER];
-    const int lane = threadIdx.x % 64, g = lane / 16;
+    const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int64_t t0 = (int64_t)blockIdx.x * 16;
-    const int n_tiles = (a.E + 15) / 16;
-    // waves per tile of 16 experts: a power of two, all 16 for one tile
-    int kw = kRouteWaves;
-    while (kw > 1 && kw * n_tiles > kRouteWaves) kw /= 2;
-    const int per_turn = kRouteWaves / kw;
     const int64_t t = t0 + lane % 16 < a.T ? t0 + lane % 16 : a.T - 1;
-    const uint16_t* const x = a.x + t * a.ldx;
     const int64_t steps = (a.H + 31) / 32;
-    const int64_t first = steps * (wave % kw) / kw, last = steps * (wave % kw + 1) / kw;
-    const int turns = (n_tiles + per_turn - 1) / per_turn;
-    for (int turn = 0; turn < turns; ++turn) {
-        const int nt = turn * per_turn + wave / kw;
-        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (nt < n_tiles) {
-            const int e = nt * 16 + lane % 16 < a.E ? nt * 16 + lane % 16 : a.E - 1;
-            const uint16_t* const w = a.w + (int64_t)e * a.ldw;
-            const int64_t whole = a.H / 32 < last ? a.H / 32 : last;
-            int64_t k = first;
-#pragma unroll 8
-            for (; k < whole; ++k) {
-                const u32x4 xv = *(const u32x4_any*)(x + k * 32 + g * 8);
-                const u32x4 wv = *(const u32x4_any*)(w + k * 32 + g * 8);
-                acc = E::mfma16(__builtin_bit_cast(f16x8, xv), __builtin_bit_cast(f16x8, wv), acc);
-            }
-            if (k < last) {  // the tail of H: absent values are 0 on both sides
-                const int64_t left = a.H - (k * 32 + g * 8);
-                u32x4 xv = {0u, 0u, 0u, 0u}, wv = {0u, 0u, 0u, 0u};
-                if (left > 0) {
-                    xv = mx::load8(x + k * 32 + g * 8, left < 8 ? (int)left : 8);
-                    wv = mx::load8(w + k * 32 + g * 8, left < 8 ? (int)left : 8);
-                }
-                acc = E::mfma16(__builtin_bit_cast(f16x8, xv), __builtin_bit_cast(f16x8, wv), acc);
-            }
-        }
+    for (int e0 = 0; e0 < a.E; e0 += 16 * NT) {
+        const uint16_t* w[NT];
+        f32x4 acc[NT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) part[wave][i][lane] = acc[i];
+        for (int nt = 0; nt < NT; ++nt) {
+            const int e = e0 + nt * 16 + lane % 16 < a.E ? e0 + nt * 16 + lane % 16 : a.E - 1;
+            w[nt] = a.w + (int64_t)e * a.ldw;
+            acc[nt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        route_product<E, NT, NT == 4 ? 2 : 4>(a.x + t * a.ldx, w, a.H, steps * wave / kRouteWaves,
+                                              steps * (wave + 1) / kRouteWaves, acc);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) *(f32x4*)&part[wave][nt][lane * 4] = acc[nt];
         __syncthreads();
-        // 256 sums per tile
-        for (int i = threadIdx.x; i < per_turn * 256; i += kRouteThreads) {
-            const int tile = i / 256, reg = i / 64 % 4, l = i % 64;
+        for (int i = threadIdx.x; i < NT * 256; i += kRouteThreads) {
+            const int nt = i / 256, at = i % 256, m = at / 64 * 4 + at % 4, e = e0 + nt * 16 + at / 4 % 16;
             float v = 0.0f;
-            for (int w = 0; w < kw; ++w) v += part[tile * kw + w][reg][l];
-            const int e = (turn * per_turn + tile) * 16 + l % 16;
+#pragma unroll
+            for (int j = 0; j < kRouteWaves; ++j) v += part[j][nt][at];
             if (e < a.E) {
                 if (a.bias != nullptr) v += a.bias[e];
-                logits[l / 16 * 4 + reg][e] = v;
+                logits[m][e] = v;
             }
         }
         __syncthreads();
     }
     const int64_t mine = t0 + wave;
-    if (mine < a.T) pick<PER>(logits[wave], a.E, a.topk, a.renorm, a.ids + mine * a.topk, a.weights + mine * a.topk);
+    if (mine < a.T)
+        pick<PER>([&](int e) { return logits[wave][e]; }, a.E, a.topk, a.renorm, a.ids + mine * a.topk,
+                  a.weights + mine * a.topk);
+}
+
+constexpr int kSliceSteps = 16;  // of 32 k
+constexpr int kSliceWaves = 4;
+constexpr int kPickWaves = 4;
+
+// Grid: tiles of 16 experts, slices, tiles of 16 tokens.
+template <typename E>
+__global__ void __launch_bounds__(64 * kSliceWaves) moe_logits_kernel(RouteArgs a) {
+    __shared__ float part[kSliceWaves][256];
+    const int lane = threadIdx.x % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int64_t t0 = (int64_t)blockIdx.z * 16;
+    const int64_t t = t0 + lane % 16 < a.T ? t0 + lane % 16 : a.T - 1;
+    const int e0 = blockIdx.x * 16, e = e0 + lane % 16 < a.E ? e0 + lane % 16 : a.E - 1;
+    const int64_t steps = (a.H + 31) / 32, first = (int64_t)blockIdx.y * kSliceSteps;
+    const int64_t mine = first + wave * (kSliceSteps / kSliceWaves), past = mine + kSliceSteps / kSliceWaves;
+    const uint16_t* const w[1] = {a.w + (int64_t)e * a.ldw};
+    f32x4 acc[1] = {};
+    route_product<E, 1, kSliceSteps / kSliceWaves>(a.x + t * a.ldx, w, a.H, mine, past < steps ? past : steps, acc);
+    *(f32x4*)&part[wave][lane * 4] = acc[0];
+    __syncthreads();
+    const int at = threadIdx.x, m = at / 64 * 4 + at % 4, col = e0 + at / 4 % 16;
+    float v = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kSliceWaves; ++j) v += part[j][at];
+    if (t0 + m < a.T && col < a.E) a.partial[((int64_t)blockIdx.y * a.T + t0 + m) * a.E + col] = v;
+}
+
+template <int PER>
+__global__ void __launch_bounds__(64 * kPickWaves) moe_pick_kernel(RouteArgs a) {
+    const int64_t t = (int64_t)blockIdx.x * kPickWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    if (t >= a.T) return;
+    const int slices = (int)((a.H + 32 * kSliceSteps - 1) / (32 * kSliceSteps));
+    pick<PER>(
+        [&](int e) {
+            float v = 0.0f;
+#pragma unroll 8
+            for (int s = 0; s < slices; ++s) v += a.partial[((int64_t)s * a.T + t) * a.E + e];
+            return a.bias != nullptr ? v + a.bias[e] : v;
+        },
+        a.E, a.topk, a.renorm, a.ids + t * a.topk, a.weights + t * a.topk);
 }
 
 }  // namespace w4

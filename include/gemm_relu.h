@@ -912,13 +912,21 @@ int gemm_w4_bt(int64_t M, int64_t N, int64_t K,
  *   X, Wr         T x H and E x H in fmt, pitches ldx, ldwr; any H
  *   bias          E floats or NULL
  *   ids, weights  T x topk, contiguous
+ *   workspace     scratch of moe_route_workspace_size bytes (256-byte aligned), which
+ *                 spreads a large Wr over the chip for few tokens; NULL or too
+ *                 small: one kernel that needs none.  The size is 0 where it
+ *                 would not help.  The logits of the two may differ by
+ *                 roundings of their fp32 sums.
  * E <= 1024, topk <= 32 (GR_ERR_TOO_LARGE), 1 <= topk <= E
  * (GR_ERR_INVALID_ARG).
  */
+int moe_route_workspace_size(int64_t T, int64_t H, int64_t E, int64_t* bytes);
+
 int moe_route(int64_t T, int64_t H, int64_t E, int64_t topk,
               const uint16_t* X, int64_t ldx,
               const uint16_t* Wr, int64_t ldwr, const float* bias, int renorm,
-              int32_t* ids, float* weights, int fmt, void* stream);
+              int32_t* ids, float* weights, int fmt,
+              void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
  * moe_w4 -- the experts of a mixture-of-experts layer with MX fp4 weights:
