@@ -21,6 +21,8 @@ bool known_fmt(int fmt) { return fmt == GR_FMT_F16 || fmt == GR_FMT_BF16; }
 bool known_act(int act) { return act >= 0 && act < gr::kActCount; }
 bool known_out(int out) { return out == GR_OUT_16 || out == GR_OUT_MXFP8 || out == GR_OUT_MXFP4; }
 
+int64_t aligned(int64_t bytes) { return (bytes + kWorkspaceAlign - 1) / kWorkspaceAlign * kWorkspaceAlign; }
+
 struct Region {
     uintptr_t at;
     int64_t bytes;
@@ -100,12 +102,16 @@ int run_gated(const gr::mx::GatedArgs& a, int out_fmt, hipStream_t stream) {
 
 // ---- 16-bit activations, MX fp4 weights ------------------------------------------
 
+constexpr int64_t kW4MaxPitch = int64_t(1) << 26;
+
 int validate_w4(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* Bt, int64_t ldbt,
                 const void* SB, int64_t ld_sb, const void* bias, int act, const void* C, int64_t ldc, int fmt) {
     if (M < 0 || N < 0 || K < 0 || K % 32 != 0) return GR_ERR_INVALID_DIM;
     if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return GR_ERR_TOO_LARGE;
     if (lda < (K > 1 ? K : 1) || ldbt < (K > 1 ? K / 2 : 1) || ld_sb < (K > 1 ? K / 32 : 1) || ldc < (N > 1 ? N : 1))
         return GR_ERR_INVALID_LD;
+    // (the kernels count a tile of 16 rows of the weights in 32 bits)
+    if (ldbt > kW4MaxPitch || ld_sb > kW4MaxPitch) return GR_ERR_TOO_LARGE;
     if (!known_act(act) || !known_fmt(fmt)) return GR_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return GR_OK;
     if (!C || (K > 0 && (!A || !Bt || !SB))) return GR_ERR_NULL_PTR;
@@ -163,11 +169,39 @@ int launch_w4_rows(const gr::w4::LinearArgs& a, const Division& d, dim3 grid, hi
     return launch_w4<E, 8, MT, 1, false>(a, grid, stream);
 }
 
+// Whether K goes to several workgroups instead of several passes of one: up to
+// 64 rows, where X is read once that way and the sums are small.
+// 64 x 8192 x 8192: one workgroup reads 256 KB of X instead of 1 MB.
+struct Splits {
+    int64_t span, count, ldp;
+};
+
+Splits splits_of(int64_t M, int64_t N, int64_t K) {
+    Splits s{K > 0 ? (K + 127) / 128 * 128 : 128, 1, (N + 3) / 4 * 4};
+    if (M > 64) return s;
+    const int MT = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
+    const Division d = divide(K, MT == 1 ? 4 : 8 / MT, MT == 1);
+    if (!d.passes) return s;
+    const int64_t steps = (K + 127) / 128, most = (int64_t)d.steps * d.waves;
+    const int64_t count = (steps + most - 1) / most;
+    if (count > 64) return s;
+    s.span = (steps + count - 1) / count * 128;
+    s.count = (K + s.span - 1) / s.span;
+    return s;
+}
+
+int64_t w4_workspace(int64_t M, int64_t N, int64_t K) {
+    const Splits s = splits_of(M, N, K);
+    return s.count > 1 ? aligned(s.count * M * s.ldp * 4) : 0;
+}
+
 template <typename E, int MT>
-int run_w4_rows(gr::w4::LinearArgs a, hipStream_t stream) {
-    const Division d = divide(a.K, MT == 1 ? 4 : 8 / MT, MT == 1);
+int run_w4_rows(gr::w4::LinearArgs a, int64_t splits, hipStream_t stream) {
+    const Division d = divide(a.span < a.K ? a.span : a.K, MT == 1 ? 4 : 8 / MT, MT == 1);
     a.kw = d.kw;
-    const int64_t gx = grid_of((a.N + 15) / 16, d, d.waves * d.steps * MT > 32 ? 1 : 2, gr::w4::kSumTiles / MT);
+    int64_t wgs = d.waves * d.steps * MT > 32 ? 1 : 2;
+    int64_t gx = grid_of((a.N + 15) / 16, d, wgs, gr::w4::kSumTiles / MT);
+    if (splits > 1 && gx > kCus * wgs / splits) gx = kCus * wgs / splits > 1 ? kCus * wgs / splits : 1;
     const int64_t gy = (a.M + 16 * MT - 1) / (16 * MT);
     // rows beyond the grid's y limit go in further launches
     for (int64_t y = 0; y < gy; y += 65535) {
@@ -175,25 +209,26 @@ int run_w4_rows(gr::w4::LinearArgs a, hipStream_t stream) {
         b.x += y * 16 * MT * a.ldx;
         b.c += y * 16 * MT * a.ldc;
         b.M -= y * 16 * MT;
-        const dim3 grid((uint32_t)gx, (uint32_t)(gy - y < 65535 ? gy - y : 65535));
+        const dim3 grid((uint32_t)gx, (uint32_t)(gy - y < 65535 ? gy - y : 65535), (uint32_t)splits);
         const int st = launch_w4_rows<E, MT>(b, d, grid, stream);
         if (st != GR_OK) return st;
     }
-    return GR_OK;
+    if (splits == 1) return GR_OK;
+    const int64_t per = 4 * gr::w4::kSumThreads;
+    return launch_grid(gr::w4::linear_w4_sum_kernel<E>, dim3((uint32_t)((a.N + per - 1) / per), (uint32_t)a.M),
+                       gr::w4::kSumThreads, stream, a);
 }
 
 template <typename E>
-int run_w4(const gr::w4::LinearArgs& a, hipStream_t stream) {
-    if (a.M <= 16) return run_w4_rows<E, 1>(a, stream);
-    if (a.M <= 32) return run_w4_rows<E, 2>(a, stream);
-    return run_w4_rows<E, 4>(a, stream);
+int run_w4(const gr::w4::LinearArgs& a, int64_t splits, hipStream_t stream) {
+    if (a.M <= 16) return run_w4_rows<E, 1>(a, splits, stream);
+    if (a.M <= 32) return run_w4_rows<E, 2>(a, splits, stream);
+    return run_w4_rows<E, 4>(a, splits, stream);
 }
 
 // ---- mixture of experts ------------------------------------------------------------
 
 constexpr int64_t kMoeMaxDim = int64_t(1) << 20;  // H and I: the kernels count steps of 128 in 32 bits
-
-int64_t aligned(int64_t bytes) { return (bytes + kWorkspaceAlign - 1) / kWorkspaceAlign * kWorkspaceAlign; }
 
 // The workspace: h (two bfloat16 planes), y (fp32), the pairs' rows.
 int64_t moe_h_bytes(int64_t T, int64_t I, int64_t topk) { return aligned(T * topk * I * 4); }
@@ -356,17 +391,41 @@ int gated_act_mx(int64_t M, int64_t N, const uint16_t* G, int64_t ldg, const uin
     return fmt == GR_FMT_BF16 ? run_gated<gr::ElemBF16>(a, out_fmt, h) : run_gated<gr::ElemF16>(a, out_fmt, h);
 }
 
+int gemm_w4_bt_workspace_size(int64_t M, int64_t N, int64_t K, int64_t* bytes) {
+    if (!bytes) return GR_ERR_INVALID_ARG;
+    if (M < 0 || N < 0 || K < 0 || K % 32 != 0) return GR_ERR_INVALID_DIM;
+    if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return GR_ERR_TOO_LARGE;
+    *bytes = w4_workspace(M, N, K);
+    return GR_OK;
+}
+
 int gemm_w4_bt(int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, const uint8_t* Bt, int64_t ldbt,
                const uint8_t* scale_b, int64_t ld_sb, const uint16_t* bias, int act, uint16_t* C, int64_t ldc,
-               int fmt, void* stream) {
+               int fmt, void* workspace, int64_t workspace_bytes, void* stream) {
     int st = validate_w4(M, N, K, A, lda, Bt, ldbt, scale_b, ld_sb, bias, act, C, ldc, fmt);
     if (st != GR_OK) return st;
+    if (workspace_bytes < 0 || reinterpret_cast<uintptr_t>(workspace) % kWorkspaceAlign != 0) return GR_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return GR_OK;
+    // (too small a workspace is none)
+    Splits s = splits_of(M, N, K);
+    const int64_t need = w4_workspace(M, N, K);
+    if (!workspace || workspace_bytes < need) {
+        s.count = 1;
+        s.span = K > 0 ? (K + 127) / 128 * 128 : 128;
+    }
+    if (s.count > 1) {
+        const Region ws{reinterpret_cast<uintptr_t>(workspace), need};
+        if (overlaps(ws, matrix16(C, M, N, ldc)) || overlaps(ws, matrix16(A, M, K, lda)) ||
+            overlaps(ws, matrix8(Bt, N, K / 2, ldbt)) || overlaps(ws, matrix8(scale_b, N, K / 32, ld_sb)) ||
+            overlaps(ws, matrix16(bias, 1, N, N)))
+            return GR_ERR_ALIAS;
+    }
     st = check_device();
     if (st != GR_OK) return st;
-    const gr::w4::LinearArgs a{A, Bt, scale_b, bias, C, M, N, K, lda, ldbt, ld_sb, ldc, act, 1};
+    const gr::w4::LinearArgs a{A,   Bt,   scale_b, bias, C,   M, N, K, lda, ldbt, ld_sb, ldc, act, 1,
+                               s.count > 1 ? static_cast<float*>(workspace) : nullptr, s.ldp, s.span};
     hipStream_t h = static_cast<hipStream_t>(stream);
-    return fmt == GR_FMT_BF16 ? run_w4<gr::ElemBF16>(a, h) : run_w4<gr::ElemF16>(a, h);
+    return fmt == GR_FMT_BF16 ? run_w4<gr::ElemBF16>(a, s.count, h) : run_w4<gr::ElemF16>(a, s.count, h);
 }
 
 int moe_route_workspace_size(int64_t T, int64_t H, int64_t E, int64_t* bytes) {

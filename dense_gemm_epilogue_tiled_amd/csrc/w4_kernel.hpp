@@ -19,22 +19,26 @@ struct LinearArgs {
     uint16_t* c;
     int64_t M, N, K, ldx, ldw, lds, ldc;
     int act;
-    int kw;  // waves that share a unit's K: 1, 2, 4 or 8
+    int kw;          // waves that share a unit's K: a power of two
+    float* partial;  // split K: a matrix of M x ldp sums for each split, else nullptr
+    int64_t ldp;
+    int64_t span;    // k of one split, a multiple of 128
 };
 
-// 16 * MT rows of X from m0 on.
+// 16 * MT rows of X from m0 on, and the k of one split.
 template <typename E>
 struct LinearUnits {
     static constexpr bool kPair = false;
     const LinearArgs& a;
     const uint8_t *w, *s;
-    int64_t K, ldw, lds, m0;
+    int64_t K, ldw, lds, m0, k0;
+    float* partial;
     struct Run {
         int from, end;
     };
     __device__ __forceinline__ Run run(int u) const { return {u, 0x7FFFFFFF}; }
     __device__ __forceinline__ const uint16_t* x(const Run&, int, int m) const {
-        return m0 + m < a.M ? a.x + (m0 + m) * a.ldx : nullptr;
+        return m0 + m < a.M ? a.x + (m0 + m) * a.ldx + k0 : nullptr;
     }
     __device__ __forceinline__ Tile tile(const Run& run, int i) const {
         const int64_t n = (int64_t)(run.from + i) * 16, rows = a.N - n < 16 ? a.N - n : 16;
@@ -45,6 +49,10 @@ struct LinearUnits {
     }
     __device__ __forceinline__ void finish(const Run& run, int i, int m, int n, float v) const {
         const int64_t col = (int64_t)(run.from + i) * 16 + n;
+        if (partial != nullptr) {
+            partial[(m0 + m) * a.ldp + col] = v;
+            return;
+        }
         if (a.bias != nullptr) v += E::widen(a.bias[col]);
         a.c[(m0 + m) * a.ldc + col] = E::round(mx::exact_activate(v, a.act));
     }
@@ -60,9 +68,36 @@ __global__ void __launch_bounds__(64 * NW, waves_per_simd(MT, 1, ST)) linear_w4_
     constexpr int TB = MT == 1 ? (NW == 16 && !PASSES ? 8 : 4) : 2, BUFS = NW == 16 ? 1 : 2;
     __shared__ Lds<NW, MT, TB, BUFS, PASSES> lds;
     const int64_t units = (a.N + 15) / 16;
-    const LinearUnits<E> p{a, a.w, a.s, a.K, a.ldw, a.lds, (int64_t)blockIdx.y * (16 * MT)};
+    const int64_t k0 = blockIdx.z * a.span, K = a.K - k0 < a.span ? a.K - k0 : a.span;
+    float* const partial = a.partial != nullptr ? a.partial + blockIdx.z * a.M * a.ldp : nullptr;
+    const LinearUnits<E> p{a, a.w + k0 / 2, a.s + k0 / 32, K, a.ldw, a.lds, (int64_t)blockIdx.y * (16 * MT), k0, partial};
     stream_units<E, 1, ST>(p, lds, (int)(units * blockIdx.x / gridDim.x), (int)(units * (blockIdx.x + 1) / gridDim.x),
                            a.kw);
+}
+
+// C from the splits' sums, added in order; 4 columns per thread.
+constexpr int kSumThreads = 256;
+
+template <typename E>
+__global__ void __launch_bounds__(kSumThreads) linear_w4_sum_kernel(LinearArgs a) {
+    const int64_t n = ((int64_t)blockIdx.x * kSumThreads + threadIdx.x) * 4, m = blockIdx.y;
+    if (n >= a.N) return;
+    const int splits = (int)((a.K + a.span - 1) / a.span);
+    const float* p = a.partial + m * a.ldp + n;
+    f32x4 v = *(const f32x4*)p;
+    for (int s = 1; s < splits; ++s) {
+        p += a.M * a.ldp;
+        const f32x4 w = *(const f32x4*)p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += w[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (n + i < a.N) {
+            float x = v[i];
+            if (a.bias != nullptr) x += E::widen(a.bias[n + i]);
+            a.c[m * a.ldc + n + i] = E::round(mx::exact_activate(x, a.act));
+        }
 }
 
 // ---- mixture of experts -----------------------------------------------------------

@@ -33,10 +33,18 @@ def gated_act_mx(M, N, G, ldg, U, ldu, act, Y, ldy, SY, ld_sy, fmt, out_fmt=GR_O
                               _ptr(stream))
 
 
-def gemm_w4_bt(M, N, K, A, lda, Bt, ldbt, scale_b, ld_sb, bias, act, C, ldc, fmt=GR_FMT_BF16, stream=None) -> int:
+def gemm_w4_bt_workspace_size(M, N, K):
+    """(status, bytes): the workspace with which gemm_w4_bt is fastest (0: none needed)."""
+    n = ctypes.c_int64(0)
+    st = lib().gemm_w4_bt_workspace_size(M, N, K, ctypes.byref(n))
+    return st, int(n.value)
+
+
+def gemm_w4_bt(M, N, K, A, lda, Bt, ldbt, scale_b, ld_sb, bias, act, C, ldc, fmt=GR_FMT_BF16, workspace=None,
+               workspace_bytes=0, stream=None) -> int:
     """C := act(A.Bt~^T + bias), A, bias and C in fmt, Bt in MX fp4 (N x K); returns the status code."""
     return lib().gemm_w4_bt(M, N, K, _ptr(A), lda, _ptr(Bt), ldbt, _ptr(scale_b), ld_sb, _ptr(bias), act, _ptr(C), ldc,
-                            fmt, _ptr(stream))
+                            fmt, _ptr(workspace), workspace_bytes, _ptr(stream))
 
 
 def moe_route_workspace_size(T, H, E):
@@ -250,10 +258,10 @@ def _mxfp4_weight(w, s, x, k, what):
     return n, _pitch(w, n, k // 2, what), _pitch(s, n, k // 32, what + "'s scales")
 
 
-def linear_mxfp4(x, weight, scale, bias=None, act="none", out=None, stream=None):
+def linear_mxfp4(x, weight, scale, bias=None, act="none", out=None, workspace="auto", stream=None):
     """``act(x @ W.T + bias)`` with 16-bit ``x`` (M x K) and W an N x K MX fp4
     weight (``weight`` N x K/2, ``scale`` N x K/32).  For few rows: the weight
-    is read once per 64 rows of x."""
+    is read once per 64 rows of x.  ``workspace`` as for gemm_relu."""
     fmt, M, K, ldx = _matrix(x, "x")
     N, ldw, ldsw = _mxfp4_weight(weight, scale, x, K, "weight")
     b = 0 if bias is None else _vector(bias, x, N, x.dtype, "bias")
@@ -261,8 +269,14 @@ def linear_mxfp4(x, weight, scale, bias=None, act="none", out=None, stream=None)
         out, ldc = _empty(x, (M, N), x.dtype, stream), N if N > 0 else 1
     else:
         ldc = _like(x, out, M, N, x.dtype, "out")
+    need = 0
+    if K > 2048 and M <= 64 and workspace is not None:
+        st, need = gemm_w4_bt_workspace_size(M, N, K)
+        if st != GR_OK:
+            raise GemmReluError(st, "gemm_w4_bt_workspace_size")
+    ws, ws_bytes, keep = _scratch(x, need, workspace, stream)
     _run(_l.gemm_w4_bt, x, (M, N, K, x.data_ptr(), ldx, weight.data_ptr(), ldw, scale.data_ptr(), ldsw, b, _act(act),
-                            out.data_ptr(), ldc, fmt), stream, "gemm_w4_bt")
+                            out.data_ptr(), ldc, fmt, ws, ws_bytes), stream, "gemm_w4_bt")
     return out
 
 

@@ -893,15 +893,20 @@ int gated_act_mx(int64_t M, int64_t N,
  * weights are read once per 64 rows.  Weights are widened exactly, products
  * accumulate in fp32 per block of 32 k, and the block's scale multiplies the fp32
  * sum: every scale 2^-127 .. 2^127 is exact, scale byte 255 gives NaN.  K % 32
- * != 0 is GR_ERR_INVALID_DIM; K == 0 gives act(bias).
+ * != 0 is GR_ERR_INVALID_DIM; K == 0 gives act(bias); pitches of the weights above 2^26
+ * bytes are GR_ERR_TOO_LARGE.  With a workspace of gemm_w4_bt_workspace_size bytes
+ * (256-byte aligned) a K that one workgroup cannot hold goes to several; NULL or too
+ * small: one workgroup goes over it in passes.  The size is 0 where it would not help.
  */
+int gemm_w4_bt_workspace_size(int64_t M, int64_t N, int64_t K, int64_t* bytes);
+
 int gemm_w4_bt(int64_t M, int64_t N, int64_t K,
                const uint16_t* A, int64_t lda,
                const uint8_t* Bt, int64_t ldbt,
                const uint8_t* scale_b, int64_t ld_sb,
                const uint16_t* bias, int act,
                uint16_t* C, int64_t ldc, int fmt,
-               void* stream);
+               void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
  * moe_route -- the router of a mixture-of-experts layer: logits[t][e] = sum_k

@@ -241,6 +241,39 @@ def test_linear(M, N, K, dtype):
     check_linear(M, N, K, dtype)
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 20, 8736), (16, 50, 16384), (17, 33, 4640), (32, 1040, 8192), (33, 65, 2080),
+                                   (64, 100, 6176), (64, 640, 2048), (70, 17, 4128)])
+@pytest.mark.parametrize("workspace", ["auto", None])
+def test_linear_long_k(M, N, K, workspace):
+    """A K that one workgroup cannot hold: several workgroups with a workspace, several passes without."""
+    dtype = "bf16" if M % 2 else "f16"
+    log("linear long k M=%d N=%d K=%d dtype=%s workspace=%s" % (M, N, K, dtype, workspace))
+    x = inputs(M, K, dtype, 25)
+    w, s = weights((N,), K, 26)
+    b = inputs(1, N, dtype, 27)[0]
+    out = gr.linear_mxfp4(x.cuda(), w.cuda(), s.cuda(), b.cuda(), "silu", workspace=workspace)
+    torch.cuda.synchronize()
+    ref, mag = mx_ref.linear(x, w, s, b, "silu")
+    mx_ref.check16(out.cpu(), ref, x.dtype, 1.2 * mag * mx_ref.sum_bound(K) + 8 * U * ref.abs())
+
+
+def test_linear_wide_scales_f16():
+    """fp16 rows whose scales differ by more than the conversion holds (2^13): the block by block form, beside
+    rows that do not."""
+    M, N, K = 7, 48, 1024
+    x = inputs(M, K, "f16", 28)
+    w, s = weights((N,), K, 29)
+    g = torch.Generator().manual_seed(30)
+    s[5] = torch.randint(96, 126, (K // 32,), generator=g, dtype=torch.uint8)
+    s[20, 7] = 0
+    s[21, 0] = 0
+    s[40] = torch.randint(60, 80, (K // 32,), generator=g, dtype=torch.uint8)
+    out = gr.linear_mxfp4(x.cuda(), w.cuda(), s.cuda())
+    torch.cuda.synchronize()
+    ref, mag = mx_ref.linear(x, w, s)
+    mx_ref.check16(out.cpu(), ref, x.dtype, mag * mx_ref.sum_bound(K))
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 16400, 64), (17, 16390, 32), (40, 16385, 128), (16, 20000, 256)])
 def test_linear_many_columns(M, N, K):
     check_linear(M, N, K, "bf16")
@@ -340,6 +373,27 @@ def test_route(T, H, E, k, renorm):
     e = torch.exp(top - logits.amax(-1, keepdim=True))
     total = e.sum(-1, keepdim=True) if renorm else torch.exp(logits - logits.amax(-1, keepdim=True)).sum(-1, keepdim=True)
     assert bool(((weights_ - e / total).abs() <= (e / total) * (4 * off + 64 * U)).all())
+
+
+@pytest.mark.parametrize("T,H,E,k", [(1, 4096, 64, 8), (5, 2080, 40, 3), (33, 1500, 129, 6), (2, 700, 1000, 20),
+                                     (512, 1100, 64, 2)])
+def test_route_workspace(T, H, E, k):
+    """With a workspace (two kernels) and without: both are the topk of logits within the sums' bounds."""
+    x, w = inputs(T, H, "bf16", 43), inputs(E, H, "bf16", 44, 2 * H ** -0.5)
+    st, size = gr.moe_route_workspace_size(T, H, E)
+    assert st == gr.GR_OK and size > 0
+    logits = x.double() @ w.double().T
+    off = (x.double().abs() @ w.double().abs().T * mx_ref.sum_bound(H)).max().item()
+    best = logits.sort(-1, descending=True).values[:, :k]
+    for workspace in ("auto", None):
+        log("route workspace T=%d H=%d E=%d k=%d %s" % (T, H, E, k, workspace))
+        ids, p = gr.moe_route(x.cuda(), w.cuda(), k, workspace=workspace)
+        torch.cuda.synchronize()
+        ids, p = ids.cpu().long(), p.cpu().double()
+        top = logits.gather(1, ids)
+        assert bool((top - best).abs().max() <= 2 * off) and all(len(set(r)) == k for r in ids.tolist())
+        ref = torch.softmax(top, -1)
+        assert bool(((p - ref).abs() <= ref * (4 * off + 64 * U)).all())
 
 
 def test_route_ties_and_not_finite():
