@@ -1,4 +1,5 @@
-"""Compile the HIP library for gfx950 (``libgemm_relu.so``, in this package).
+"""Compile the HIP library for gfx950 (``libgemm_relu.so``, in this package) and the
+tensor helpers on it (``_tensors.so``, host code on torch's headers).
 
 Run as ``python -m dense_gemm_epilogue_tiled_amd.build``. The library is built
 in-tree so the shared object sits next to the Python binding that loads it.
@@ -15,6 +16,8 @@ ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "gemm_relu.hip")
 UNITS = [SRC, os.path.join(HERE, "csrc", "mx_ops.hip")]
 LIB = os.path.join(HERE, "libgemm_relu.so")
+TENSORS = os.path.join(HERE, "csrc", "tensors.cpp")
+EXT = os.path.join(HERE, "_tensors.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -35,6 +38,36 @@ def sources():
     return out
 
 
+def _run(cmd, verbose, what):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("failed building %s" % what)
+
+
+def build_tensors(verbose: bool = False) -> str:
+    """Build the tensor helpers against the library."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = EXT + ".tmp%d" % os.getpid()
+    try:
+        _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+              "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+              "-I", os.path.join(root, "include"), "-I", sysconfig.get_paths()["include"],
+              "-I", os.path.join(ROOT, "include"), TENSORS, "-L", HERE, "-l:" + os.path.basename(LIB),
+              "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+              "-Wl,-rpath,$ORIGIN", "-o", tmp], verbose, EXT)
+        os.replace(tmp, EXT)
+    finally:
+        if os.path.exists(tmp):
+            os.remove(tmp)
+    return EXT
+
+
 def build(verbose: bool = False) -> str:
     tag = ".tmp%d" % os.getpid()
     objs = [os.path.splitext(u)[0] + tag + ".o" for u in UNITS]
@@ -50,18 +83,13 @@ def build(verbose: bool = False) -> str:
             if job.returncode != 0:
                 sys.stderr.write(text)
                 raise RuntimeError("hipcc failed compiling %s" % unit)
-        cmd = [HIPCC, "--offload-arch=gfx950", "-fPIC", "-shared", *objs, "-o", LIB + tag]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if res.returncode != 0:
-            sys.stderr.write(res.stdout + res.stderr)
-            raise RuntimeError("hipcc failed linking %s" % LIB)
+        _run([HIPCC, "--offload-arch=gfx950", "-fPIC", "-shared", *objs, "-o", LIB + tag], verbose, LIB)
         os.replace(LIB + tag, LIB)
     finally:
         for obj in objs:
             if os.path.exists(obj):
                 os.remove(obj)
+    build_tensors(verbose)
     return LIB
 
 
