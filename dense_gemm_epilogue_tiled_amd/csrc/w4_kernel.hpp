@@ -33,16 +33,27 @@ struct LinearUnits {
     const uint8_t *w, *s;
     int64_t K, ldw, lds, m0, k0;
     float* partial;
+    uint16_t* bias;  // LDS: the workgroup's first columns' bias, one per thread
+    int u0;
     struct Run {
         int from, end;
     };
     __device__ __forceinline__ Run run(int u) const { return {u, 0x7FFFFFFF}; }
+    __device__ __forceinline__ uint16_t early(int u0, int u1) const {
+        const int64_t col = (int64_t)u0 * 16 + threadIdx.x;
+        return a.bias != nullptr && col < (int64_t)u1 * 16 && col < a.N ? a.bias[col] : 0;
+    }
+    __device__ __forceinline__ void late(int, uint16_t v) const { bias[threadIdx.x] = v; }
     __device__ __forceinline__ const uint16_t* x(const Run&, int, int m) const {
         return m0 + m < a.M ? a.x + (m0 + m) * a.ldx + k0 : nullptr;
     }
+    __device__ __forceinline__ int rows(const Run& run, int i) const {
+        const int64_t left = a.N - (int64_t)(run.from + i) * 16;
+        return left < 16 ? (int)left : 16;
+    }
     __device__ __forceinline__ Tile tile(const Run& run, int i) const {
-        const int64_t n = (int64_t)(run.from + i) * 16, rows = a.N - n < 16 ? a.N - n : 16;
-        return {w + n * ldw, s + n * lds, (uint32_t)((rows - 1) * ldw + K / 2), (uint32_t)((rows - 1) * lds + K / 32)};
+        const int64_t n = (int64_t)(run.from + i) * 16, more = rows(run, i) - 1;
+        return {w + n * ldw, s + n * lds, (uint32_t)(more * ldw + K / 2), (uint32_t)(more * lds + K / 32)};
     }
     __device__ __forceinline__ bool wanted(const Run& run, int i, int m, int n) const {
         return m0 + m < a.M && (int64_t)(run.from + i) * 16 + n < a.N;
@@ -53,7 +64,10 @@ struct LinearUnits {
             partial[(m0 + m) * a.ldp + col] = v;
             return;
         }
-        if (a.bias != nullptr) v += E::widen(a.bias[col]);
+        if (a.bias != nullptr) {
+            const uint32_t at = (run.from - u0 + i) * 16 + n;
+            v += E::widen(at < blockDim.x ? bias[at] : a.bias[col]);
+        }
         a.c[(m0 + m) * a.ldc + col] = E::round(mx::exact_activate(v, a.act));
     }
 };
@@ -70,9 +84,11 @@ __global__ void __launch_bounds__(64 * NW, waves_per_simd(MT, 1, ST)) linear_w4_
     const int64_t units = (a.N + 15) / 16;
     const int64_t k0 = blockIdx.z * a.span, K = a.K - k0 < a.span ? a.K - k0 : a.span;
     float* const partial = a.partial != nullptr ? a.partial + blockIdx.z * a.M * a.ldp : nullptr;
-    const LinearUnits<E> p{a, a.w + k0 / 2, a.s + k0 / 32, K, a.ldw, a.lds, (int64_t)blockIdx.y * (16 * MT), k0, partial};
-    stream_units<E, 1, ST>(p, lds, (int)(units * blockIdx.x / gridDim.x), (int)(units * (blockIdx.x + 1) / gridDim.x),
-                           a.kw);
+    __shared__ uint16_t bias[64 * NW];
+    const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
+    const LinearUnits<E> p{a,     a.w + k0 / 2, a.s + k0 / 32, K, a.ldw, a.lds, (int64_t)blockIdx.y * (16 * MT), k0,
+                           partial, bias, u0};
+    stream_units<E, 1, ST>(p, lds, u0, u1, a.kw);
 }
 
 // C from the splits' sums, added in order; 4 columns per thread.
@@ -125,6 +141,7 @@ struct Routing {
     uint16_t* row;               // first pair of each; [chosen]: pairs in all
     uint16_t* row_of;            // the same by expert number
     uint16_t* tile;              // tiles of 16 pairs: slot in `expert` * 4 + tile of that expert
+    float* weight;               // a pair's weight (gate and up)
     uint8_t* token;              // a pair's token
     int tiles;
 };
@@ -132,33 +149,35 @@ struct Routing {
 // sum over the experts of ceil(pairs / 16) < experts + pairs / 16
 __host__ __device__ constexpr int max_tiles(int E, int topk) { return E + kChunk * topk / 16; }
 __host__ __device__ constexpr int routing_bytes(int E, int topk) {
-    return 8 * E + 8 + 2 * (3 * E + 2 + max_tiles(E, topk)) + kChunk * topk;
-}
-
-// The token's earlier slot with the same expert, or -1.
-__device__ __forceinline__ int earlier(const int32_t* ids, int j, int32_t e) {
-    for (int i = 0; i < j; ++i)
-        if (ids[i] == e) return i;
-    return -1;
+    return 8 * E + 8 + 3 * 4 * kChunk * topk + 2 * (3 * E + 2 + max_tiles(E, topk)) + kChunk * topk;
 }
 
 // The routing of the chunk's ids (n tokens x topk); called by the whole
 // workgroup.  Ids outside [0, E) choose nothing, and a token that names an
-// expert twice is one pair.
-__device__ __forceinline__ Routing route(const int32_t* ids, int n, int topk, int E) {
+// expert twice is one pair.  With `weights` each pair's weight is put down too, and
+// with `pair` the pair of each choice (-1: none, or named before).
+__device__ __forceinline__ Routing route(const int32_t* ids, const float* weights, int32_t* pair, int n, int topk,
+                                         int E) {
     extern __shared__ unsigned long long routing_lds[];
     Routing r;
     r.tokens = routing_lds;
     int* const tiles_of_all = reinterpret_cast<int*>(r.tokens + E);
-    r.expert = reinterpret_cast<uint16_t*>(tiles_of_all + 2);
+    r.weight = reinterpret_cast<float*>(tiles_of_all + 2);
+    int32_t* const id = reinterpret_cast<int32_t*>(r.weight + kChunk * topk);
+    float* const share = reinterpret_cast<float*>(id + kChunk * topk);
+    r.expert = reinterpret_cast<uint16_t*>(share + kChunk * topk);
     r.row = r.expert + E + 1;
     r.row_of = r.row + E + 1;
     r.tile = r.row_of + E;
     r.token = reinterpret_cast<uint8_t*>(r.tile + max_tiles(E, topk));
+    for (int i = threadIdx.x; i < n * topk; i += blockDim.x) {
+        id[i] = ids[i];
+        if (weights != nullptr) share[i] = weights[i];
+    }
     for (int e = threadIdx.x; e < E; e += blockDim.x) r.tokens[e] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < n * topk; i += blockDim.x) {
-        const uint32_t e = (uint32_t)ids[i];
+        const uint32_t e = (uint32_t)id[i];
         if (e < (uint32_t)E) atomicOr(&r.tokens[e], 1ull << (i / topk));
     }
     __syncthreads();
@@ -198,10 +217,23 @@ __device__ __forceinline__ Routing route(const int32_t* ids, int n, int topk, in
     }
     __syncthreads();
     for (int i = threadIdx.x; i < n * topk; i += blockDim.x) {
-        const uint32_t e = (uint32_t)ids[i];
-        const int t = i / topk;
-        // (tokens that name e twice write the same value)
-        if (e < (uint32_t)E) r.token[r.row_of[e] + __popcll(r.tokens[e] & ((1ull << t) - 1))] = (uint8_t)t;
+        const int32_t e = id[i];
+        const int t = i / topk, j = i % topk;
+        int row = -1;
+        if ((uint32_t)e < (uint32_t)E) {
+            row = r.row_of[e] + __popcll(r.tokens[e] & ((1ull << t) - 1));
+            float weight = 0.0f;
+            for (int q = 0; q < topk; ++q)
+                if (id[t * topk + q] == e) {
+                    if (q < j) row = -1;
+                    if (weights != nullptr) weight += share[t * topk + q];
+                }
+            if (row >= 0) {
+                r.token[row] = (uint8_t)t;
+                r.weight[row] = weight;
+            }
+        }
+        if (pair != nullptr) pair[i] = row;
     }
     r.tiles = __builtin_amdgcn_readfirstlane(*tiles_of_all);
     __syncthreads();
@@ -245,6 +277,8 @@ struct GateUpUnits {
     const Routing& r;
     int64_t K, ldw, lds, t0;
     int tiles;  // of 16 columns of h
+    __device__ __forceinline__ int early(int, int) const { return 0; }
+    __device__ __forceinline__ void late(int, int) const {}
     __device__ __forceinline__ MoeRun run(int u) const {
         MoeRun run = moe_run(r, u / 2, tiles);
         run.end *= 2;
@@ -253,6 +287,7 @@ struct GateUpUnits {
     __device__ __forceinline__ const uint16_t* x(const MoeRun& run, int, int m) const {
         return m < run.pairs ? a.x + (t0 + r.token[run.row + m]) * a.ldx : nullptr;
     }
+    __device__ __forceinline__ int rows(const MoeRun&, int) const { return 16; }  // H and I are multiples of 16
     __device__ __forceinline__ Tile tile(const MoeRun& run, int i) const {
         const int64_t n = (2 * (int64_t)run.expert + i % 2) * a.I + run.col + i / 2 * 16;
         return {a.w13 + n * ldw, a.s13 + n * lds, (uint32_t)(16 * ldw), (uint32_t)(16 * lds)};
@@ -264,11 +299,7 @@ struct GateUpUnits {
             g += E::widen(a.b13[2 * (int64_t)run.expert * a.I + col]);
             v += E::widen(a.b13[(2 * (int64_t)run.expert + 1) * a.I + col]);
         }
-        const int64_t t = t0 + r.token[run.row + m];
-        float weight = 0.0f;
-        for (int j = 0; j < a.topk; ++j)
-            if (a.ids[t * a.topk + j] == run.expert) weight += a.weights[t * a.topk + j];
-        const float h = mx::exact_activate(g, a.act) * v * weight;
+        const float h = mx::exact_activate(g, a.act) * v * r.weight[run.row + m];
         const uint16_t high = to_bf16(h);
         const int64_t to = (t0 * a.topk + run.row + m) * a.I + col;
         a.h[to] = high;
@@ -283,18 +314,9 @@ __global__ void __launch_bounds__(64 * NW, waves_per_simd(1, 1, ST)) moe_gate_up
     __shared__ Lds<NW, 1, kMoeBatch, NW == 16 ? 1 : 2, PASSES> lds;
     const int64_t t0 = (int64_t)blockIdx.y * kChunk;
     const int n_tok = (int)(a.T - t0 < kChunk ? a.T - t0 : kChunk);
-    const int32_t* const ids = a.ids + t0 * a.topk;
-    const Routing r = route(ids, n_tok, a.topk, a.E);
-    if (blockIdx.x == 0) {
-        for (int i = threadIdx.x; i < n_tok * a.topk; i += 64 * NW) {
-            const int32_t e = ids[i];
-            const int t = i / a.topk;
-            int row = -1;
-            if ((uint32_t)e < (uint32_t)a.E && earlier(ids + t * a.topk, i % a.topk, e) < 0)
-                row = r.row_of[e] + __popcll(r.tokens[e] & ((1ull << t) - 1));
-            a.pair[t0 * a.topk + i] = row;
-        }
-    }
+    const int64_t first = t0 * a.topk;
+    const Routing r =
+        route(a.ids + first, a.weights + first, blockIdx.x == 0 ? a.pair + first : nullptr, n_tok, a.topk, a.E);
     const int tiles = (int)(a.I / 16);
     const GateUpUnits<E> p{a, r, a.H, a.H / 2, a.H / 32, t0, tiles};
     const int64_t items = (int64_t)r.tiles * tiles;
@@ -309,10 +331,13 @@ struct DownUnits {
     const Routing& r;
     int64_t K, ldw, lds, first;  // first: the chunk's first row of h and y
     int tiles;                   // of 16 columns
+    __device__ __forceinline__ int early(int, int) const { return 0; }
+    __device__ __forceinline__ void late(int, int) const {}
     __device__ __forceinline__ MoeRun run(int u) const { return moe_run(r, u, tiles); }
     __device__ __forceinline__ const uint16_t* x(const MoeRun& run, int plane, int m) const {
         return m < run.pairs ? a.h + (plane * (a.T * a.topk) + first + run.row + m) * a.I : nullptr;
     }
+    __device__ __forceinline__ int rows(const MoeRun&, int) const { return 16; }  // H and I are multiples of 16
     __device__ __forceinline__ Tile tile(const MoeRun& run, int i) const {
         const int64_t n = (int64_t)run.expert * a.H + run.col + i * 16;
         return {a.w2 + n * ldw, a.s2 + n * lds, (uint32_t)(16 * ldw), (uint32_t)(16 * lds)};
@@ -328,7 +353,7 @@ __global__ void __launch_bounds__(64 * NW, waves_per_simd(1, 2, ST)) moe_down_ke
     __shared__ Lds<NW, 1, kMoeBatch, NW == 16 ? 1 : 2, PASSES> lds;
     const int64_t t0 = (int64_t)blockIdx.y * kChunk;
     const int n_tok = (int)(a.T - t0 < kChunk ? a.T - t0 : kChunk);
-    const Routing r = route(a.ids + t0 * a.topk, n_tok, a.topk, a.E);
+    const Routing r = route(a.ids + t0 * a.topk, nullptr, nullptr, n_tok, a.topk, a.E);
     const int tiles = (int)(a.H / 16);
     const DownUnits p{a, r, a.I, a.I / 2, a.I / 32, t0 * a.topk, tiles};
     const int64_t items = (int64_t)r.tiles * tiles;

@@ -17,8 +17,9 @@
 // at no cost.  In bfloat16 this is exact for scale codes 2 .. 252.  In fp16 the
 // scale is taken relative to the first one of the row in the wave's range,
 // which multiplies the fp32 sum afterwards; it is exact within 2^+-13 of that.
-// Units with other codes take multiply_any, which multiplies each block's fp32 sum by its
-// scale: exact for all codes; code 255 gives NaN.
+// A workgroup that meets other codes goes over its units again with multiply_any, which
+// multiplies each block's fp32 sum by its scale: exact for all codes; code 255 gives
+// NaN.  (In the loop itself that form cost 20 registers, which spilled.)
 #pragma once
 
 #include "common.hpp"
@@ -121,8 +122,8 @@ __device__ __forceinline__ uint32_t from_group_0(uint32_t x) {
     return __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false)[0];
 }
 
-// What multiplies a unit: the lane's scale codes, relative to ref, and whether the
-// conversion can apply them all.  The row of W whose code a lane holds is also its column
+// What multiplies a unit: the lane's scale codes, relative to ref, and whether there is
+// one among the rows that are there that the conversion cannot apply.  The row of W whose code a lane holds is also its column
 // of the result (D[i][j] of the MFMA has row i of X in lane / 16 * 4 + register and
 // row j of W in lane % 16).
 template <typename E, int ST>
@@ -131,7 +132,7 @@ struct Scales {
     uint32_t code[ST];
     bool any;
 
-    __device__ __forceinline__ Scales(const uint32_t (&c)[ST], int shift) {
+    __device__ __forceinline__ Scales(const uint32_t (&c)[ST], int shift, bool there) {
         ref = 127;
         if constexpr (E::kIsF16) {
             ref = (int)(from_group_0(c[0]) & 255u);
@@ -146,48 +147,52 @@ struct Scales {
             code[i] = (c[i] >> shift) & 255u;
             worst = code[i] - low > worst ? code[i] - low : worst;
         }
-        any = __ballot(worst > kSpan) != 0;
+        any = __ballot(there && worst > kSpan) != 0;
     }
 };
 
-// acc[mt] += the product of one step: 16 rows of W, 128 k, in units of 2^(ref - 127).
+// acc[mt] += the product of one step: 16 rows of W, 128 k, in units of 2^(ref - 127),
+// with codes that the conversion can apply.
 template <typename E, int MT, int PL, int ST>
 __device__ __forceinline__ void multiply(const u32x4& wi, const Scales<E, ST>& s, int i, const Rows<MT, PL, ST>& r,
-                                         f32x4 (&acc)[MT], int g) {
-    if (__builtin_expect(!s.any, 1)) {
-        const float scale = __builtin_bit_cast(float, (s.code[i] + (uint32_t)(127 - s.ref)) << 23);
+                                         f32x4 (&acc)[MT]) {
+    const float scale = __builtin_bit_cast(float, (s.code[i] + (uint32_t)(127 - s.ref)) << 23);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const f16x8 w = widen8<E>(wi[j], scale);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int p = 0; p < PL; ++p)
+                acc[mt] = E::mfma16(__builtin_bit_cast(f16x8, r.x[p][mt][i][j]), w, acc[mt]);
+    }
+}
+
+// The same for any codes, block by block: the groups that hold the other blocks put
+// zeros on both sides.
+template <typename E, int MT, int PL, int ST>
+__device__ __forceinline__ void multiply_any(const u32x4& wi, const Scales<E, ST>& s, int i,
+                                             const Rows<MT, PL, ST>& r, f32x4 (&acc)[MT], int g) {
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+        const bool mine = g == q;
+        const int code = __shfl((int)s.code[i], 16 * q + (int)(threadIdx.x % 16));
+        f32x4 t[MT] = {};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const f16x8 w = widen8<E>(wi[j], scale);
+            const f16x8 w = widen8<E>(mine ? wi[j] : 0u, 1.0f);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int p = 0; p < PL; ++p)
-                    acc[mt] = E::mfma16(__builtin_bit_cast(f16x8, r.x[p][mt][i][j]), w, acc[mt]);
+                    t[mt] = E::mfma16(__builtin_bit_cast(f16x8, mine ? r.x[p][mt][i][j] : zero), w, t[mt]);
         }
-    } else {
-        // block by block: the groups that hold the other blocks put zeros on both sides
-        const u32x4 zero = {0u, 0u, 0u, 0u};
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-            const bool mine = g == q;
-            const int code = __shfl((int)s.code[i], 16 * q + (int)(threadIdx.x % 16));
-            f32x4 t[MT] = {};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const f16x8 w = widen8<E>(mine ? wi[j] : 0u, 1.0f);
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int p = 0; p < PL; ++p)
-                        t[mt] = E::mfma16(__builtin_bit_cast(f16x8, mine ? r.x[p][mt][i][j] : zero), w, t[mt]);
-            }
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    acc[mt][k] += code == 255 ? __builtin_nanf("") : __builtin_amdgcn_ldexpf(t[mt][k], code - s.ref);
-        }
+            for (int k = 0; k < 4; ++k)
+                acc[mt][k] += code == 255 ? __builtin_nanf("") : __builtin_amdgcn_ldexpf(t[mt][k], code - s.ref);
     }
 }
 
@@ -206,6 +211,7 @@ template <int NW, int MT, int TB, int BUFS, bool PASSES>
 struct Lds {
     float part[BUFS][TB * MT][NW][256];
     float sum[PASSES ? kSumTiles * 256 : 1];
+    int again;  // a wave met codes that the conversion cannot apply
 };
 
 // Units [u0, u1) of policy P by one workgroup of NW waves.  kw of them share a
@@ -215,12 +221,17 @@ struct Lds {
 //   run(u)                    what the units from u on share: their X and more; run.end
 //                             is the first unit with other rows of X
 //   x(run, plane, m)          row m of X, or nullptr
-//   tile(run, i)              the rows of W and S of the run's i-th unit
+//   tile(run, i), rows(run, i)   the rows of W and S of the run's i-th unit, their number
 //   K, ldw, lds               in k and bytes
 //   kPair                     a run's units 2i and 2i + 1 are finished together
+//   early(u0, u1), late(u0, value)   a load that goes out before all others, and what is
+//                             done with its value once they are under way
 //   wanted(run, i, m, n), finish(run, i, m, n, v[, v2])   column n of unit i, row m
-template <typename E, int PL, int ST, int NW, int MT, int TB, int BUFS, bool PASSES, typename P>
-__device__ __forceinline__ void stream_units(const P& p, Lds<NW, MT, TB, BUFS, PASSES>& lds, int u0, int u1, int kw) {
+// ANY: for any scale codes; otherwise returns whether there were some that need it, in
+// which case the results are not right.
+template <bool ANY, typename E, int PL, int ST, int NW, int MT, int TB, int BUFS, bool PASSES, typename P>
+__device__ __forceinline__ bool stream_units_by(const P& p, Lds<NW, MT, TB, BUFS, PASSES>& lds, int u0, int u1,
+                                                int kw) {
     // units in flight: 4 steps where a batch has as many units
     constexpr int D = 4 / ST < TB ? 4 / ST : TB;
     static_assert(TB % D == 0, "a batch is a whole number of turns of the ring");
@@ -229,6 +240,9 @@ __device__ __forceinline__ void stream_units(const P& p, Lds<NW, MT, TB, BUFS, P
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int groups = NW / kw, group = wave / kw, part_of = wave % kw;
     const int64_t span = (int64_t)kw * (128 * ST);
+    const auto ahead = p.early(u0, u1);
+    if (!ANY && threadIdx.x == 0) lds.again = 0;
+    bool bad = false;
     int parity = 0;
     for (int64_t pass = 0; pass == 0 || (PASSES && pass * span < p.K); ++pass) {
         const int64_t k0 = pass * span + part_of * (128 * ST);
@@ -273,6 +287,7 @@ __device__ __forceinline__ void stream_units(const P& p, Lds<NW, MT, TB, BUFS, P
                     }
                 load_rows<MT, PL, ST>(rows, x, g, blocks);
             }
+            if (pass == 0 && from == u0) p.late(u0, ahead);
             for (int turn = 0; turn < turns; ++turn) {
 #pragma unroll 1
                 for (int t0 = 0; t0 < TB; t0 += D) {
@@ -284,12 +299,16 @@ __device__ __forceinline__ void stream_units(const P& p, Lds<NW, MT, TB, BUFS, P
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) acc[mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                         if (active) {
-                            const Scales<E, ST> scales(c[d], shift);
+                            const Scales<E, ST> scales(c[d], shift, r16 < p.rows(run, unit_of(turn * TB + t)));
+                            bad = bad || scales.any;
                             const Tile next = tile_of(turn * TB + t + D);
                             load_codes<ST>(c[d], buffer_of(next.s, next.s_bytes), s_at, g, blocks);
 #pragma unroll
                             for (int i = 0; i < ST; ++i) {
-                                multiply<E, MT, PL, ST>(w[d][i], scales, i, rows, acc, g);
+                                if constexpr (ANY)
+                                    multiply_any<E, MT, PL, ST>(w[d][i], scales, i, rows, acc, g);
+                                else
+                                    multiply<E, MT, PL, ST>(w[d][i], scales, i, rows, acc);
                                 w[d][i] = __builtin_amdgcn_raw_buffer_load_b128(buffer_of(next.w, next.w_bytes),
                                                                                 w_at + 64 * i, 0, 0);
                             }
@@ -306,6 +325,7 @@ __device__ __forceinline__ void stream_units(const P& p, Lds<NW, MT, TB, BUFS, P
                             *(f32x4*)&lds.part[parity][t * MT + mt][wave][lane * 4] = acc[mt];
                     }
                 }
+                if (!ANY && bad && lane == 0) lds.again = 1;
                 lds_barrier();
                 const int total = TB / kPer * groups * MT * 256;
                 // (a thread number that the compiler takes for new in each turn: what follows
@@ -352,6 +372,17 @@ __device__ __forceinline__ void stream_units(const P& p, Lds<NW, MT, TB, BUFS, P
                     lds_barrier();
             }
         }
+    }
+    if constexpr (ANY) return false;
+    // (written before the last barrier, if at all; without units there was none)
+    return u0 < u1 && lds.again != 0;
+}
+
+template <typename E, int PL, int ST, int NW, int MT, int TB, int BUFS, bool PASSES, typename P>
+__device__ __forceinline__ void stream_units(const P& p, Lds<NW, MT, TB, BUFS, PASSES>& lds, int u0, int u1, int kw) {
+    if (__builtin_expect(stream_units_by<false, E, PL, ST>(p, lds, u0, u1, kw), 0)) {
+        __syncthreads();
+        stream_units_by<true, E, PL, ST>(p, lds, u0, u1, kw);
     }
 }
 
