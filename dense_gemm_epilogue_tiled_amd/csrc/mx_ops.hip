@@ -105,7 +105,8 @@ int run_gated(const gr::mx::GatedArgs& a, int out_fmt, hipStream_t stream) {
 constexpr int64_t kW4MaxPitch = int64_t(1) << 26;
 
 int validate_w4(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* Bt, int64_t ldbt,
-                const void* SB, int64_t ld_sb, const void* bias, int act, const void* C, int64_t ldc, int fmt) {
+                const void* SB, int64_t ld_sb, const void* bias, int act, const void* C, int64_t ldc, int fmt,
+                bool with_a = true) {
     if (M < 0 || N < 0 || K < 0 || K % 32 != 0) return GR_ERR_INVALID_DIM;
     if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return GR_ERR_TOO_LARGE;
     if (lda < (K > 1 ? K : 1) || ldbt < (K > 1 ? K / 2 : 1) || ld_sb < (K > 1 ? K / 32 : 1) || ldc < (N > 1 ? N : 1))
@@ -114,7 +115,7 @@ int validate_w4(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, con
     if (ldbt > kW4MaxPitch || ld_sb > kW4MaxPitch) return GR_ERR_TOO_LARGE;
     if (!known_act(act) || !known_fmt(fmt)) return GR_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return GR_OK;
-    if (!C || (K > 0 && (!A || !Bt || !SB))) return GR_ERR_NULL_PTR;
+    if (!C || (K > 0 && ((with_a && !A) || !Bt || !SB))) return GR_ERR_NULL_PTR;
     const Region c = matrix16(C, M, N, ldc), a = matrix16(A, M, K, lda), b = matrix8(Bt, N, K / 2, ldbt),
                  s = matrix8(SB, N, K / 32, ld_sb), v = matrix16(bias, 1, N, N);
     if (c.bytes < 0 || a.bytes < 0 || b.bytes < 0 || s.bytes < 0) return GR_ERR_TOO_LARGE;
@@ -224,6 +225,83 @@ int run_w4(const gr::w4::LinearArgs& a, int64_t splits, hipStream_t stream) {
     if (a.M <= 16) return run_w4_rows<E, 1>(a, splits, stream);
     if (a.M <= 32) return run_w4_rows<E, 2>(a, splits, stream);
     return run_w4_rows<E, 4>(a, splits, stream);
+}
+
+// ---- both operands in MX fp4 -------------------------------------------------------
+
+// The streaming kernel's time goes with what a CU has to read, some 32 KB a
+// microsecond whether from L2 or farther (its L1 holds 32 KB of misses): with tiles of
+// 16 * MT rows a CU reads those rows once and takes `units` tiles of 16 rows of Bt.
+struct Fp4Plan {
+    int MT;
+    int64_t units;
+};
+
+Fp4Plan fp4_plan(int64_t M, int64_t N) {
+    Fp4Plan best{1, 0};
+    int64_t least = 0;
+    for (int MT = 1; MT <= 4; MT *= 2) {
+        const int64_t tiles = (M + 16 * MT - 1) / (16 * MT), all = (N + 15) / 16;
+        int64_t units = (tiles * all + kCus - 1) / kCus;
+        if (units > all) units = all;
+        const int64_t rounds = (tiles * ((all + units - 1) / units) + kCus - 1) / kCus, rows = rounds * (MT + units);
+        if (least == 0 || rows < least) {
+            least = rows;
+            best = {MT, units};
+        }
+    }
+    return best;
+}
+
+// Whether the streaming kernel is the faster one: always where gemm_mxfp4_bt has only its
+// guarded kernel (200x4000x2080: 11.9 against 25.1 us); against its 128 x 128
+// tiles, one per CU, where it reads less (4x4096x4096: 4.9 against 10.0 us,
+// 512x4096x4096: 29.9 against 17.7); not where those tiles fill the chip.
+bool fp4_streams(int64_t M, int64_t N, int64_t K, int64_t ldbt, int64_t ld_sb, int path) {
+    if (ldbt > kW4MaxPitch || ld_sb > kW4MaxPitch || K < 32) return false;
+    if (path == GR_PATH_TILE_EDGE) return true;
+    if ((M + 127) / 128 * ((N + 127) / 128) > kCus) return false;
+    const Fp4Plan p = fp4_plan(M, N);
+    // (2 microseconds more to start, and half of one for each unit's sums)
+    const double row = (double)K * 17 / 32 / 32768;
+    const double stream = 2.0 + 16 * (p.MT + p.units) * row + 0.5 * p.units;
+    const double tile = (M < 128 ? M + 128 : 256) * row;
+    return stream < tile;
+}
+
+template <typename E, int MT>
+int run_fp4_rows(gr::w4::Fp4Args a, int64_t units, hipStream_t stream) {
+    using namespace gr::w4;
+    const Division d = divide(a.K, 4, false);
+    a.kw = d.kw;
+    const int64_t gy = (a.M + 16 * MT - 1) / (16 * MT);
+    const int64_t all = (a.N + 15) / 16, groups = d.waves / d.kw;
+    int64_t gx = (all + units - 1) / units;
+    if (gx > (all + groups - 1) / groups) gx = (all + groups - 1) / groups;
+    const int64_t room = kSumTiles / MT;
+    if (d.passes && gx * room < all) gx = (all + room - 1) / room;
+    for (int64_t y = 0; y < gy; y += 65535) {
+        Fp4Args b = a;
+        b.x += y * 16 * MT * a.ldx;
+        b.sx += y * 16 * MT * a.ldsx;
+        b.c += y * 16 * MT * a.ldc;
+        b.M -= y * 16 * MT;
+        const dim3 grid((uint32_t)gx, (uint32_t)(gy - y < 65535 ? gy - y : 65535));
+        const int st = d.passes       ? launch_grid(fp4_stream_kernel<E, MT, 4, true>, grid, 512, stream, b)
+                       : d.steps == 4 ? launch_grid(fp4_stream_kernel<E, MT, 4, false>, grid, 512, stream, b)
+                       : d.steps == 2 ? launch_grid(fp4_stream_kernel<E, MT, 2, false>, grid, 512, stream, b)
+                                      : launch_grid(fp4_stream_kernel<E, MT, 1, false>, grid, 512, stream, b);
+        if (st != GR_OK) return st;
+    }
+    return GR_OK;
+}
+
+template <typename E>
+int run_fp4(const gr::w4::Fp4Args& a, hipStream_t stream) {
+    const Fp4Plan p = fp4_plan(a.M, a.N);
+    if (p.MT == 1) return run_fp4_rows<E, 1>(a, p.units, stream);
+    if (p.MT == 2) return run_fp4_rows<E, 2>(a, p.units, stream);
+    return run_fp4_rows<E, 4>(a, p.units, stream);
 }
 
 // ---- mixture of experts ------------------------------------------------------------
@@ -426,6 +504,29 @@ int gemm_w4_bt(int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, 
                                s.count > 1 ? static_cast<float*>(workspace) : nullptr, s.ldp, s.span};
     hipStream_t h = static_cast<hipStream_t>(stream);
     return fmt == GR_FMT_BF16 ? run_w4<gr::ElemBF16>(a, s.count, h) : run_w4<gr::ElemF16>(a, s.count, h);
+}
+
+int gemm_mxfp4_linear_bt(int64_t M, int64_t N, int64_t K, const uint8_t* A, int64_t lda, const uint8_t* scale_a,
+                         int64_t ld_sa, const uint8_t* Bt, int64_t ldbt, const uint8_t* scale_b, int64_t ld_sb,
+                         const uint16_t* bias, int act, uint16_t* C, int64_t ldc, int fmt, void* stream) {
+    gr_plan_t plan;
+    int st = gemm_mxfp4_bt_plan(M, N, K, A, lda, scale_a, ld_sa, Bt, ldbt, scale_b, ld_sb, bias, act, C, ldc, fmt, &plan);
+    if (st != GR_OK) return st;
+    if (!fp4_streams(M, N, K, ldbt, ld_sb, plan.path))
+        return gemm_mxfp4_bt(M, N, K, A, lda, scale_a, ld_sa, Bt, ldbt, scale_b, ld_sb, bias, act, C, ldc, fmt, stream);
+    st = validate_w4(M, N, K, nullptr, K > 1 ? K : 1, Bt, ldbt, scale_b, ld_sb, bias, act, C, ldc, fmt, false);
+    if (st != GR_OK) return st;
+    if (lda < (K > 1 ? K / 2 : 1) || ld_sa < (K > 1 ? K / 32 : 1)) return GR_ERR_INVALID_LD;
+    if (M == 0 || N == 0) return GR_OK;
+    if (K > 0 && (!A || !scale_a)) return GR_ERR_NULL_PTR;
+    const Region c = matrix16(C, M, N, ldc), a = matrix8(A, M, K / 2, lda), s = matrix8(scale_a, M, K / 32, ld_sa);
+    if (a.bytes < 0 || s.bytes < 0) return GR_ERR_TOO_LARGE;
+    if (overlaps(c, a) || overlaps(c, s)) return GR_ERR_ALIAS;
+    st = check_device();
+    if (st != GR_OK) return st;
+    const gr::w4::Fp4Args args{A, scale_a, Bt, scale_b, bias, C, M, N, K, lda, ld_sa, ldbt, ld_sb, ldc, act, 1};
+    hipStream_t h = static_cast<hipStream_t>(stream);
+    return fmt == GR_FMT_BF16 ? run_fp4<gr::ElemBF16>(args, h) : run_fp4<gr::ElemF16>(args, h);
 }
 
 int moe_route_workspace_size(int64_t T, int64_t H, int64_t E, int64_t* bytes) {

@@ -335,7 +335,7 @@ PyObject* gemm_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const uint16_t* bias = vector_of<uint16_t>(a[4], at_, w.rows, kind, "bias");
         const int act = (int)int_of(a[5]), path = (int)int_of(a[8]);
         uint16_t* const to = data_of<uint16_t>(c.t);
-        const int st = path < 0 ? gemm_mxfp4_bt(x.rows, w.rows, K, x.data, x.ld, x.scale, x.ld_s, w.data, w.ld, w.scale,
+        const int st = path < 0 ? gemm_mxfp4_linear_bt(x.rows, w.rows, K, x.data, x.ld, x.scale, x.ld_s, w.data, w.ld, w.scale,
                                                 w.ld_s, bias, act, to, c.ld, fmt, stream_of(a[9]))
                                 : gemm_mxfp4_bt_forced(x.rows, w.rows, K, x.data, x.ld, x.scale, x.ld_s, w.data, w.ld,
                                                        w.scale, w.ld_s, bias, act, to, c.ld, fmt, stream_of(a[9]), path);

@@ -91,6 +91,71 @@ __global__ void __launch_bounds__(64 * NW, waves_per_simd(MT, 1, ST)) linear_w4_
     stream_units<E, 1, ST>(p, lds, u0, u1, a.kw);
 }
 
+// ---- both operands in MX fp4 --------------------------------------------------------
+
+struct Fp4Args {
+    const uint8_t *x, *sx, *w, *s;
+    const uint16_t* bias;  // nullptr for none
+    uint16_t* c;
+    int64_t M, N, K, ldx, ldsx, ldw, lds, ldc;
+    int act;
+    int kw;
+};
+
+// E: the output's type.
+template <typename E>
+struct Fp4Units {
+    static constexpr bool kPair = false;
+    const Fp4Args& a;
+    int64_t K, ldw, lds, m0;
+    uint16_t* bias;  // as in LinearUnits
+    int u0;
+    struct Run {
+        int from, end;
+    };
+    __device__ __forceinline__ Run run(int u) const { return {u, 0x7FFFFFFF}; }
+    __device__ __forceinline__ uint16_t early(int u0, int u1) const {
+        const int64_t col = (int64_t)u0 * 16 + threadIdx.x;
+        return a.bias != nullptr && col < (int64_t)u1 * 16 && col < a.N ? a.bias[col] : 0;
+    }
+    __device__ __forceinline__ void late(int, uint16_t v) const { bias[threadIdx.x] = v; }
+    __device__ __forceinline__ const uint8_t* x(int m) const {
+        return m0 + m < a.M ? a.x + (m0 + m) * a.ldx : nullptr;
+    }
+    __device__ __forceinline__ const uint8_t* x_scale(int m) const { return a.sx + (m0 + m) * a.ldsx; }
+    __device__ __forceinline__ int rows(const Run& run, int i) const {
+        const int64_t left = a.N - (int64_t)(run.from + i) * 16;
+        return left < 16 ? (int)left : 16;
+    }
+    __device__ __forceinline__ Tile tile(const Run& run, int i) const {
+        const int64_t n = (int64_t)(run.from + i) * 16, more = rows(run, i) - 1;
+        return {a.w + n * ldw, a.s + n * lds, (uint32_t)(more * ldw + K / 2), (uint32_t)(more * lds + K / 32)};
+    }
+    __device__ __forceinline__ bool wanted(const Run& run, int i, int m, int n) const {
+        return m0 + m < a.M && (int64_t)(run.from + i) * 16 + n < a.N;
+    }
+    __device__ __forceinline__ void finish(const Run& run, int i, int m, int n, float v) const {
+        const int64_t col = (int64_t)(run.from + i) * 16 + n;
+        if (a.bias != nullptr) {
+            const uint32_t at = (run.from - u0 + i) * 16 + n;
+            v += E::widen(at < blockDim.x ? bias[at] : a.bias[col]);
+        }
+        a.c[(m0 + m) * a.ldc + col] = E::round(mx::exact_activate(v, a.act));
+    }
+};
+
+template <typename E, int MT, int ST, bool PASSES>
+__global__ void __launch_bounds__(512, 4) fp4_stream_kernel(Fp4Args a) {
+    // few units per barrier, so that two workgroups' sums fit in LDS
+    constexpr int TB = 4 / MT;
+    __shared__ Lds<8, MT, TB, 2, PASSES> lds;
+    __shared__ uint16_t bias[512];
+    const int64_t units = (a.N + 15) / 16;
+    const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
+    const Fp4Units<E> p{a, a.K, a.ldw, a.lds, (int64_t)blockIdx.y * (16 * MT), bias, u0};
+    stream_units<ElemFp4, 1, ST>(p, lds, u0, u1, a.kw);
+}
+
 // C from the splits' sums, added in order; 4 columns per thread.
 constexpr int kSumThreads = 256;
 

@@ -22,6 +22,8 @@
 // NaN.  (In the loop itself that form cost 20 registers, which spilled.)
 #pragma once
 
+#include <type_traits>
+
 #include "common.hpp"
 #include "norm_kernel.hpp"
 
@@ -92,16 +94,31 @@ __device__ __forceinline__ void load_codes(uint32_t (&c)[ST], __amdgpu_buffer_rs
     }
 }
 
+// X in MX fp4 itself: the scaled MFMA 16 x 16 x 128 takes both operands as they are, a
+// block and its scale per lane and operand.
+struct ElemFp4 {
+    static constexpr bool kIsF16 = false;
+};
+template <typename E>
+inline constexpr bool is_fp4 = std::is_same_v<E, ElemFp4>;
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
 // The columns of X in the wave's range, PL planes (2: a value in two parts).
-template <int MT, int PL, int ST>
+template <typename E, int MT, int PL, int ST>
 struct Rows {
     u32x4 x[PL][MT][ST][4];
+};
+template <int MT, int PL, int ST>
+struct Rows<ElemFp4, MT, PL, ST> {
+    u32x4 x[MT][ST];
+    uint32_t scale[MT];  // byte i: the code of step i
 };
 
 // x: this lane's row of each plane and tile from the range's first column on;
 // nullptr for a row that does not exist.
-template <int MT, int PL, int ST>
-__device__ __forceinline__ void load_rows(Rows<MT, PL, ST>& r, const uint16_t* const (&x)[PL][MT], int g, int blocks) {
+template <typename E, int MT, int PL, int ST>
+__device__ __forceinline__ void load_rows(Rows<E, MT, PL, ST>& r, const uint16_t* const (&x)[PL][MT], int g, int blocks) {
 #pragma unroll
     for (int p = 0; p < PL; ++p)
 #pragma unroll
@@ -114,6 +131,26 @@ __device__ __forceinline__ void load_rows(Rows<MT, PL, ST>& r, const uint16_t* c
                     r.x[p][mt][i][j] = there ? *(const u32x4_any*)(x[p][mt] + 128 * i + 32 * g + 8 * j)
                                              : u32x4{0u, 0u, 0u, 0u};
             }
+}
+
+// The same for MX fp4: x the lane's row of each tile from its range on, scale its
+// codes.  Blocks that are not there are 0 with the scale 1.
+template <int MT, int PL, int ST>
+__device__ __forceinline__ void load_rows(Rows<ElemFp4, MT, PL, ST>& r, const uint8_t* const (&x)[MT],
+                                          const uint8_t* const (&scale)[MT], int g, int blocks) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        uint32_t code[ST];
+#pragma unroll
+        for (int i = 0; i < ST; ++i) {
+            const bool there = x[mt] != nullptr && 4 * i + g < blocks;
+            r.x[mt][i] = there ? *(const u32x4_any*)(x[mt] + 64 * i + 16 * g) : u32x4{0u, 0u, 0u, 0u};
+            code[i] = there ? scale[mt][4 * i + g] : 127u;
+        }
+        r.scale[mt] = 0;
+#pragma unroll
+        for (int i = 0; i < ST; ++i) r.scale[mt] |= code[i] << (8 * i);
+    }
 }
 
 // The value that lane % 16 holds, in all four lane groups.
@@ -147,15 +184,16 @@ struct Scales {
             code[i] = (c[i] >> shift) & 255u;
             worst = code[i] - low > worst ? code[i] - low : worst;
         }
-        any = __ballot(there && worst > kSpan) != 0;
+        // (the scaled MFMA takes every code)
+        any = !is_fp4<E> && __ballot(there && worst > kSpan) != 0;
     }
 };
 
 // acc[mt] += the product of one step: 16 rows of W, 128 k, in units of 2^(ref - 127),
 // with codes that the conversion can apply.
 template <typename E, int MT, int PL, int ST>
-__device__ __forceinline__ void multiply(const u32x4& wi, const Scales<E, ST>& s, int i, const Rows<MT, PL, ST>& r,
-                                         f32x4 (&acc)[MT]) {
+__device__ __forceinline__ void multiply(const u32x4& wi, const Scales<E, ST>& s, int i,
+                                         const Rows<E, MT, PL, ST>& r, f32x4 (&acc)[MT]) {
     const float scale = __builtin_bit_cast(float, (s.code[i] + (uint32_t)(127 - s.ref)) << 23);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -168,11 +206,25 @@ __device__ __forceinline__ void multiply(const u32x4& wi, const Scales<E, ST>& s
     }
 }
 
+// (I: the step, which selects the byte of X's scales)
+template <int I, int MT, int PL, int ST>
+__device__ __forceinline__ void multiply_fp4(const u32x4& wi, const Scales<ElemFp4, ST>& s,
+                                             const Rows<ElemFp4, MT, PL, ST>& r, f32x4 (&acc)[MT]) {
+    const i32x8 w = {(int)wi[0], (int)wi[1], (int)wi[2], (int)wi[3], 0, 0, 0, 0};
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const u32x4& q = r.x[mt][I];
+        const i32x8 x = {(int)q[0], (int)q[1], (int)q[2], (int)q[3], 0, 0, 0, 0};
+        acc[mt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, w, acc[mt], 4, 4, I, (int)r.scale[mt], 0,
+                                                                   (int)s.code[I]);
+    }
+}
+
 // The same for any codes, block by block: the groups that hold the other blocks put
 // zeros on both sides.
 template <typename E, int MT, int PL, int ST>
 __device__ __forceinline__ void multiply_any(const u32x4& wi, const Scales<E, ST>& s, int i,
-                                             const Rows<MT, PL, ST>& r, f32x4 (&acc)[MT], int g) {
+                                             const Rows<E, MT, PL, ST>& r, f32x4 (&acc)[MT], int g) {
     const u32x4 zero = {0u, 0u, 0u, 0u};
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
@@ -267,7 +319,7 @@ __device__ __forceinline__ bool stream_units_by(const P& p, Lds<NW, MT, TB, BUFS
             };
             u32x4 w[D][ST];
             uint32_t c[D][ST];
-            Rows<MT, PL, ST> rows;
+            Rows<E, MT, PL, ST> rows;
             if (active) {
 #pragma unroll
                 for (int d = 0; d < D; ++d) {
@@ -277,15 +329,26 @@ __device__ __forceinline__ bool stream_units_by(const P& p, Lds<NW, MT, TB, BUFS
                     for (int i = 0; i < ST; ++i)
                         w[d][i] = __builtin_amdgcn_raw_buffer_load_b128(buffer_of(t.w, t.w_bytes), w_at + 64 * i, 0, 0);
                 }
-                const uint16_t* x[PL][MT];
-#pragma unroll
-                for (int pl = 0; pl < PL; ++pl)
+                if constexpr (is_fp4<E>) {
+                    const uint8_t *x[MT], *scale[MT];
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
-                        x[pl][mt] = p.x(run, pl, mt * 16 + r16);
-                        if (x[pl][mt] != nullptr) x[pl][mt] += k0;
+                        x[mt] = p.x(mt * 16 + r16);
+                        scale[mt] = p.x_scale(mt * 16 + r16) + k0 / 32;
+                        if (x[mt] != nullptr) x[mt] += k0 / 2;
                     }
-                load_rows<MT, PL, ST>(rows, x, g, blocks);
+                    load_rows<MT, PL, ST>(rows, x, scale, g, blocks);
+                } else {
+                    const uint16_t* x[PL][MT];
+#pragma unroll
+                    for (int pl = 0; pl < PL; ++pl)
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            x[pl][mt] = p.x(run, pl, mt * 16 + r16);
+                            if (x[pl][mt] != nullptr) x[pl][mt] += k0;
+                        }
+                    load_rows<E, MT, PL, ST>(rows, x, g, blocks);
+                }
             }
             if (pass == 0 && from == u0) p.late(u0, ahead);
             for (int turn = 0; turn < turns; ++turn) {
@@ -303,14 +366,32 @@ __device__ __forceinline__ bool stream_units_by(const P& p, Lds<NW, MT, TB, BUFS
                             bad = bad || scales.any;
                             const Tile next = tile_of(turn * TB + t + D);
                             load_codes<ST>(c[d], buffer_of(next.s, next.s_bytes), s_at, g, blocks);
-#pragma unroll
-                            for (int i = 0; i < ST; ++i) {
-                                if constexpr (ANY)
-                                    multiply_any<E, MT, PL, ST>(w[d][i], scales, i, rows, acc, g);
-                                else
-                                    multiply<E, MT, PL, ST>(w[d][i], scales, i, rows, acc);
+                            const auto more = [&](int i) {
                                 w[d][i] = __builtin_amdgcn_raw_buffer_load_b128(buffer_of(next.w, next.w_bytes),
                                                                                 w_at + 64 * i, 0, 0);
+                            };
+                            if constexpr (is_fp4<E>) {
+                                multiply_fp4<0, MT, PL, ST>(w[d][0], scales, rows, acc);
+                                more(0);
+                                if constexpr (ST > 1) {
+                                    multiply_fp4<1, MT, PL, ST>(w[d][1], scales, rows, acc);
+                                    more(1);
+                                }
+                                if constexpr (ST > 2) {
+                                    multiply_fp4<2, MT, PL, ST>(w[d][2], scales, rows, acc);
+                                    more(2);
+                                    multiply_fp4<3, MT, PL, ST>(w[d][3], scales, rows, acc);
+                                    more(3);
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < ST; ++i) {
+                                    if constexpr (ANY)
+                                        multiply_any<E, MT, PL, ST>(w[d][i], scales, i, rows, acc, g);
+                                    else
+                                        multiply<E, MT, PL, ST>(w[d][i], scales, i, rows, acc);
+                                    more(i);
+                                }
                             }
                             if constexpr (E::kIsF16) {
 #pragma unroll
@@ -380,9 +461,12 @@ __device__ __forceinline__ bool stream_units_by(const P& p, Lds<NW, MT, TB, BUFS
 
 template <typename E, int PL, int ST, int NW, int MT, int TB, int BUFS, bool PASSES, typename P>
 __device__ __forceinline__ void stream_units(const P& p, Lds<NW, MT, TB, BUFS, PASSES>& lds, int u0, int u1, int kw) {
-    if (__builtin_expect(stream_units_by<false, E, PL, ST>(p, lds, u0, u1, kw), 0)) {
-        __syncthreads();
-        stream_units_by<true, E, PL, ST>(p, lds, u0, u1, kw);
+    const bool again = stream_units_by<false, E, PL, ST>(p, lds, u0, u1, kw);
+    if constexpr (!is_fp4<E>) {
+        if (__builtin_expect(again, 0)) {
+            __syncthreads();
+            stream_units_by<true, E, PL, ST>(p, lds, u0, u1, kw);
+        }
     }
 }
 

@@ -909,6 +909,19 @@ int gemm_w4_bt(int64_t M, int64_t N, int64_t K,
                void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
+ * gemm_mxfp4_linear_bt -- gemm_mxfp4_bt for a layer's activations and weights of any
+ * shape and alignment: the faster of gemm_mxfp4_bt's kernels and a kernel that streams
+ * Bt past up to 64 rows of A held in registers, which has no tile to fill (few
+ * rows, few tiles, K not a multiple of 128).  The same values up to the order of
+ * the fp32 sums; arguments and errors as for gemm_mxfp4_bt.
+ */
+int gemm_mxfp4_linear_bt(int64_t M, int64_t N, int64_t K,
+                         const uint8_t* A, int64_t lda, const uint8_t* scale_a, int64_t ld_sa,
+                         const uint8_t* Bt, int64_t ldbt, const uint8_t* scale_b, int64_t ld_sb,
+                         const uint16_t* bias, int act, uint16_t* C, int64_t ldc, int fmt,
+                         void* stream);
+
+/*
  * moe_route -- the router of a mixture-of-experts layer: logits[t][e] = sum_k
  * X[t][k] * Wr[e][k] + bias[e] in fp32, the topk largest of each token in
  * descending order (equal logits: the lower index first; NaN counts as the

@@ -350,6 +350,66 @@ def test_quantised_product():
     mx_ref.check16(out.cpu(), a @ b.T, torch.bfloat16, (a.abs() @ b.abs().T) * 2.0 ** -16)
 
 
+def check_fp4(M, N, K, dtype="bf16", act="none", bias=False, low=118, high=124, seed=90, **kw):
+    log("fp4 x fp4 M=%d N=%d K=%d dtype=%s act=%s bias=%s scales=%d..%d" % (M, N, K, dtype, act, bias, low, high - 1))
+    (qa, sa), (qb, sb) = weights((M,), K, seed, low, high), weights((N,), K, seed + 1, 250 - high, 250 - low)
+    b = inputs(1, N, dtype, seed + 2)[0] if bias else None
+    out = gr.gemm_mxfp4(qa.cuda(), sa.cuda(), qb.cuda(), sb.cuda(), b.cuda() if bias else None, act,
+                        mx_ref.TYPES[dtype], **kw)
+    torch.cuda.synchronize()
+    a, w = mx_ref.weight(qa, sa), mx_ref.weight(qb, sb)
+    v, mag = a @ w.T, a.abs() @ w.abs().T
+    if bias:
+        v, mag = v + b.double(), mag + b.double().abs()
+    # the matrix cores' own sums, as the MX fp4 tests allow; 1.2: the steepest activation
+    ref = mx_ref.act(v, act)
+    mx_ref.check16(out.cpu(), ref, mx_ref.TYPES[dtype], 1.2 * mag * (2.0 ** -16 + mx_ref.sum_bound(K)) + 8 * U * ref.abs())
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1, 32), (2, 17, 64), (16, 16, 96), (5, 40, 128), (17, 33, 160), (64, 48, 480),
+                                   (65, 50, 512), (100, 130, 1056), (1, 1000, 2080), (200, 100, 4096), (3, 40, 4128),
+                                   (33, 70, 8224), (130, 600, 1024)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_fp4_product(M, N, K, dtype):
+    check_fp4(M, N, K, dtype)
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu", "sigmoid", "tanh"])
+def test_fp4_product_epilogue(act):
+    check_fp4(21, 37, 352, "f16", act, True)
+    check_fp4(3, 70, 4160, "bf16", act, True)
+
+
+def test_fp4_product_scale_extremes():
+    check_fp4(5, 20, 256, low=0, high=2)
+    check_fp4(18, 20, 256, low=248, high=250)
+
+
+def test_fp4_product_nan_scales():
+    """Scale code 255 on either side makes its row or column NaN and nothing else."""
+    (qa, sa), (qb, sb) = weights((20,), 160, 93), weights((24,), 160, 94)
+    sa[3, 4] = sb[5, 0] = 255
+    out = gr.gemm_mxfp4(qa.cuda(), sa.cuda(), qb.cuda(), sb.cuda(), act="none").cpu()
+    bad = torch.zeros(20, 24, dtype=torch.bool)
+    bad[3] = bad[:, 5] = True
+    assert torch.equal(out.isnan(), bad)
+
+
+def test_fp4_product_pitches():
+    """Padded rows at odd addresses, nothing outside the output written."""
+    M, N, K = 19, 45, 288
+    (qa, sa), (qb, sb) = weights((M,), K, 95), weights((N,), K, 96)
+    views = [padded(t, t.shape[1] + p, o, fill=0xFF)[1] for t, p, o in ((qa, 5, 3), (sa, 1, 1), (qb, 3, 1), (sb, 2, 3))]
+    bc, vc = padded(torch.zeros(M, N, dtype=torch.bfloat16), N + 3, 1)
+    before = bc.clone()
+    gr.gemm_mxfp4(*views, act="none", out=vc)
+    torch.cuda.synchronize()
+    a, w = mx_ref.weight(qa, sa), mx_ref.weight(qb, sb)
+    mx_ref.check16(vc.cpu(), a @ w.T, torch.bfloat16, (a.abs() @ w.abs().T) * (2.0 ** -16 + mx_ref.sum_bound(K)))
+    vc.copy_(torch.zeros(M, N, dtype=torch.bfloat16))
+    assert torch.equal(bc.view(torch.int16), before.view(torch.int16)), "padding was written"
+
+
 # ---- mixture of experts -------------------------------------------------------------------
 
 @pytest.mark.parametrize("T,H,E,k", [(1, 64, 4, 1), (3, 96, 8, 8), (16, 100, 17, 3), (17, 1000, 64, 8), (5, 33, 65, 4),
