@@ -262,10 +262,10 @@ bool fp4_streams(int64_t M, int64_t N, int64_t K, int64_t ldbt, int64_t ld_sb, i
     if (path == GR_PATH_TILE_EDGE) return true;
     if ((M + 127) / 128 * ((N + 127) / 128) > kCus) return false;
     const Fp4Plan p = fp4_plan(M, N);
-    // (2 microseconds more to start, and half of one for each unit's sums)
-    const double row = (double)K * 17 / 32 / 32768;
-    const double stream = 2.0 + 16 * (p.MT + p.units) * row + 0.5 * p.units;
-    const double tile = (M < 128 ? M + 128 : 256) * row;
+    // (fitted: microseconds to start, KB per microsecond, and the sums of a unit)
+    const double row = (double)K * 17 / 32 / 1024;  // KB
+    const double stream = 1.5 + 16 * (p.MT + p.units) * row / 26 + (0.4 + 0.27 * p.MT) * p.units;
+    const double tile = 4.5 + (M < 128 ? M + 128 : 256) * row / 42;
     return stream < tile;
 }
 

@@ -25,6 +25,24 @@ struct LinearArgs {
     int64_t span;    // k of one split, a multiple of 128
 };
 
+// The bias of a column: from LDS if it is among the workgroup's first ones.
+template <typename E, typename Args>
+__device__ __forceinline__ float staged_bias(const Args& a, const uint16_t* staged, uint32_t at, int64_t col) {
+    return a.bias == nullptr ? 0.0f : E::widen(at < blockDim.x ? staged[at] : a.bias[col]);
+}
+
+// Rows of one column, `rows` of them there.
+template <typename E, typename Args, int R>
+__device__ __forceinline__ void write_rows(const Args& a, uint16_t* to, int64_t rows, float bias, Column<R> v) {
+    act::dispatch(a.act, [&](auto tag) {
+#pragma unroll
+        for (int j = 0; j < R; ++j) v.v[j] = mx::exact_act<decltype(tag)::value>(v.v[j] + bias);
+    });
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+        if (j < rows) to[j * a.ldc] = E::round(v.v[j]);
+}
+
 // 16 * MT rows of X from m0 on, and the k of one split.
 template <typename E>
 struct LinearUnits {
@@ -58,17 +76,17 @@ struct LinearUnits {
     __device__ __forceinline__ bool wanted(const Run& run, int i, int m, int n) const {
         return m0 + m < a.M && (int64_t)(run.from + i) * 16 + n < a.N;
     }
-    __device__ __forceinline__ void finish(const Run& run, int i, int m, int n, float v) const {
-        const int64_t col = (int64_t)(run.from + i) * 16 + n;
+    template <int R>
+    __device__ __forceinline__ void finish(const Run& run, int i, int m, int n, const Column<R>& v) const {
+        const int64_t col = (int64_t)(run.from + i) * 16 + n, rows = a.M - (m0 + m);
         if (partial != nullptr) {
-            partial[(m0 + m) * a.ldp + col] = v;
+            float* const to = partial + (m0 + m) * a.ldp + col;
+#pragma unroll
+            for (int j = 0; j < R; ++j)
+                if (j < rows) to[j * a.ldp] = v.v[j];
             return;
         }
-        if (a.bias != nullptr) {
-            const uint32_t at = (run.from - u0 + i) * 16 + n;
-            v += E::widen(at < blockDim.x ? bias[at] : a.bias[col]);
-        }
-        a.c[(m0 + m) * a.ldc + col] = E::round(mx::exact_activate(v, a.act));
+        write_rows<E>(a, a.c + (m0 + m) * a.ldc + col, rows, staged_bias<E>(a, bias, (run.from - u0 + i) * 16 + n, col), v);
     }
 };
 
@@ -134,13 +152,11 @@ struct Fp4Units {
     __device__ __forceinline__ bool wanted(const Run& run, int i, int m, int n) const {
         return m0 + m < a.M && (int64_t)(run.from + i) * 16 + n < a.N;
     }
-    __device__ __forceinline__ void finish(const Run& run, int i, int m, int n, float v) const {
+    template <int R>
+    __device__ __forceinline__ void finish(const Run& run, int i, int m, int n, const Column<R>& v) const {
         const int64_t col = (int64_t)(run.from + i) * 16 + n;
-        if (a.bias != nullptr) {
-            const uint32_t at = (run.from - u0 + i) * 16 + n;
-            v += E::widen(at < blockDim.x ? bias[at] : a.bias[col]);
-        }
-        a.c[(m0 + m) * a.ldc + col] = E::round(mx::exact_activate(v, a.act));
+        write_rows<E>(a, a.c + (m0 + m) * a.ldc + col, a.M - (m0 + m),
+                      staged_bias<E>(a, bias, (run.from - u0 + i) * 16 + n, col), v);
     }
 };
 
@@ -358,8 +374,10 @@ struct GateUpUnits {
         return {a.w13 + n * ldw, a.s13 + n * lds, (uint32_t)(16 * ldw), (uint32_t)(16 * lds)};
     }
     __device__ __forceinline__ bool wanted(const MoeRun& run, int, int m, int) const { return m < run.pairs; }
-    __device__ __forceinline__ void finish(const MoeRun& run, int i, int m, int n, float g, float v) const {
+    __device__ __forceinline__ void finish(const MoeRun& run, int i, int m, int n, const Column<1>& gate,
+                                           const Column<1>& up) const {
         const int64_t col = run.col + i / 2 * 16 + n;
+        float g = gate.v[0], v = up.v[0];
         if (a.b13 != nullptr) {
             g += E::widen(a.b13[2 * (int64_t)run.expert * a.I + col]);
             v += E::widen(a.b13[(2 * (int64_t)run.expert + 1) * a.I + col]);
@@ -408,8 +426,8 @@ struct DownUnits {
         return {a.w2 + n * ldw, a.s2 + n * lds, (uint32_t)(16 * ldw), (uint32_t)(16 * lds)};
     }
     __device__ __forceinline__ bool wanted(const MoeRun& run, int, int m, int) const { return m < run.pairs; }
-    __device__ __forceinline__ void finish(const MoeRun& run, int i, int m, int n, float v) const {
-        a.y[(first + run.row + m) * a.H + run.col + i * 16 + n] = v;
+    __device__ __forceinline__ void finish(const MoeRun& run, int i, int m, int n, const Column<1>& v) const {
+        a.y[(first + run.row + m) * a.H + run.col + i * 16 + n] = v.v[0];
     }
 };
 

@@ -266,6 +266,15 @@ struct Lds {
     int again;  // a wave met codes that the conversion cannot apply
 };
 
+// A few rows of one column of a result.  One per thread for 16 rows of X: more would
+// take registers that X has, and leave threads idle; four for more rows, in a
+// quarter of the instructions (64x8192x8192: 31 -> 27 us).
+template <int R>
+struct Column {
+    float v[R];
+};
+constexpr int rows_at_once(int MT) { return MT == 1 ? 1 : 4; }
+
 // Units [u0, u1) of policy P by one workgroup of NW waves.  kw of them share a
 // unit's K, 128 * ST each; with PASSES the X of the next kw * 128 * ST k is loaded
 // and the units are gone through again, at most kSumTiles / MT of them.
@@ -278,7 +287,7 @@ struct Lds {
 //   kPair                     a run's units 2i and 2i + 1 are finished together
 //   early(u0, u1), late(u0, value)   a load that goes out before all others, and what is
 //                             done with its value once they are under way
-//   wanted(run, i, m, n), finish(run, i, m, n, v[, v2])   column n of unit i, row m
+//   wanted(run, i, m, n), finish(run, i, m, n, v[, v2])   column n of unit i, rows m ..
 // ANY: for any scale codes; otherwise returns whether there were some that need it, in
 // which case the results are not right.
 template <bool ANY, typename E, int PL, int ST, int NW, int MT, int TB, int BUFS, bool PASSES, typename P>
@@ -408,36 +417,43 @@ __device__ __forceinline__ bool stream_units_by(const P& p, Lds<NW, MT, TB, BUFS
                 }
                 if (!ANY && bad && lane == 0) lds.again = 1;
                 lds_barrier();
-                const int total = TB / kPer * groups * MT * 256;
+                constexpr int R = rows_at_once(MT);
+                const int total = TB / kPer * groups * MT * (256 / R);
                 // (a thread number that the compiler takes for new in each turn: what follows
                 // from it is not kept in registers through the loop above)
                 int first = threadIdx.x;
                 asm volatile("" : "+v"(first));
                 for (int at = first; at < total; at += 64 * NW) {
-                    const int e = at % 256, q = at / 256, mt = q % MT, t = q / MT % (TB / kPer);
+                    // R rows of one column of one unit: register e % 4 of lane e / 4
+                    const int e = at % (256 / R) * R, q = at / (256 / R), mt = q % MT, t = q / MT % (TB / kPer);
                     const int m = mt * 16 + e / 64 * 4 + e % 4, n = e / 4 % 16, gi = q / MT / (TB / kPer);
                     const int u = ((turn * (TB / kPer) + t) * groups + gi) * kPer;
                     if (u < units && p.wanted(run, u, m, n)) {
-                        float v[kPer];
+                        typedef float Floats __attribute__((ext_vector_type(R)));
+                        Column<R> v[kPer];
 #pragma unroll
                         for (int h = 0; h < kPer; ++h) {
                             const auto& part = lds.part[parity][(t * kPer + h) * MT + mt];
-                            v[h] = part[gi * kw][e];
+                            const auto of = [&](int i) { return *(const Floats*)&part[gi * kw + i][e]; };
+                            Floats x = of(0);
                             if (kw >= 4) {
+                                const Floats b = of(1), y = of(2), z = of(3);
+                                x = x + b + y + z;
 #pragma unroll 1
-                                for (int i = 0; i < kw; i += 4) {
-                                    const float a = part[gi * kw + i][e], b = part[gi * kw + i + 1][e],
-                                                y = part[gi * kw + i + 2][e], z = part[gi * kw + i + 3][e];
-                                    v[h] = (i == 0 ? a : v[h] + a) + b + y + z;
+                                for (int i = 4; i < kw; i += 4) {
+                                    const Floats a = of(i), b = of(i + 1), y = of(i + 2), z = of(i + 3);
+                                    x = x + a + b + y + z;
                                 }
                             } else if (kw == 2) {
-                                v[h] += part[gi * kw + 1][e];
+                                x = x + of(1);
                             }
                             if constexpr (PASSES) {
-                                float& sum = lds.sum[((from - u0 + u + h) * MT + mt) * 256 + e];
-                                if (pass > 0) v[h] += sum;
-                                if (!last_pass) sum = v[h];
+                                Floats& sum = *(Floats*)&lds.sum[((from - u0 + u + h) * MT + mt) * 256 + e];
+                                if (pass > 0) x = x + sum;
+                                if (!last_pass) sum = x;
                             }
+#pragma unroll
+                            for (int j = 0; j < R; ++j) v[h].v[j] = x[j];
                         }
                         if (last_pass) {
                             if constexpr (P::kPair)
