@@ -34,10 +34,21 @@ typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 typedef uint32_t u32_any __attribute__((aligned(1)));
 
-// 8 consecutive 16-bit values; only the first n (1 to 8) are read, the others are 0.
-__device__ __forceinline__ u32x4 load8(const uint16_t* p, int n) {
+// 8 consecutive 16-bit values; only the first n (1 to 8) are used, the others are 0.
+// Where `before` says that there are 8 - n more in front of p in the same row, those are
+// read along in one load and shifted out (their values do not matter: another
+// thread may be writing them); else one by one.
+__device__ __forceinline__ u32x4 load8(const uint16_t* p, int n, bool before = false) {
     if (n >= 8) return *(const u32x4_any*)p;
     u32x4 v = {0u, 0u, 0u, 0u};
+    if (before) {
+        v = *(const u32x4_any*)(p - (8 - n));
+        const int shift = 16 * (8 - n);  // 16 .. 112 bits
+        const uint64_t low = v[0] | (uint64_t)v[1] << 32, high = v[2] | (uint64_t)v[3] << 32;
+        const uint64_t l = shift < 64 ? low >> shift | high << (64 - shift) : high >> (shift - 64);
+        const uint64_t h = shift < 64 ? high >> shift : 0;
+        return u32x4{(uint32_t)l, (uint32_t)(l >> 32), (uint32_t)h, (uint32_t)(h >> 32)};
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (i < n) v[i / 2] |= (uint32_t)p[i] << (16 * (i % 2));
@@ -217,14 +228,14 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_kernel(NormArg
         const int64_t at = t + (int64_t)c * TPR;
         const int64_t left = a.N - at * 8;
         n[c] = at < chunks ? (left < 8 ? (int)left : 8) : 0;
-        s[c] = n[c] > 0 ? load8(x + at * 8, n[c]) : u32x4{0u, 0u, 0u, 0u};
+        s[c] = n[c] > 0 ? load8(x + at * 8, n[c], at > 0) : u32x4{0u, 0u, 0u, 0u};
     }
     if (a.r != nullptr) {
         const uint16_t* const r = a.r + row * a.ldr;
         u32x4 b[C];
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            b[c] = n[c] > 0 ? load8(r + (t + (int64_t)c * TPR) * 8, n[c]) : u32x4{0u, 0u, 0u, 0u};
+            b[c] = n[c] > 0 ? load8(r + (t + (int64_t)c * TPR) * 8, n[c], a.N > 8) : u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
         for (int c = 0; c < C; ++c) s[c] = add8<E>(s[c], b[c]);
     }
@@ -232,7 +243,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_kernel(NormArg
     if (a.w != nullptr) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            w[c] = n[c] > 0 ? load8(a.w + (t + (int64_t)c * TPR) * 8, n[c]) : u32x4{0u, 0u, 0u, 0u};
+            w[c] = n[c] > 0 ? load8(a.w + (t + (int64_t)c * TPR) * 8, n[c], a.N > 8) : u32x4{0u, 0u, 0u, 0u};
     }
     float sum = 0.0f;
 #pragma unroll
@@ -272,8 +283,8 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(NormArgs a) {
     float sum = 0.0f;
     for (int64_t at = threadIdx.x; at < chunks; at += 1024) {
         const int n = a.N - at * 8 < 8 ? (int)(a.N - at * 8) : 8;
-        u32x4 s = load8(x + at * 8, n);
-        if (r != nullptr) s = add8<E>(s, load8(r + at * 8, n));
+        u32x4 s = load8(x + at * 8, n, at > 0);
+        if (r != nullptr) s = add8<E>(s, load8(r + at * 8, n, at > 0));
         if (a.s != nullptr) store8(a.s + row * a.lds + at * 8, s, n);
         float part = 0.0f;
 #pragma unroll
@@ -290,14 +301,14 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(NormArgs a) {
         if (a.s != nullptr) {
             s = load8(a.s + row * a.lds + at * 8, n);
         } else {
-            s = load8(x + at * 8, n);
-            if (r != nullptr) s = add8<E>(s, load8(r + at * 8, n));
+            s = load8(x + at * 8, n, at > 0);
+            if (r != nullptr) s = add8<E>(s, load8(r + at * 8, n, at > 0));
         }
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = value_of<E>(s, i) * scale;
         if (a.w != nullptr) {
-            const u32x4 w = load8(a.w + at * 8, n);
+            const u32x4 w = load8(a.w + at * 8, n, at > 0);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] *= value_of<E>(w, i);
         }
@@ -363,31 +374,28 @@ struct GatedArgs {
     int act;
 };
 
-constexpr int kGatedThreads = 256;
-constexpr int kGatedChunks = 2;  // 16-byte loads of each input in flight per thread
-
-// A workgroup handles kGatedThreads * kGatedChunks chunks of one row, and rows
-// blockIdx.y, blockIdx.y + gridDim.y, ...; rows without padding come as one
-// long row.
-template <typename E, int OUT>
-__global__ void __launch_bounds__(kGatedThreads) gated_act_kernel(GatedArgs a) {
+// A workgroup of THREADS handles THREADS * CHUNKS chunks of one row (CHUNKS 16-byte
+// loads of each input in flight per thread), and rows blockIdx.y, blockIdx.y +
+// gridDim.y, ...; rows without padding come as one long row.
+template <typename E, int OUT, int THREADS, int CHUNKS>
+__global__ void __launch_bounds__(THREADS) gated_act_kernel(GatedArgs a) {
     const int64_t chunks = (a.N + 7) / 8;
-    const int64_t first = (int64_t)blockIdx.x * (kGatedThreads * kGatedChunks) + threadIdx.x;
+    const int64_t first = (int64_t)blockIdx.x * (THREADS * CHUNKS) + threadIdx.x;
     for (int64_t row = blockIdx.y; row < a.M; row += gridDim.y) {
-        u32x4 g[kGatedChunks], u[kGatedChunks];
-        int n[kGatedChunks];
+        u32x4 g[CHUNKS], u[CHUNKS];
+        int n[CHUNKS];
 #pragma unroll
-        for (int c = 0; c < kGatedChunks; ++c) {
-            const int64_t at = first + c * kGatedThreads;
+        for (int c = 0; c < CHUNKS; ++c) {
+            const int64_t at = first + c * THREADS;
             const int64_t left = a.N - at * 8;
             n[c] = at < chunks ? (left < 8 ? (int)left : 8) : 0;
             if (n[c] > 0) {
-                g[c] = load8(a.g + row * a.ldg + at * 8, n[c]);
-                if (a.u != nullptr) u[c] = load8(a.u + row * a.ldu + at * 8, n[c]);
+                g[c] = load8(a.g + row * a.ldg + at * 8, n[c], at > 0);
+                if (a.u != nullptr) u[c] = load8(a.u + row * a.ldu + at * 8, n[c], at > 0);
             }
         }
 #pragma unroll
-        for (int c = 0; c < kGatedChunks; ++c) {
+        for (int c = 0; c < CHUNKS; ++c) {
             if (n[c] > 0) {
                 float v[8];
                 act::dispatch(a.act, [&](auto tag) {
@@ -398,7 +406,7 @@ __global__ void __launch_bounds__(kGatedThreads) gated_act_kernel(GatedArgs a) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[i] *= value_of<E>(u[c], i);
                 }
-                emit<E, OUT>(v, a.y + row * a.ldy_bytes, a.e + row * a.lde, first + c * kGatedThreads, n[c]);
+                emit<E, OUT>(v, a.y + row * a.ldy_bytes, a.e + row * a.lde, first + c * THREADS, n[c]);
             }
         }
     }
