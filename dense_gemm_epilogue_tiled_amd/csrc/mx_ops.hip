@@ -369,6 +369,16 @@ int run_moe(gr::w4::MoeArgs a, hipStream_t stream) {
                  : d13.steps == 2  ? launch_lds(moe_gate_up_kernel<E, 8, 2, false>, g13, 512, lds, stream, a)
                                    : launch_lds(moe_gate_up_kernel<E, 8, 1, false>, g13, 512, lds, stream, a);
         if (st != GR_OK) return st;
+        // few tokens and experts: the sum over the experts within the product, in two passes
+        // at most (a third costs what the kernel that it saves does)
+        const int64_t parts = tiles * ((a.I + 128 * kFewSteps - 1) / (128 * kFewSteps));
+        if (a.T <= kFewTokens && parts <= 32) {
+            const int64_t units = a.H / 16, room = kSumTiles;
+            int64_t grid = units < kCus ? units : kCus;
+            if (parts > 16 && grid * room < units) grid = (units + room - 1) / room;
+            return parts > 16 ? launch_lds(moe_down_few_kernel<E, true>, dim3((uint32_t)grid), 1024, lds, stream, a)
+                              : launch_lds(moe_down_few_kernel<E, false>, dim3((uint32_t)grid), 1024, lds, stream, a);
+        }
         st = d2.passes        ? launch_lds(moe_down_kernel<16, 2, true>, g2, 1024, lds, stream, a)
              : d2.waves == 16 ? launch_lds(moe_down_kernel<16, 2, false>, g2, 1024, lds, stream, a)
              : d2.steps == 2  ? launch_lds(moe_down_kernel<8, 2, false>, g2, 512, lds, stream, a)

@@ -62,16 +62,17 @@ struct LinearUnits {
         return a.bias != nullptr && col < (int64_t)u1 * 16 && col < a.N ? a.bias[col] : 0;
     }
     __device__ __forceinline__ void late(int, uint16_t v) const { bias[threadIdx.x] = v; }
-    __device__ __forceinline__ const uint16_t* x(const Run&, int, int m) const {
-        return m0 + m < a.M ? a.x + (m0 + m) * a.ldx + k0 : nullptr;
+    __device__ __forceinline__ Range range(int64_t k) const { return {k, K - k}; }
+    __device__ __forceinline__ const uint16_t* x(const Run&, int, int m, const Range& range) const {
+        return m0 + m < a.M ? a.x + (m0 + m) * a.ldx + k0 + range.k : nullptr;
     }
     __device__ __forceinline__ int rows(const Run& run, int i) const {
         const int64_t left = a.N - (int64_t)(run.from + i) * 16;
         return left < 16 ? (int)left : 16;
     }
-    __device__ __forceinline__ Tile tile(const Run& run, int i) const {
-        const int64_t n = (int64_t)(run.from + i) * 16, more = rows(run, i) - 1;
-        return {w + n * ldw, s + n * lds, (uint32_t)(more * ldw + K / 2), (uint32_t)(more * lds + K / 32)};
+    __device__ __forceinline__ Tile tile(const Run& run, int i, const Range& range) const {
+        const int64_t n = (int64_t)(run.from + i) * 16;
+        return tile_at(w + n * ldw, ldw, s + n * lds, lds, rows(run, i), K, range.k);
     }
     __device__ __forceinline__ bool wanted(const Run& run, int i, int m, int n) const {
         return m0 + m < a.M && (int64_t)(run.from + i) * 16 + n < a.N;
@@ -137,17 +138,20 @@ struct Fp4Units {
         return a.bias != nullptr && col < (int64_t)u1 * 16 && col < a.N ? a.bias[col] : 0;
     }
     __device__ __forceinline__ void late(int, uint16_t v) const { bias[threadIdx.x] = v; }
-    __device__ __forceinline__ const uint8_t* x(int m) const {
-        return m0 + m < a.M ? a.x + (m0 + m) * a.ldx : nullptr;
+    __device__ __forceinline__ Range range(int64_t k) const { return {k, K - k}; }
+    __device__ __forceinline__ const uint8_t* x(int m, const Range& range) const {
+        return m0 + m < a.M ? a.x + (m0 + m) * a.ldx + range.k / 2 : nullptr;
     }
-    __device__ __forceinline__ const uint8_t* x_scale(int m) const { return a.sx + (m0 + m) * a.ldsx; }
+    __device__ __forceinline__ const uint8_t* x_scale(int m, const Range& range) const {
+        return a.sx + (m0 + m) * a.ldsx + range.k / 32;
+    }
     __device__ __forceinline__ int rows(const Run& run, int i) const {
         const int64_t left = a.N - (int64_t)(run.from + i) * 16;
         return left < 16 ? (int)left : 16;
     }
-    __device__ __forceinline__ Tile tile(const Run& run, int i) const {
-        const int64_t n = (int64_t)(run.from + i) * 16, more = rows(run, i) - 1;
-        return {a.w + n * ldw, a.s + n * lds, (uint32_t)(more * ldw + K / 2), (uint32_t)(more * lds + K / 32)};
+    __device__ __forceinline__ Tile tile(const Run& run, int i, const Range& range) const {
+        const int64_t n = (int64_t)(run.from + i) * 16;
+        return tile_at(a.w + n * ldw, ldw, a.s + n * lds, lds, rows(run, i), K, range.k);
     }
     __device__ __forceinline__ bool wanted(const Run& run, int i, int m, int n) const {
         return m0 + m < a.M && (int64_t)(run.from + i) * 16 + n < a.N;
@@ -365,13 +369,14 @@ struct GateUpUnits {
         run.end *= 2;
         return run;
     }
-    __device__ __forceinline__ const uint16_t* x(const MoeRun& run, int, int m) const {
-        return m < run.pairs ? a.x + (t0 + r.token[run.row + m]) * a.ldx : nullptr;
+    __device__ __forceinline__ Range range(int64_t k) const { return {k, K - k}; }
+    __device__ __forceinline__ const uint16_t* x(const MoeRun& run, int, int m, const Range& range) const {
+        return m < run.pairs ? a.x + (t0 + r.token[run.row + m]) * a.ldx + range.k : nullptr;
     }
     __device__ __forceinline__ int rows(const MoeRun&, int) const { return 16; }  // H and I are multiples of 16
-    __device__ __forceinline__ Tile tile(const MoeRun& run, int i) const {
+    __device__ __forceinline__ Tile tile(const MoeRun& run, int i, const Range& range) const {
         const int64_t n = (2 * (int64_t)run.expert + i % 2) * a.I + run.col + i / 2 * 16;
-        return {a.w13 + n * ldw, a.s13 + n * lds, (uint32_t)(16 * ldw), (uint32_t)(16 * lds)};
+        return tile_at(a.w13 + n * ldw, ldw, a.s13 + n * lds, lds, 16, K, range.k);
     }
     __device__ __forceinline__ bool wanted(const MoeRun& run, int, int m, int) const { return m < run.pairs; }
     __device__ __forceinline__ void finish(const MoeRun& run, int i, int m, int n, const Column<1>& gate,
@@ -417,13 +422,14 @@ struct DownUnits {
     __device__ __forceinline__ int early(int, int) const { return 0; }
     __device__ __forceinline__ void late(int, int) const {}
     __device__ __forceinline__ MoeRun run(int u) const { return moe_run(r, u, tiles); }
-    __device__ __forceinline__ const uint16_t* x(const MoeRun& run, int plane, int m) const {
-        return m < run.pairs ? a.h + (plane * (a.T * a.topk) + first + run.row + m) * a.I : nullptr;
+    __device__ __forceinline__ Range range(int64_t k) const { return {k, K - k}; }
+    __device__ __forceinline__ const uint16_t* x(const MoeRun& run, int plane, int m, const Range& range) const {
+        return m < run.pairs ? a.h + (plane * (a.T * a.topk) + first + run.row + m) * a.I + range.k : nullptr;
     }
     __device__ __forceinline__ int rows(const MoeRun&, int) const { return 16; }  // H and I are multiples of 16
-    __device__ __forceinline__ Tile tile(const MoeRun& run, int i) const {
+    __device__ __forceinline__ Tile tile(const MoeRun& run, int i, const Range& range) const {
         const int64_t n = (int64_t)run.expert * a.H + run.col + i * 16;
-        return {a.w2 + n * ldw, a.s2 + n * lds, (uint32_t)(16 * ldw), (uint32_t)(16 * lds)};
+        return tile_at(a.w2 + n * ldw, ldw, a.s2 + n * lds, lds, 16, K, range.k);
     }
     __device__ __forceinline__ bool wanted(const MoeRun& run, int, int m, int) const { return m < run.pairs; }
     __device__ __forceinline__ void finish(const MoeRun& run, int i, int m, int n, const Column<1>& v) const {
@@ -442,6 +448,72 @@ __global__ void __launch_bounds__(64 * NW, waves_per_simd(1, 2, ST)) moe_down_ke
     const int64_t items = (int64_t)r.tiles * tiles;
     stream_units<ElemBF16, 2, ST>(p, lds, (int)(items * blockIdx.x / gridDim.x),
                                   (int)(items * (blockIdx.x + 1) / gridDim.x), a.kw2);
+}
+
+// The second product for few tokens and few chosen experts, with the sum over the experts
+// in it: the experts' rows of W2 side by side are one long K, of which a wave holds a
+// part of one expert; row m of X is token m's h where it chose that expert, else 0.
+constexpr int kFewTokens = 16;
+constexpr int kFewSteps = 2;
+
+template <typename E>
+struct DownFewUnits {
+    static constexpr bool kPair = false;
+    const MoeArgs& a;
+    const Routing& r;
+    int64_t K, ldw, lds;
+    int parts;  // of kFewSteps * 128 k of one expert
+    struct Run {
+        int from, end;
+    };
+    struct Range {
+        int64_t k, left;
+        int expert, row;  // the expert's first pair
+        unsigned long long tokens;
+    };
+    __device__ __forceinline__ int early(int, int) const { return 0; }
+    __device__ __forceinline__ void late(int, int) const {}
+    __device__ __forceinline__ Run run(int u) const { return {u, 0x7FFFFFFF}; }
+    __device__ __forceinline__ Range range(int64_t k) const {
+        const int part = (int)(k / (128 * kFewSteps)), slot = part / parts;
+        if (slot >= r.tiles) return {0, 0, 0, 0, 0};
+        const int64_t at = (int64_t)(part - slot * parts) * (128 * kFewSteps);
+        const int e = __builtin_amdgcn_readfirstlane(r.expert[slot]);
+        return {at, a.I - at, e, __builtin_amdgcn_readfirstlane(r.row[slot]), r.tokens[e]};
+    }
+    __device__ __forceinline__ const uint16_t* x(const Run&, int plane, int m, const Range& range) const {
+        if ((range.tokens >> m & 1) == 0) return nullptr;
+        const int row = range.row + __popcll(range.tokens & ((1ull << m) - 1));
+        return a.h + (plane * (a.T * a.topk) + row) * a.I + range.k;
+    }
+    __device__ __forceinline__ int rows(const Run&, int) const { return 16; }
+    __device__ __forceinline__ Tile tile(const Run& run, int i, const Range& range) const {
+        const int64_t n = (int64_t)range.expert * a.H + (run.from + i) * 16;
+        return tile_at(a.w2 + n * ldw, ldw, a.s2 + n * lds, lds, 16, a.I, range.k);
+    }
+    __device__ __forceinline__ bool wanted(const Run&, int, int m, int) const { return m < a.T; }
+    __device__ __forceinline__ void finish(const Run& run, int i, int m, int n, const Column<1>& sum) const {
+        const int64_t col = (run.from + i) * 16 + n;
+        float v = sum.v[0];
+        if (a.b2 != nullptr) {
+            for (int j = 0; j < a.topk; ++j) {
+                const uint32_t e = (uint32_t)a.ids[m * a.topk + j];
+                if (e < (uint32_t)a.E)
+                    v = __builtin_fmaf(a.weights[m * a.topk + j], E::widen(a.b2[(int64_t)e * a.H + col]), v);
+            }
+        }
+        a.c[m * a.ldc + col] = E::round(v);
+    }
+};
+
+template <typename E, bool PASSES>
+__global__ void __launch_bounds__(1024, 4) moe_down_few_kernel(MoeArgs a) {
+    __shared__ Lds<16, 1, 4, 1, PASSES> lds;
+    const Routing r = route(a.ids, nullptr, nullptr, (int)a.T, a.topk, a.E);
+    const int parts = (int)((a.I + 128 * kFewSteps - 1) / (128 * kFewSteps)), units = (int)(a.H / 16);
+    const DownFewUnits<E> p{a, r, (int64_t)r.tiles * parts * (128 * kFewSteps), a.I / 2, a.I / 32, parts};
+    stream_units<ElemBF16, 2, kFewSteps>(p, lds, (int)((int64_t)units * blockIdx.x / gridDim.x),
+                                         (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x), 16);
 }
 
 // out: 4 columns per thread; the sum goes through a token's choices in order.

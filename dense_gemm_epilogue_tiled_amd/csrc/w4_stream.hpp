@@ -62,10 +62,22 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* p, ui
                                              __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
 }
 
-// A unit: up to 16 rows of W and S.
+// A unit: up to 16 rows of W and S from some k on.
 struct Tile {
     const uint8_t *w, *s;
     uint32_t w_bytes, s_bytes;
+};
+
+// `rows` rows of K k with the pitches ldw and lds, from k on.
+__device__ __forceinline__ Tile tile_at(const uint8_t* w, int64_t ldw, const uint8_t* s, int64_t lds, int64_t rows,
+                                        int64_t K, int64_t k) {
+    return {w + k / 2, s + k / 32, (uint32_t)((rows - 1) * ldw + (K - k) / 2),
+            (uint32_t)((rows - 1) * lds + (K - k) / 32)};
+}
+
+// The usual range of a wave: the k from k on, of K.
+struct Range {
+    int64_t k, left;
 };
 
 // The scale codes of a unit, `blocks` whole blocks of whose rows are in the wave's
@@ -281,8 +293,10 @@ constexpr int rows_at_once(int MT) { return MT == 1 ? 1 : 4; }
 // P gives
 //   run(u)                    what the units from u on share: their X and more; run.end
 //                             is the first unit with other rows of X
-//   x(run, plane, m)          row m of X, or nullptr
-//   tile(run, i), rows(run, i)   the rows of W and S of the run's i-th unit, their number
+//   range(k)                  where the k from k on are: range.left of them from there
+//   x(run, plane, m, range)   row m of X from the range on, or nullptr
+//   tile(run, i, range)       the run's i-th unit from the range on
+//   rows(run, i)              the number of its rows
 //   K, ldw, lds               in k and bytes
 //   kPair                     a run's units 2i and 2i + 1 are finished together
 //   early(u0, u1), late(u0, value)   a load that goes out before all others, and what is
@@ -307,10 +321,11 @@ __device__ __forceinline__ bool stream_units_by(const P& p, Lds<NW, MT, TB, BUFS
     int parity = 0;
     for (int64_t pass = 0; pass == 0 || (PASSES && pass * span < p.K); ++pass) {
         const int64_t k0 = pass * span + part_of * (128 * ST);
-        const int64_t left = (p.K - k0) / 32;
+        const auto range = p.range(k0);
+        const int64_t left = range.left / 32;
         const bool active = left > 0;
         const int blocks = (int)(left < 4 * ST ? left : 4 * ST), shift = blocks < 4 * ST ? 0 : 8 * g;
-        const int w_at = r16 * (int)p.ldw + (int)(k0 / 2) + 16 * g, s_at = r16 * (int)p.lds + (int)(k0 / 32);
+        const int w_at = r16 * (int)p.ldw + 16 * g, s_at = r16 * (int)p.lds;
         const bool last_pass = !PASSES || (pass + 1) * span >= p.K;
         // runs of units with the same X
         for (int from = u0, to = 0; from < u1; from = to) {
@@ -322,7 +337,7 @@ __device__ __forceinline__ bool stream_units_by(const P& p, Lds<NW, MT, TB, BUFS
             const auto unit_of = [&](int i) { return (i / kPer * groups + group) * kPer + i % kPer; };
             const auto tile_of = [&](int i) {
                 const int u = unit_of(i);
-                Tile t = p.tile(run, u < units ? u : units - 1);
+                Tile t = p.tile(run, u < units ? u : units - 1, range);
                 if (u >= units) t.w_bytes = t.s_bytes = 0;
                 return t;
             };
@@ -342,9 +357,8 @@ __device__ __forceinline__ bool stream_units_by(const P& p, Lds<NW, MT, TB, BUFS
                     const uint8_t *x[MT], *scale[MT];
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
-                        x[mt] = p.x(mt * 16 + r16);
-                        scale[mt] = p.x_scale(mt * 16 + r16) + k0 / 32;
-                        if (x[mt] != nullptr) x[mt] += k0 / 2;
+                        x[mt] = p.x(mt * 16 + r16, range);
+                        scale[mt] = p.x_scale(mt * 16 + r16, range);
                     }
                     load_rows<MT, PL, ST>(rows, x, scale, g, blocks);
                 } else {
@@ -352,10 +366,7 @@ __device__ __forceinline__ bool stream_units_by(const P& p, Lds<NW, MT, TB, BUFS
 #pragma unroll
                     for (int pl = 0; pl < PL; ++pl)
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            x[pl][mt] = p.x(run, pl, mt * 16 + r16);
-                            if (x[pl][mt] != nullptr) x[pl][mt] += k0;
-                        }
+                        for (int mt = 0; mt < MT; ++mt) x[pl][mt] = p.x(run, pl, mt * 16 + r16, range);
                     load_rows<E, MT, PL, ST>(rows, x, g, blocks);
                 }
             }

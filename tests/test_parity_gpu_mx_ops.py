@@ -495,7 +495,8 @@ def check_moe(T, H, I, E, k, dtype, act="silu", bias=False, seed=50, ids=None):
 @pytest.mark.parametrize("T,H,I,E,k", [(1, 32, 32, 1, 1), (1, 64, 96, 4, 2), (2, 160, 64, 8, 8), (7, 256, 160, 5, 3),
                                        (16, 128, 128, 3, 2), (17, 96, 288, 4, 2), (40, 64, 64, 2, 2),
                                        (64, 128, 96, 6, 4), (65, 64, 128, 7, 2), (130, 32, 64, 9, 3),
-                                       (3, 512, 1024, 64, 6), (5, 64, 64, 600, 4)])
+                                       (3, 512, 1024, 64, 6), (5, 64, 64, 600, 4), (2, 64, 2080, 3, 3), (1, 96, 1056, 9, 4),
+                                       (12, 4128, 32, 3, 2), (20, 8224, 64, 2, 1), (18, 32, 4160, 2, 2)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_moe(T, H, I, E, k, dtype):
     check_moe(T, H, I, E, k, dtype, bias=(T % 2 == 0))
