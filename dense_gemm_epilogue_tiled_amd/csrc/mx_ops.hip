@@ -359,9 +359,18 @@ int run_moe(gr::w4::MoeArgs a, hipStream_t stream) {
         const Division d13 = divide(a.H, 4, true), d2 = divide(a.I, 2, true);
         a.kw13 = d13.kw;
         a.kw2 = d2.kw;
-        // an item of the first product is two units
-        const dim3 g13((uint32_t)grid_of(tiles * (a.I / 16), d13, 16 / d13.waves, kSumTiles / 2), chunks);
-        const dim3 g2((uint32_t)grid_of(tiles * (a.H / 16), d2, 16 / d2.waves, kSumTiles), chunks);
+        // workgroups for every tile of pairs; with several passes no more units each
+        // than their sums have room for, whichever tiles there are (an item of the first
+        // product is two units)
+        const auto grid = [&](int64_t each, const Division& d, int64_t room) {
+            int64_t wgs = tiles * ((each + d.waves / d.kw - 1) / (d.waves / d.kw));
+            const int64_t most = kCus * (16 / d.waves);
+            if (wgs > most) wgs = most;
+            const int64_t least = tiles * ((each + room - 1) / room);
+            if (d.passes && wgs < least) wgs = least;
+            return dim3((uint32_t)wgs, chunks);
+        };
+        const dim3 g13 = grid(a.I / 16, d13, kSumTiles / 2), g2 = grid(a.H / 16, d2, kSumTiles);
         const int lds = routing_bytes(a.E, a.topk);
         int st = d13.passes        ? launch_lds(moe_gate_up_kernel<E, 16, 4, true>, g13, 1024, lds, stream, a)
                  : d13.waves == 16 ? launch_lds(moe_gate_up_kernel<E, 16, 4, false>, g13, 1024, lds, stream, a)

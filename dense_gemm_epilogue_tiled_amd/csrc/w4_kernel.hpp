@@ -237,6 +237,54 @@ __host__ __device__ constexpr int routing_bytes(int E, int topk) {
     return 8 * E + 8 + 3 * 4 * kChunk * topk + 2 * (3 * E + 2 + max_tiles(E, topk)) + kChunk * topk;
 }
 
+// The tables for at most 8 choices: lane 8i + q holds choice i next to choice q, so one
+// comparison serves all pairs of choices, and the 8 bits of a ballot that belong to
+// i count.  Every wave fills the tables with the same values and reads only after its
+// own writes, so there is no barrier.
+constexpr int kFewChoices = 8;
+
+__device__ __forceinline__ void route_few(Routing& r, const int32_t* ids, const float* weights, int32_t* pair, int n,
+                                          int topk, int E) {
+    const int lane = threadIdx.x % 64, i = lane / 8, q = lane % 8, count = n * topk;
+    const int e = i < count ? ids[i] : -1, eq = q < count ? ids[q] : -1;
+    const int t = (uint32_t)i / (uint32_t)topk, tq = (uint32_t)q / (uint32_t)topk;
+    const float share = weights != nullptr && q < count ? weights[q] : 0.0f;
+    const auto bits = [&](bool x) { return (uint32_t)(__ballot(x) >> (8 * i)) & 255u; };  // q's, of this i
+    // choices of the same expert by the same token are one pair, with their weights' sum
+    const bool same = e == eq && t == tq;
+    const unsigned long long again = __ballot(same && q < i);
+    const bool is = (uint32_t)e < (uint32_t)E && (again >> (8 * i) & 255u) == 0;
+    const bool is_q = (uint32_t)eq < (uint32_t)E && (again >> (8 * q) & 255u) == 0;
+    const int row = __popc(bits(is_q && (eq < e || (eq == e && tq < t))));
+    const bool first = is && bits(is_q && eq == e && tq < t) == 0;
+    float weight = same ? share : 0.0f;
+    uint32_t tokens = is_q && eq == e ? 1u << tq : 0u;
+    weight += mx::dppf<mx::kQuadXor1>(weight);
+    tokens |= mx::dpp<mx::kQuadXor1>(tokens);
+    weight += mx::dppf<mx::kQuadXor2>(weight);
+    tokens |= mx::dpp<mx::kQuadXor2>(tokens);
+    weight += mx::dppf<mx::kRowHalfMirror>(weight);
+    tokens |= mx::dpp<mx::kRowHalfMirror>(tokens);
+    const unsigned long long experts = __ballot(first && q == 0);
+    const int slot = __popc(bits((experts >> (8 * q) & 1) != 0 && eq < e));
+    const int pairs = __popcll(__ballot(is && q == 0));
+    r.tiles = __popcll(experts);
+    if (q == 0) {
+        if (is) {
+            r.token[row] = (uint8_t)t;
+            r.weight[row] = weight;
+        }
+        if (first) {
+            r.tokens[e] = tokens;
+            r.expert[slot] = (uint16_t)e;
+            r.row[slot] = (uint16_t)row;
+            r.tile[slot] = (uint16_t)(slot * 4);
+        }
+        if (pair != nullptr && i < count && threadIdx.x < 64) pair[i] = is ? row : -1;
+    }
+    if (lane == 0) r.row[r.tiles] = (uint16_t)pairs;
+}
+
 // The routing of the chunk's ids (n tokens x topk); called by the whole
 // workgroup.  Ids outside [0, E) choose nothing, and a token that names an
 // expert twice is one pair.  With `weights` each pair's weight is put down too, and
@@ -255,6 +303,10 @@ __device__ __forceinline__ Routing route(const int32_t* ids, const float* weight
     r.row_of = r.row + E + 1;
     r.tile = r.row_of + E;
     r.token = reinterpret_cast<uint8_t*>(r.tile + max_tiles(E, topk));
+    if (n * topk <= kFewChoices) {
+        route_few(r, ids, weights, pair, n, topk, E);
+        return r;
+    }
     for (int i = threadIdx.x; i < n * topk; i += blockDim.x) {
         id[i] = ids[i];
         if (weights != nullptr) share[i] = weights[i];
@@ -354,6 +406,25 @@ __device__ __forceinline__ MoeRun moe_run(const Routing& r, int item, int tiles)
             __builtin_amdgcn_readfirstlane(r.row[at / 4 + 1]) - row, (item - tile * tiles) * 16};
 }
 
+// The items [first, last) of a workgroup, `tiles` for each tile of pairs: all of one
+// tile of pairs where there are workgroups enough (a change of X costs a trip to
+// memory), else an equal share of all.
+struct Items {
+    int first, last;
+};
+
+__device__ __forceinline__ Items items_of(int pair_tiles, int tiles) {
+    const int wgs = gridDim.x, wg = blockIdx.x;
+    if (pair_tiles > wgs) {
+        const int64_t all = (int64_t)pair_tiles * tiles;
+        return {(int)(all * wg / wgs), (int)(all * (wg + 1) / wgs)};
+    }
+    if (pair_tiles == 0) return {0, 0};
+    const int each = wgs / pair_tiles, tile = wg / each, part = wg % each;
+    if (tile >= pair_tiles) return {0, 0};
+    return {tile * tiles + (int)((int64_t)tiles * part / each), tile * tiles + (int)((int64_t)tiles * (part + 1) / each)};
+}
+
 // Units of the first product: 16 columns of h for a tile of pairs, gate and up.
 template <typename E>
 struct GateUpUnits {
@@ -407,9 +478,8 @@ __global__ void __launch_bounds__(64 * NW, waves_per_simd(1, 1, ST)) moe_gate_up
         route(a.ids + first, a.weights + first, blockIdx.x == 0 ? a.pair + first : nullptr, n_tok, a.topk, a.E);
     const int tiles = (int)(a.I / 16);
     const GateUpUnits<E> p{a, r, a.H, a.H / 2, a.H / 32, t0, tiles};
-    const int64_t items = (int64_t)r.tiles * tiles;
-    stream_units<E, 1, ST>(p, lds, (int)(items * blockIdx.x / gridDim.x) * 2,
-                           (int)(items * (blockIdx.x + 1) / gridDim.x) * 2, a.kw13);
+    const Items items = items_of(r.tiles, tiles);
+    stream_units<E, 1, ST>(p, lds, items.first * 2, items.last * 2, a.kw13);
 }
 
 // Units of the second product: 16 columns of the output for a tile of pairs.
@@ -445,9 +515,8 @@ __global__ void __launch_bounds__(64 * NW, waves_per_simd(1, 2, ST)) moe_down_ke
     const Routing r = route(a.ids + t0 * a.topk, nullptr, nullptr, n_tok, a.topk, a.E);
     const int tiles = (int)(a.H / 16);
     const DownUnits p{a, r, a.I, a.I / 2, a.I / 32, t0 * a.topk, tiles};
-    const int64_t items = (int64_t)r.tiles * tiles;
-    stream_units<ElemBF16, 2, ST>(p, lds, (int)(items * blockIdx.x / gridDim.x),
-                                  (int)(items * (blockIdx.x + 1) / gridDim.x), a.kw2);
+    const Items items = items_of(r.tiles, tiles);
+    stream_units<ElemBF16, 2, ST>(p, lds, items.first, items.last, a.kw2);
 }
 
 // The second product for few tokens and few chosen experts, with the sum over the experts
