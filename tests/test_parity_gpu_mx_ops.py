@@ -581,3 +581,55 @@ def test_block_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(captured.cpu().view(torch.int16), want.view(torch.int16)), i
+
+
+# ---- the blocks --------------------------------------------------------------------------
+
+def block_inputs(T, H, I, E, seed):
+    x, r, n = inputs(T, H, "bf16", seed), inputs(T, H, "bf16", seed + 1), (1 + inputs(1, H, "bf16", seed + 2, 0.1)[0])
+    return x, r, n.bfloat16(), inputs(2 * I * max(E, 1), H, "bf16", seed + 3, 0.05), inputs(H * max(E, 1), I, "bf16",
+                                                                                            seed + 4, 0.05)
+
+
+@pytest.mark.parametrize("T", [1, 5, 40])
+def test_dense_blocks(T):
+    """Each step's rounding to bfloat16 (or MX fp4) is repeated in the plain form, so that only the sums differ: the
+    products' inputs agree but for values next to a rounding border, which a comparison of norms allows for."""
+    from dense_gemm_epilogue_tiled_amd import feed_forward as ff
+    H, I = 256, 192
+    x, r, n, w13, w2 = block_inputs(T, H, I, 0, 100)
+    q13, q2 = ff.quantize_weight(w13.cuda()), ff.quantize_weight(w2.cuda())
+    a, b = mx_ref.weight(q13[0].cpu(), q13[1].cpu()), mx_ref.weight(q2[0].cpu(), q2[1].cpu())
+    total, h = norm_ref(x, r, n, 1e-6)
+    for fp4 in (False, True):
+        out, got_total = (ff.dense_block_fp4 if fp4 else ff.dense_block)(x.cuda(), r.cuda(), n.cuda(), q13, q2)
+        assert torch.equal(got_total.cpu(), total)
+
+        def rounded(v):
+            if not fp4:
+                return v.bfloat16().double()
+            q, e = mx_ref.quantise(v, "mxfp4")
+            return q * torch.pow(2.0, e.double()).repeat_interleave(32, -1)
+
+        both = (rounded(h) @ a.T).bfloat16().double()
+        ref = rounded(mx_ref.act(both[:, :I], "silu") * both[:, I:]) @ b.T
+        err = (out.cpu().double() - ref).norm() / ref.norm()
+        # half steps of bfloat16 in the output and, where a border was crossed, in the inputs; an fp4 element
+        # that crosses one is off by half of itself, which few do
+        assert err < (2.0 ** -8 * 2 if not fp4 else 0.05), (fp4, float(err))
+
+
+@pytest.mark.parametrize("T", [1, 6, 40])
+def test_moe_block(T):
+    from dense_gemm_epilogue_tiled_amd import feed_forward as ff
+    H, I, E, k = 256, 128, 8, 2
+    x, r, n, w13, w2 = block_inputs(T, H, I, E, 110)
+    router = inputs(E, H, "bf16", 120, 2 * H ** -0.5)
+    q13, q2 = ff.quantize_weight(w13.view(E, 2 * I, H).cuda()), ff.quantize_weight(w2.view(E, H, I).cuda())
+    out, got_total = ff.moe_block(x.cuda(), r.cuda(), n.cuda(), router.cuda(), k, q13, q2)
+    h, _, _ = gr.rms_norm(x.cuda(), n.cuda(), r.cuda(), out_format="same")
+    ids, p = gr.moe_route(h, router.cuda(), k)
+    total, _ = norm_ref(x, r, n, 1e-6)
+    assert torch.equal(got_total.cpu(), total)
+    ref, bound = mx_ref.moe(h.cpu(), ids.cpu(), p.cpu(), *(t.cpu() for t in (*q13, *q2)), None, None, "silu")
+    mx_ref.check16(out.cpu(), ref, torch.bfloat16, bound)
