@@ -168,16 +168,6 @@ Division divide(int64_t K, int most, bool wide) {
     return d;
 }
 
-// Workgroups along the units (`per` of them go together): enough to fill the chip, and
-// for several passes no more units each than their sums have room for.
-int64_t grid_of(int64_t units, const Division& d, int64_t wgs_per_cu, int64_t room) {
-    const int groups = d.waves / d.kw;
-    int64_t grid = (units + groups - 1) / groups;
-    if (grid > kCus * wgs_per_cu) grid = kCus * wgs_per_cu;
-    if (d.passes && grid * room < units) grid = (units + room - 1) / room;
-    return grid;
-}
-
 template <typename E, int NW, int MT, int ST, bool PASSES>
 int launch_w4(const gr::w4::LinearArgs& a, dim3 grid, hipStream_t stream) {
     return launch_grid(gr::w4::linear_w4_kernel<E, NW, MT, ST, PASSES>, grid, 64 * NW, stream, a);
@@ -195,39 +185,69 @@ int launch_w4_rows(const gr::w4::LinearArgs& a, const Division& d, dim3 grid, hi
     return launch_w4<E, 8, MT, 1, false>(a, grid, stream);
 }
 
-// Whether K goes to several workgroups instead of several passes of one: up to
-// 64 rows, where X is read once that way and the sums are small.
-// 64 x 8192 x 8192: one workgroup reads 256 KB of X instead of 1 MB.
-struct Splits {
-    int64_t span, count, ldp;
+// Rows of X per workgroup (16 * MT), units of 16 rows of W that one takes, and whether K
+// goes to several workgroups (`splits` of `span` k, sums in a workspace with rows of ldp)
+// instead of several passes of one.
+struct W4Plan {
+    int MT;
+    Division d;
+    int64_t units, splits, span, ldp;
 };
 
-Splits splits_of(int64_t M, int64_t N, int64_t K) {
-    Splits s{K > 0 ? (K + 127) / 128 * 128 : 128, 1, (N + 3) / 4 * 4};
-    if (M > 64) return s;
-    const int MT = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
-    const Division d = divide(K, MT == 1 ? 4 : 8 / MT, MT == 1);
-    if (!d.passes) return s;
-    const int64_t steps = (K + 127) / 128, most = (int64_t)d.steps * d.waves;
-    const int64_t count = (steps + most - 1) / most;
-    if (count > 64) return s;
-    s.span = (steps + count - 1) / count * 128;
-    s.count = (K + s.span - 1) / s.span;
-    return s;
+// What a CU reads (26 KB a microsecond, from L2 or farther) and the units' sums make the
+// time of the streaming kernels; the split's second kernel takes 4.5 more.  More
+// rows of X per workgroup read W less often, fewer read X less often: 64x1000x2048 takes
+// 11.4 us with 64 rows and 6.1 with 16, 64x8192x8192 is fastest with 64.  Two workgroups
+// per CU, where they fit, share the units but read X twice.
+W4Plan w4_plan(int64_t M, int64_t N, int64_t K, bool split) {
+    W4Plan best{};
+    double least = -1;
+    const int64_t all = (N + 15) / 16, steps = K > 0 ? (K + 127) / 128 : 1;
+    for (int MT = 1; MT <= (M <= 16 ? 1 : (M <= 32 ? 2 : 4)); MT *= 2) {
+        const int most = MT == 1 ? 4 : 8 / MT;
+        const int64_t held = most * (MT == 1 ? 16 : 8);  // steps of 128 that a workgroup holds
+        const int64_t needed = (steps + held - 1) / held, tiles = (M + 16 * MT - 1) / (16 * MT);
+        const int64_t rows = M < 16 * MT ? M : 16 * MT;
+        // as many splits as X needs, or more where the units are too few for the chip
+        for (int64_t want = split && M <= 64 && needed <= 64 ? needed : 1;; want *= 2) {
+            W4Plan p{MT, {}, 1, 1, steps * 128, (N + 3) / 4 * 4};
+            if (want > 1) {
+                p.span = (steps + want - 1) / want * 128;
+                p.splits = (steps * 128 + p.span - 1) / p.span;
+            }
+            p.d = divide(p.span, most, MT == 1);
+            for (int wgs = 1; wgs <= (MT == 1 && p.d.waves == 8 ? 2 : 1); ++wgs) {
+                p.units = (tiles * p.splits * all + kCus * wgs - 1) / (kCus * wgs);
+                if (p.units > all) p.units = all;
+                const int64_t grid = tiles * p.splits * ((all + p.units - 1) / p.units);
+                const int64_t rounds = (grid + kCus * wgs - 1) / (kCus * wgs);
+                const double kb = wgs * (2.0 * rows + 8.5 * p.units) * (double)p.span / 1024;
+                const double us = rounds * (kb / 26 + (0.4 + 0.27 * MT) * p.units) + (p.splits > 1 ? 4.5 : 0);
+                if (least < 0 || us < least) {
+                    least = us;
+                    best = p;
+                }
+            }
+            if (!split || M > 64 || want * 2 > 64 || p.span <= 512 || tiles * p.splits * all >= kCus) break;
+        }
+    }
+    return best;
 }
 
 int64_t w4_workspace(int64_t M, int64_t N, int64_t K) {
-    const Splits s = splits_of(M, N, K);
-    return s.count > 1 ? aligned(s.count * M * s.ldp * 4) : 0;
+    const W4Plan p = w4_plan(M, N, K, true);
+    return p.splits > 1 ? aligned(p.splits * M * p.ldp * 4) : 0;
 }
 
 template <typename E, int MT>
-int run_w4_rows(gr::w4::LinearArgs a, int64_t splits, hipStream_t stream) {
-    const Division d = divide(a.span < a.K ? a.span : a.K, MT == 1 ? 4 : 8 / MT, MT == 1);
+int run_w4_rows(gr::w4::LinearArgs a, const W4Plan& p, hipStream_t stream) {
+    const Division& d = p.d;
     a.kw = d.kw;
-    int64_t wgs = d.waves * d.steps * MT > 32 ? 1 : 2;
-    int64_t gx = grid_of((a.N + 15) / 16, d, wgs, gr::w4::kSumTiles / MT);
-    if (splits > 1 && gx > kCus * wgs / splits) gx = kCus * wgs / splits > 1 ? kCus * wgs / splits : 1;
+    a.span = p.span;
+    a.ldp = p.ldp;
+    const int64_t all = (a.N + 15) / 16, room = gr::w4::kSumTiles / MT;
+    int64_t gx = (all + p.units - 1) / p.units;
+    if (d.passes && gx * room < all) gx = (all + room - 1) / room;
     const int64_t gy = (a.M + 16 * MT - 1) / (16 * MT);
     // rows beyond the grid's y limit go in further launches
     for (int64_t y = 0; y < gy; y += 65535) {
@@ -235,21 +255,21 @@ int run_w4_rows(gr::w4::LinearArgs a, int64_t splits, hipStream_t stream) {
         b.x += y * 16 * MT * a.ldx;
         b.c += y * 16 * MT * a.ldc;
         b.M -= y * 16 * MT;
-        const dim3 grid((uint32_t)gx, (uint32_t)(gy - y < 65535 ? gy - y : 65535), (uint32_t)splits);
+        const dim3 grid((uint32_t)gx, (uint32_t)(gy - y < 65535 ? gy - y : 65535), (uint32_t)p.splits);
         const int st = launch_w4_rows<E, MT>(b, d, grid, stream);
         if (st != GR_OK) return st;
     }
-    if (splits == 1) return GR_OK;
+    if (p.splits == 1) return GR_OK;
     const int64_t per = 4 * gr::w4::kSumThreads;
     return launch_grid(gr::w4::linear_w4_sum_kernel<E>, dim3((uint32_t)((a.N + per - 1) / per), (uint32_t)a.M),
                        gr::w4::kSumThreads, stream, a);
 }
 
 template <typename E>
-int run_w4(const gr::w4::LinearArgs& a, int64_t splits, hipStream_t stream) {
-    if (a.M <= 16) return run_w4_rows<E, 1>(a, splits, stream);
-    if (a.M <= 32) return run_w4_rows<E, 2>(a, splits, stream);
-    return run_w4_rows<E, 4>(a, splits, stream);
+int run_w4(const gr::w4::LinearArgs& a, const W4Plan& p, hipStream_t stream) {
+    if (p.MT == 1) return run_w4_rows<E, 1>(a, p, stream);
+    if (p.MT == 2) return run_w4_rows<E, 2>(a, p, stream);
+    return run_w4_rows<E, 4>(a, p, stream);
 }
 
 // ---- both operands in MX fp4 -------------------------------------------------------
@@ -300,9 +320,8 @@ int run_fp4_rows(gr::w4::Fp4Args a, int64_t units, hipStream_t stream) {
     const Division d = divide(a.K, 4, false);
     a.kw = d.kw;
     const int64_t gy = (a.M + 16 * MT - 1) / (16 * MT);
-    const int64_t all = (a.N + 15) / 16, groups = d.waves / d.kw;
+    const int64_t all = (a.N + 15) / 16;
     int64_t gx = (all + units - 1) / units;
-    if (gx > (all + groups - 1) / groups) gx = (all + groups - 1) / groups;
     const int64_t room = kSumTiles / MT;
     if (d.passes && gx * room < all) gx = (all + room - 1) / room;
     for (int64_t y = 0; y < gy; y += 65535) {
@@ -363,7 +382,7 @@ int run_moe(gr::w4::MoeArgs a, hipStream_t stream) {
         // than their sums have room for, whichever tiles there are (an item of the first
         // product is two units)
         const auto grid = [&](int64_t each, const Division& d, int64_t room) {
-            int64_t wgs = tiles * ((each + d.waves / d.kw - 1) / (d.waves / d.kw));
+            int64_t wgs = tiles * each;
             const int64_t most = kCus * (16 / d.waves);
             if (wgs > most) wgs = most;
             const int64_t least = tiles * ((each + room - 1) / room);
@@ -530,13 +549,9 @@ int gemm_w4_bt(int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, 
     if (workspace_bytes < 0 || reinterpret_cast<uintptr_t>(workspace) % kWorkspaceAlign != 0) return GR_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return GR_OK;
     // (too small a workspace is none)
-    Splits s = splits_of(M, N, K);
     const int64_t need = w4_workspace(M, N, K);
-    if (!workspace || workspace_bytes < need) {
-        s.count = 1;
-        s.span = K > 0 ? (K + 127) / 128 * 128 : 128;
-    }
-    if (s.count > 1) {
+    const W4Plan p = w4_plan(M, N, K, workspace && workspace_bytes >= need);
+    if (p.splits > 1) {
         const Region ws{reinterpret_cast<uintptr_t>(workspace), need};
         if (overlaps(ws, matrix16(C, M, N, ldc)) || overlaps(ws, matrix16(A, M, K, lda)) ||
             overlaps(ws, matrix8(Bt, N, K / 2, ldbt)) || overlaps(ws, matrix8(scale_b, N, K / 32, ld_sb)) ||
@@ -545,10 +560,10 @@ int gemm_w4_bt(int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, 
     }
     st = check_device();
     if (st != GR_OK) return st;
-    const gr::w4::LinearArgs a{A,   Bt,   scale_b, bias, C,   M, N, K, lda, ldbt, ld_sb, ldc, act, 1,
-                               s.count > 1 ? static_cast<float*>(workspace) : nullptr, s.ldp, s.span};
+    const gr::w4::LinearArgs a{A,   Bt,    scale_b, bias, C,   M, N, K, lda, ldbt, ld_sb, ldc, act, 1,
+                               p.splits > 1 ? static_cast<float*>(workspace) : nullptr, 0, 0};
     hipStream_t h = static_cast<hipStream_t>(stream);
-    return fmt == GR_FMT_BF16 ? run_w4<gr::ElemBF16>(a, s.count, h) : run_w4<gr::ElemF16>(a, s.count, h);
+    return fmt == GR_FMT_BF16 ? run_w4<gr::ElemBF16>(a, p, h) : run_w4<gr::ElemF16>(a, p, h);
 }
 
 int gemm_mxfp4_linear_bt(int64_t M, int64_t N, int64_t K, const uint8_t* A, int64_t lda, const uint8_t* scale_a,

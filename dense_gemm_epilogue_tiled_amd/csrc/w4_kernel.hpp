@@ -91,9 +91,9 @@ struct LinearUnits {
     }
 };
 
-// Registers for two workgroups of 8 waves, or one of 16, per CU while X takes 64 of
-// them.
-constexpr int waves_per_simd(int MT, int PL, int ST) { return MT * PL * ST <= 4 ? 4 : 2; }
+// Registers for two workgroups of 8 waves, or one of 16, per CU with 16 rows of X, which
+// take 64 of them.
+constexpr int waves_per_simd(int MT, int PL, int ST) { return PL * ST <= 4 && MT == 1 ? 4 : 2; }
 
 template <typename E, int NW, int MT, int ST, bool PASSES>
 __global__ void __launch_bounds__(64 * NW, waves_per_simd(MT, 1, ST)) linear_w4_kernel(LinearArgs a) {

@@ -313,7 +313,7 @@ __device__ __forceinline__ bool stream_units_by(const P& p, Lds<NW, MT, TB, BUFS
     constexpr int kPer = P::kPair ? 2 : 1;
     const int lane = threadIdx.x % 64, g = lane / 16, r16 = lane % 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int groups = NW / kw, group = wave / kw, part_of = wave % kw;
+    const int groups = NW / kw, group = wave / kw, part_of = wave % kw;  // powers of two
     const int64_t span = (int64_t)kw * (128 * ST);
     const auto ahead = p.early(u0, u1);
     if (!ANY && threadIdx.x == 0) lds.again = 0;
@@ -429,17 +429,19 @@ __device__ __forceinline__ bool stream_units_by(const P& p, Lds<NW, MT, TB, BUFS
                 if (!ANY && bad && lane == 0) lds.again = 1;
                 lds_barrier();
                 constexpr int R = rows_at_once(MT);
-                const int total = TB / kPer * groups * MT * (256 / R);
+                // what this turn finishes, pairs counted once
+                const int all = TB / kPer * groups, rest = units / kPer - turn * all;
+                const int total = (rest < all ? rest : all) * MT * (256 / R);
                 // (a thread number that the compiler takes for new in each turn: what follows
                 // from it is not kept in registers through the loop above)
                 int first = threadIdx.x;
                 asm volatile("" : "+v"(first));
                 for (int at = first; at < total; at += 64 * NW) {
                     // R rows of one column of one unit: register e % 4 of lane e / 4
-                    const int e = at % (256 / R) * R, q = at / (256 / R), mt = q % MT, t = q / MT % (TB / kPer);
-                    const int m = mt * 16 + e / 64 * 4 + e % 4, n = e / 4 % 16, gi = q / MT / (TB / kPer);
-                    const int u = ((turn * (TB / kPer) + t) * groups + gi) * kPer;
-                    if (u < units && p.wanted(run, u, m, n)) {
+                    const int e = at % (256 / R) * R, mt = at / (256 / R) % MT, q = at / (256 / R) / MT;
+                    const int m = mt * 16 + e / 64 * 4 + e % 4, n = e / 4 % 16, gi = q & (groups - 1), t = q / groups;
+                    const int u = (turn * all + q) * kPer;
+                    if (p.wanted(run, u, m, n)) {
                         typedef float Floats __attribute__((ext_vector_type(R)));
                         Column<R> v[kPer];
 #pragma unroll
