@@ -204,9 +204,10 @@ def lib() -> ctypes.CDLL:
             l.moe_route_workspace_size.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
             l.moe_w4_workspace_size.argtypes = [i64, i64, i64, i64, i64, ctypes.POINTER(ctypes.c_int64)]
             l.moe_w4.argtypes = [i64, i64, i64, i64, i64, p, i64, p, p, p, p, p, p, p, p, i32, p, i64, i32, p, i64, p]
-            for nm in ("rms_norm_mx", "gated_act_mx", "gemm_w4_bt", "gemm_w4_bt_workspace_size", "moe_route",
-                       "moe_route_workspace_size",
-                       "moe_w4_workspace_size", "moe_w4"):
+            l.gemm_mxfp4_linear_bt.argtypes = l.gemm_mxfp4_bt.argtypes
+            for nm in ("rms_norm_mx", "gated_act_mx", "gemm_w4_bt", "gemm_w4_bt_workspace_size",
+                       "gemm_mxfp4_linear_bt", "moe_route", "moe_route_workspace_size", "moe_w4_workspace_size",
+                       "moe_w4"):
                 getattr(l, nm).restype = i32
             l.gemm_relu_status_string.argtypes = [i32]
             l.gemm_relu_status_string.restype = ctypes.c_char_p
@@ -743,6 +744,7 @@ def linear(x, weight, bias=None, act="none", out=None, stream=None, path=None):
     return out
 
 
-from .mx_ops import (gated_act, gated_act_mx, gemm_mxfp4, gemm_w4_bt, gemm_w4_bt_workspace_size, linear_mxfp4, moe_mxfp4,  # noqa: E402,F401
+from .mx_ops import (gated_act, gated_act_mx, gemm_mxfp4, gemm_mxfp4_linear_bt, gemm_w4_bt,  # noqa: E402,F401
+                     gemm_w4_bt_workspace_size, linear_mxfp4, moe_mxfp4,
                      moe_route, moe_route_raw, moe_route_workspace_size, moe_w4, moe_w4_workspace_size, mx_quantize,
                      rms_norm, rms_norm_mx)

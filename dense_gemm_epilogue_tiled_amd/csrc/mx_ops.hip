@@ -194,7 +194,7 @@ struct W4Plan {
     int64_t units, splits, span, ldp;
 };
 
-// What a CU reads (26 KB a microsecond, from L2 or farther) and the units' sums make the
+// (M and N at least 1.)  What a CU reads (26 KB a microsecond, from L2 or farther) and the units' sums make the
 // time of the streaming kernels; the split's second kernel takes 4.5 more.  More
 // rows of X per workgroup read W less often, fewer read X less often: 64x1000x2048 takes
 // 11.4 us with 64 rows and 6.1 with 16, 64x8192x8192 is fastest with 64.  Two workgroups
@@ -235,6 +235,7 @@ W4Plan w4_plan(int64_t M, int64_t N, int64_t K, bool split) {
 }
 
 int64_t w4_workspace(int64_t M, int64_t N, int64_t K) {
+    if (M == 0 || N == 0) return 0;
     const W4Plan p = w4_plan(M, N, K, true);
     return p.splits > 1 ? aligned(p.splits * M * p.ldp * 4) : 0;
 }
@@ -299,9 +300,9 @@ Fp4Plan fp4_plan(int64_t M, int64_t N) {
 }
 
 // Whether the streaming kernel is the faster one: always where gemm_mxfp4_bt has only its
-// guarded kernel (200x4000x2080: 11.9 against 25.1 us); against its 128 x 128
+// guarded kernel (200x4000x2080: 12.7 against 25.1 us); against its 128 x 128
 // tiles, one per CU, where it reads less (4x4096x4096: 4.9 against 10.0 us,
-// 512x4096x4096: 29.9 against 17.7); not where those tiles fill the chip.
+// 512x4096x4096: 29.9 against 17.3); not where those tiles fill the chip.
 bool fp4_streams(int64_t M, int64_t N, int64_t K, int64_t ldbt, int64_t ld_sb, int path) {
     if (ldbt > kW4MaxPitch || ld_sb > kW4MaxPitch || K < 32) return false;
     if (path == GR_PATH_TILE_EDGE) return true;
@@ -572,6 +573,7 @@ int gemm_mxfp4_linear_bt(int64_t M, int64_t N, int64_t K, const uint8_t* A, int6
     gr_plan_t plan;
     int st = gemm_mxfp4_bt_plan(M, N, K, A, lda, scale_a, ld_sa, Bt, ldbt, scale_b, ld_sb, bias, act, C, ldc, fmt, &plan);
     if (st != GR_OK) return st;
+    if (M == 0 || N == 0) return GR_OK;
     if (!fp4_streams(M, N, K, ldbt, ld_sb, plan.path))
         return gemm_mxfp4_bt(M, N, K, A, lda, scale_a, ld_sa, Bt, ldbt, scale_b, ld_sb, bias, act, C, ldc, fmt, stream);
     st = validate_w4(M, N, K, nullptr, K > 1 ? K : 1, Bt, ldbt, scale_b, ld_sb, bias, act, C, ldc, fmt, false);

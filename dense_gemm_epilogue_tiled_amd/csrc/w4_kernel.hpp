@@ -214,6 +214,10 @@ __global__ void __launch_bounds__(kSumThreads) linear_w4_sum_kernel(LinearArgs a
 // h and y.  h holds weight * act(g) * u in two bfloat16 parts (high and the
 // rest's high: 16 bits and fp32's range), so that the second product starts from
 // nearly fp32 values.
+//
+// 32 tokens with 8 of 64 experts, 4096 x 2048: 113 us for the first product (561 MB,
+// 5.0 TB/s), 67 for the second (295 MB, 4.4 TB/s), 5 for the sum.  One token with 4
+// experts of 2048 x 1024: 9 and 6 us, a launch, the ids and a trip for the weights each.
 
 constexpr int kChunk = 64;         // tokens per chunk
 constexpr int kMaxExperts = 1024;

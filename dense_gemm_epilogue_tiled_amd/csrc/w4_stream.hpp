@@ -17,6 +17,12 @@
 // at no cost.  In bfloat16 this is exact for scale codes 2 .. 252.  In fp16 the
 // scale is taken relative to the first one of the row in the wave's range,
 // which multiplies the fp32 sum afterwards; it is exact within 2^+-13 of that.
+//
+// Measured: 16x28672x8192 (126 MB) 35 us with new weights, 30 when they are cached; a
+// plain read of the weights takes 23 to 25.  Matrix cores and conversions would allow
+// 14 TB/s (16 conversions of 1.9 ns and 4 MFMA of 7 ns per KB and SIMD); X, 256 KB per CU
+// here, and the 25 to 34 KB a microsecond that a CU has in flight do not.
+//
 // A workgroup that meets other codes goes over its units again with multiply_any, which
 // multiplies each block's fp32 sum by its scale: exact for all codes; code 255 gives
 // NaN.  (In the loop itself that form cost 20 registers, which spilled.)

@@ -46,6 +46,13 @@ def gemm_w4_bt(M, N, K, A, lda, Bt, ldbt, scale_b, ld_sb, bias, act, C, ldc, fmt
                             fmt, _ptr(workspace), workspace_bytes, _ptr(stream))
 
 
+def gemm_mxfp4_linear_bt(M, N, K, A, lda, SA, ld_sa, Bt, ldbt, SB, ld_sb, bias, act, C, ldc, out_fmt=GR_FMT_F16,
+                         stream=None) -> int:
+    """gemm_mxfp4_bt for any shape (few rows, few tiles, any K % 32 == 0); returns the status code."""
+    return lib().gemm_mxfp4_linear_bt(M, N, K, _ptr(A), lda, _ptr(SA), ld_sa, _ptr(Bt), ldbt, _ptr(SB), ld_sb,
+                                      _ptr(bias), act, _ptr(C), ldc, out_fmt, _ptr(stream))
+
+
 def moe_route_workspace_size(T, H, E):
     """(status, bytes): the workspace with which moe_route is fastest (0: none needed)."""
     n = ctypes.c_int64(0)

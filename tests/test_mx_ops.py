@@ -21,13 +21,22 @@ def gated(M=4, N=64, g=X, ldg=64, u=R, ldu=64, act=gr.GR_ACT_SILU, y=Y, ldy=64, 
     return gr.gated_act_mx(M, N, g, ldg, u, ldu, act, y, ldy, sy, ld_sy, fmt, out)
 
 
+WS = 0x900000000000
+
+
 def linear(M=4, N=48, K=64, a=X, lda=64, bt=W, ldbt=32, s=S, lds=2, bias=None, act=gr.GR_ACT_NONE, c=Y, ldc=48,
-           fmt=BF):
-    return gr.gemm_w4_bt(M, N, K, a, lda, bt, ldbt, s, lds, bias, act, c, ldc, fmt)
+           fmt=BF, ws=None, size=0):
+    return gr.gemm_w4_bt(M, N, K, a, lda, bt, ldbt, s, lds, bias, act, c, ldc, fmt, ws, size)
 
 
-def route(T=4, H=64, E=8, k=2, x=X, ldx=64, w=W, ldw=64, bias=None, renorm=1, ids=I, weights=Y, fmt=BF):
-    return gr.moe_route_raw(T, H, E, k, x, ldx, w, ldw, bias, renorm, ids, weights, fmt)
+def fp4(M=4, N=48, K=64, a=X, lda=32, sa=R, ld_sa=2, bt=W, ldbt=32, s=S, lds=2, bias=None, act=gr.GR_ACT_NONE, c=Y,
+        ldc=48, fmt=BF):
+    return gr.gemm_mxfp4_linear_bt(M, N, K, a, lda, sa, ld_sa, bt, ldbt, s, lds, bias, act, c, ldc, fmt)
+
+
+def route(T=4, H=64, E=8, k=2, x=X, ldx=64, w=W, ldw=64, bias=None, renorm=1, ids=I, weights=Y, fmt=BF, ws=None,
+          size=0):
+    return gr.moe_route_raw(T, H, E, k, x, ldx, w, ldw, bias, renorm, ids, weights, fmt, ws, size)
 
 
 def moe(T=4, H=64, I_=96, E=8, k=2, x=X, ldx=64, ids=I, weights=R, w13=W, s13=S, b13=None, w2=B, s2=SY, b2=None,
@@ -89,6 +98,27 @@ REFUSALS = [
     (linear, dict(c=X), gr.GR_ERR_ALIAS),
     (linear, dict(c=W), gr.GR_ERR_ALIAS),
     (linear, dict(bias=Y), gr.GR_ERR_ALIAS),
+    (linear, dict(ldbt=(1 << 26) + 1), gr.GR_ERR_TOO_LARGE),
+    (linear, dict(ws=WS + 8, size=1 << 20), gr.GR_ERR_INVALID_ARG),
+    (linear, dict(ws=WS, size=-1), gr.GR_ERR_INVALID_ARG),
+    (linear, dict(M=64, K=8192, lda=8192, ldbt=4096, lds=256, ws=Y, size=1 << 30), gr.GR_ERR_ALIAS),
+    (linear, dict(M=64, K=8192, lda=8192, ldbt=4096, lds=256, ws=W, size=1 << 30), gr.GR_ERR_ALIAS),
+    (fp4, dict(K=48), gr.GR_ERR_INVALID_DIM),
+    (fp4, dict(M=-1), gr.GR_ERR_INVALID_DIM),
+    (fp4, dict(lda=31), gr.GR_ERR_INVALID_LD),
+    (fp4, dict(ld_sa=1), gr.GR_ERR_INVALID_LD),
+    (fp4, dict(ldbt=31), gr.GR_ERR_INVALID_LD),
+    (fp4, dict(lds=1), gr.GR_ERR_INVALID_LD),
+    (fp4, dict(ldc=47), gr.GR_ERR_INVALID_LD),
+    (fp4, dict(act=9), gr.GR_ERR_INVALID_ARG),
+    (fp4, dict(fmt=5), gr.GR_ERR_INVALID_ARG),
+    (fp4, dict(a=None), gr.GR_ERR_NULL_PTR),
+    (fp4, dict(sa=None), gr.GR_ERR_NULL_PTR),
+    (fp4, dict(bt=None), gr.GR_ERR_NULL_PTR),
+    (fp4, dict(c=None), gr.GR_ERR_NULL_PTR),
+    (fp4, dict(c=X), gr.GR_ERR_ALIAS),
+    (fp4, dict(c=S), gr.GR_ERR_ALIAS),
+    (fp4, dict(bias=Y), gr.GR_ERR_ALIAS),
     (route, dict(k=0), gr.GR_ERR_INVALID_ARG),
     (route, dict(k=9), gr.GR_ERR_INVALID_ARG),
     (route, dict(E=0), gr.GR_ERR_INVALID_DIM),
@@ -99,6 +129,9 @@ REFUSALS = [
     (route, dict(ids=None), gr.GR_ERR_NULL_PTR),
     (route, dict(ids=Y), gr.GR_ERR_ALIAS),
     (route, dict(weights=X), gr.GR_ERR_ALIAS),
+    (route, dict(ws=WS + 4, size=1 << 20), gr.GR_ERR_INVALID_ARG),
+    (route, dict(ws=WS, size=-5), gr.GR_ERR_INVALID_ARG),
+    (route, dict(H=8192, E=64, ldx=8192, ldw=8192, ws=W, size=1 << 30), gr.GR_ERR_ALIAS),
     (moe, dict(H=48), gr.GR_ERR_INVALID_DIM),
     (moe, dict(I_=100), gr.GR_ERR_INVALID_DIM),
     (moe, dict(E=0), gr.GR_ERR_INVALID_DIM),
@@ -125,7 +158,7 @@ def test_refused(call, args, status):
 
 @pytest.mark.parametrize("call,args", [
     (norm, dict(M=0)), (norm, dict(N=0, x=None, y=None)), (gated, dict(M=0, g=None)), (gated, dict(N=0)),
-    (linear, dict(M=0)), (linear, dict(N=0, ldc=1)), (route, dict(T=0)), (moe, dict(T=0)), (moe, dict(H=0))])
+    (linear, dict(M=0)), (linear, dict(N=0, ldc=1)), (fp4, dict(M=0)), (fp4, dict(N=0, ldc=1)), (route, dict(T=0)), (moe, dict(T=0)), (moe, dict(H=0))])
 def test_empty_is_ok_without_a_device(call, args):
     assert call(**args) == gr.GR_OK
 
@@ -136,6 +169,41 @@ def test_workspace_size():
     assert gr.moe_w4_workspace_size(0, 64, 96, 8, 2) == (gr.GR_OK, 0)
     assert gr.moe_w4_workspace_size(5, 64, 90, 8, 2)[0] == gr.GR_ERR_INVALID_DIM
     assert gr.lib().moe_w4_workspace_size(5, 64, 96, 8, 2, ctypes.POINTER(ctypes.c_int64)()) == gr.GR_ERR_INVALID_ARG
+
+
+def test_workspace_sizes_of_the_products_and_the_router():
+    """None where it would not help; the split sums' size where it does."""
+    assert gr.gemm_w4_bt_workspace_size(1, 4096, 4096) == (gr.GR_OK, 0)
+    st, n = gr.gemm_w4_bt_workspace_size(64, 8192, 8192)
+    assert st == gr.GR_OK and n >= 2 * 64 * 8192 * 4 and n % 256 == 0
+    assert gr.gemm_w4_bt_workspace_size(65, 8192, 8192) == (gr.GR_OK, 0)
+    assert gr.gemm_w4_bt_workspace_size(0, 8192, 8192) == gr.gemm_w4_bt_workspace_size(4, 0, 8192) == (gr.GR_OK, 0)
+    assert gr.gemm_w4_bt_workspace_size(4, 16, 0) == (gr.GR_OK, 0)
+    assert gr.gemm_w4_bt_workspace_size(4, 16, 40)[0] == gr.GR_ERR_INVALID_DIM
+    assert gr.moe_route_workspace_size(1, 64, 8) == (gr.GR_OK, 0)
+    st, n = gr.moe_route_workspace_size(3, 4096, 64)
+    assert st == gr.GR_OK and n >= 8 * 3 * 64 * 4
+    assert gr.moe_route_workspace_size(100000, 4096, 64) == (gr.GR_OK, 0)
+    assert gr.moe_route_workspace_size(1, 64, 0)[0] == gr.GR_ERR_INVALID_DIM
+
+
+def test_streaming_kernels_keep_to_registers():
+    """The kernels whose K is held at once use no more than a few spill slots, none of them in the streaming
+    loop (a reload there waits for every load in flight): checked with the compiler's resource report."""
+    import os
+    import re
+    import subprocess
+    from dense_gemm_epilogue_tiled_amd import build as b
+    unit = os.path.join(b.HERE, "csrc", "mx_ops.hip")
+    cmd = [b.HIPCC, *b.FLAGS, "-c", "--cuda-device-only", unit, "-o", os.devnull,
+           "-Rpass-analysis=kernel-resource-usage"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr[-2000:]
+    names = re.findall(r"Function Name: (\S+)", res.stderr)
+    scratch = [int(x) for x in re.findall(r"ScratchSize \[bytes/lane\]: (\d+)", res.stderr)]
+    assert names and len(names) == len(scratch)
+    for n, s in zip(names, scratch):
+        assert s <= 64, (n, s)
 
 
 def test_helpers_refuse():

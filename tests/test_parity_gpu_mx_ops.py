@@ -633,3 +633,93 @@ def test_moe_block(T):
     assert torch.equal(got_total.cpu(), total)
     ref, bound = mx_ref.moe(h.cpu(), ids.cpu(), p.cpu(), *(t.cpu() for t in (*q13, *q2)), None, None, "silu")
     mx_ref.check16(out.cpu(), ref, torch.bfloat16, bound)
+
+
+# ---- what all of them share ------------------------------------------------------------------
+
+def test_empty_tensors():
+    """No rows, no columns, no tokens: empty results, nothing launched on them."""
+    x = torch.zeros(0, 64, dtype=torch.bfloat16, device="cuda")
+    w, s = torch.zeros(8, 32, dtype=torch.uint8, device="cuda"), torch.zeros(8, 2, dtype=torch.uint8, device="cuda")
+    y, scale, total = gr.rms_norm(x, residual=x)
+    assert y.shape == (0, 64) and scale.shape == (0, 2) and total.shape == (0, 64)
+    assert gr.rms_norm(x[:, :0], out_format="same")[0].shape == (0, 0)
+    y, scale = gr.gated_act(x, x)
+    assert y.shape == (0, 64) and scale.shape == (0, 2)
+    assert gr.linear_mxfp4(x, w, s).shape == (0, 8)
+    one = torch.zeros(3, 64, dtype=torch.bfloat16, device="cuda")
+    assert gr.linear_mxfp4(one, w[:0], s[:0]).shape == (3, 0)
+    assert gr.gemm_mxfp4(w[:0], s[:0], w, s).shape == (0, 8) and gr.gemm_mxfp4(w, s, w[:0], s[:0]).shape == (8, 0)
+    ids, p = gr.moe_route(x, one, 2)
+    assert ids.shape == p.shape == (0, 2)
+    w13, s13 = torch.zeros(2, 64, 32, dtype=torch.uint8, device="cuda"), torch.zeros(2, 64, 2, dtype=torch.uint8,
+                                                                                  device="cuda")
+    w2, s2 = torch.zeros(2, 64, 16, dtype=torch.uint8, device="cuda"), torch.zeros(2, 64, 1, dtype=torch.uint8,
+                                                                                 device="cuda")
+    assert gr.moe_mxfp4(x, ids, p, w13, s13, w2, s2).shape == (0, 64)
+    torch.cuda.synchronize()
+
+
+def test_empty_intermediate():
+    """Experts without an intermediate dimension leave their biases."""
+    x = torch.ones(3, 64, dtype=torch.bfloat16, device="cuda")
+    none = torch.zeros(2, 0, 32, dtype=torch.uint8, device="cuda"), torch.zeros(2, 0, 2, dtype=torch.uint8, device="cuda")
+    w2, s2 = torch.zeros(2, 64, 0, dtype=torch.uint8, device="cuda"), torch.zeros(2, 64, 0, dtype=torch.uint8,
+                                                                                device="cuda")
+    b2 = inputs(2, 64, "bf16", 130)
+    ids = torch.tensor([[0], [1], [-1]], dtype=torch.int32, device="cuda")
+    out = gr.moe_mxfp4(x, ids, torch.ones(3, 1, device="cuda"), *none, w2, s2, b2=b2.cuda()).cpu()
+    assert torch.equal(out[:2], b2) and bool((out[2] == 0).all())
+
+
+def test_streams():
+    """On a stream given as an object or as a handle, new tensors included: the same bits as on the current one."""
+    x, r = inputs(5, 512, "bf16", 140).cuda(), inputs(5, 512, "bf16", 141).cuda()
+    (w, s), (w13, s13), (w2, s2) = weights((96,), 512, 142), weights((4, 128), 512, 143), weights((4, 512), 64, 144)
+    dev = [t.cuda() for t in (w, s, w13, s13, w2, s2)]
+    router = inputs(4, 512, "bf16", 145).cuda()
+
+    def step(**kw):
+        y, _, total = gr.rms_norm(x, None, r, out_format="same", **kw)
+        ids, p = gr.moe_route(y, router, 2, **kw)
+        z = gr.moe_mxfp4(y, ids, p, *dev[2:], **kw)
+        q, scale = gr.mx_quantize(z, "mxfp4", **kw)
+        g, _ = gr.gated_act(z, total, "silu", "same", **kw)
+        return gr.linear_mxfp4(g, *dev[:2], **kw), gr.gemm_mxfp4(q, scale, *dev[:2], **kw)
+
+    want = [t.cpu() for t in step()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        side = torch.cuda.Stream()
+        for stream in (side, side.cuda_stream):
+            got = step(stream=stream)
+            side.synchronize()
+            for a, b in zip(got, want):
+                assert torch.equal(a.cpu().view(torch.int16), b.view(torch.int16))
+
+
+def test_offsets_beyond_32_bits():
+    """Rows more than 2^32 bytes apart, in the activations and over all rows of the weights."""
+    pitch = (1 << 31) + 24
+    buf = torch.empty(2 * pitch + 4096, dtype=torch.bfloat16, device="cuda")
+    x = inputs(3, 512, "bf16", 150)
+    vx = buf.as_strided((3, 512), (pitch, 1))
+    vx.copy_(x)
+    y, scale, _ = gr.rms_norm(vx)
+    s, ref = norm_ref(x, None, None, 1e-6)
+    mx_ref.check_mx(y.cpu(), scale.cpu(), ref, "mxfp8", NORM)
+    y, scale = gr.mx_quantize(vx, "mxfp4")
+    q, e = mx_ref.quantise(x.double(), "mxfp4")
+    assert torch.equal(mx_ref.elements(y.cpu(), "mxfp4"), q) and torch.equal(scale.cpu().int() - 127, e)
+    N, step = 300, 1 << 24
+    w, ws = weights((N,), 512, 151)
+    wide = buf.view(torch.uint8).as_strided((N, 256), (step, 1), 4096)
+    wide.copy_(w)
+    vx = inputs(3, 512, "bf16", 152).cuda()
+    out = gr.linear_mxfp4(vx, wide, ws.cuda())
+    ref, mag = mx_ref.linear(vx.cpu(), w, ws)
+    mx_ref.check16(out.cpu(), ref, torch.bfloat16, mag * mx_ref.sum_bound(512))
+    out = gr.gemm_mxfp4(*gr.mx_quantize(vx, "mxfp4"), wide, ws.cuda(), act="none", out_dtype=torch.bfloat16)
+    q, e = mx_ref.quantise(vx.cpu().double(), "mxfp4")
+    a, b = q * torch.pow(2.0, e.double()).repeat_interleave(32, -1), mx_ref.weight(w, ws)
+    mx_ref.check16(out.cpu(), a @ b.T, torch.bfloat16, (a.abs() @ b.abs().T) * (2.0 ** -16 + mx_ref.sum_bound(512)))
