@@ -374,6 +374,13 @@ def test_fp4_product(M, N, K, dtype):
     check_fp4(M, N, K, dtype)
 
 
+@pytest.mark.parametrize("strips", [1, 2, 3, 4, 5, 6, 7, 8, 9, 16, 31])
+@pytest.mark.parametrize("M,N", [(130, 200), (128, 256)])
+def test_fp4_product_tiles(M, N, strips):
+    """The 128 x 128 tiles: whole ones and edges, every remainder of their ring of strips."""
+    check_fp4(M, N, 128 * strips, "f16" if strips % 2 else "bf16", path=gr.GR_PATH_TILE)
+
+
 @pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu", "sigmoid", "tanh"])
 def test_fp4_product_epilogue(act):
     check_fp4(21, 37, 352, "f16", act, True)
