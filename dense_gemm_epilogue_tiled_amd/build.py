@@ -59,7 +59,8 @@ def build_tensors(verbose: bool = False) -> str:
               "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
               "-I", os.path.join(root, "include"), "-I", sysconfig.get_paths()["include"],
               "-I", os.path.join(ROOT, "include"), TENSORS, "-L", HERE, "-l:" + os.path.basename(LIB),
-              "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+              "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+              "-ltorch_hip", "-lc10",
               "-Wl,-rpath,$ORIGIN", "-o", tmp], verbose, EXT)
         os.replace(tmp, EXT)
     finally:

@@ -36,7 +36,6 @@
 namespace gr {
 namespace w4 {
 
-using mx::u32_any;
 using mx::u32x2_any;
 using mx::u32x4_any;
 

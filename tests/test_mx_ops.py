@@ -188,8 +188,8 @@ def test_workspace_sizes_of_the_products_and_the_router():
 
 
 def test_streaming_kernels_keep_to_registers():
-    """The kernels whose K is held at once use no more than a few spill slots, none of them in the streaming
-    loop (a reload there waits for every load in flight): checked with the compiler's resource report."""
+    """At most 16 registers of any kernel are spilled (the streaming kernels' spills surround their loops; a reload
+    within waits for every load in flight): checked with the compiler's resource report."""
     import os
     import re
     import subprocess
