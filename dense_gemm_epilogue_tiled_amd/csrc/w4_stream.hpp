@@ -280,7 +280,7 @@ template <int NW, int MT, int TB, int BUFS, bool PASSES>
 struct Lds {
     float part[BUFS][TB * MT][NW][256];
     float sum[PASSES ? kSumTiles * 256 : 1];
-    int again;  // a wave met codes that the conversion cannot apply
+    int again[NW];  // of each wave: it met codes that the conversion cannot apply
 };
 
 // A few rows of one column of a result.  One per thread for 16 rows of X: more would
@@ -321,7 +321,6 @@ __device__ __forceinline__ bool stream_units_by(const P& p, Lds<NW, MT, TB, BUFS
     const int groups = NW / kw, group = wave / kw, part_of = wave % kw;  // powers of two
     const int64_t span = (int64_t)kw * (128 * ST);
     const auto ahead = p.early(u0, u1);
-    if (!ANY && threadIdx.x == 0) lds.again = 0;
     bool bad = false;
     int parity = 0;
     for (int64_t pass = 0; pass == 0 || (PASSES && pass * span < p.K); ++pass) {
@@ -431,7 +430,8 @@ __device__ __forceinline__ bool stream_units_by(const P& p, Lds<NW, MT, TB, BUFS
                             *(f32x4*)&lds.part[parity][t * MT + mt][wave][lane * 4] = acc[mt];
                     }
                 }
-                if (!ANY && bad && lane == 0) lds.again = 1;
+                // (a word for each wave, which it alone writes: nothing orders the waves before this barrier)
+                if (!ANY && !is_fp4<E> && lane == 0) lds.again[wave] = bad;
                 lds_barrier();
                 constexpr int R = rows_at_once(MT);
                 // what this turn finishes, pairs counted once
@@ -488,9 +488,9 @@ __device__ __forceinline__ bool stream_units_by(const P& p, Lds<NW, MT, TB, BUFS
             }
         }
     }
-    if constexpr (ANY) return false;
-    // (written before the last barrier, if at all; without units there was none)
-    return u0 < u1 && lds.again != 0;
+    if constexpr (ANY || is_fp4<E>) return false;
+    // (every wave's word was written before the last barrier; without units there was none)
+    return u0 < u1 && __ballot(lds.again[lane % NW] != 0) != 0;
 }
 
 template <typename E, int PL, int ST, int NW, int MT, int TB, int BUFS, bool PASSES, typename P>
