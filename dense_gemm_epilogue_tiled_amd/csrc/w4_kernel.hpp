@@ -66,6 +66,7 @@ struct LinearUnits {
     __device__ __forceinline__ const uint16_t* x(const Run&, int, int m, const Range& range) const {
         return m0 + m < a.M ? a.x + (m0 + m) * a.ldx + k0 + range.k : nullptr;
     }
+    __device__ __forceinline__ bool takes(const Range&, int) const { return true; }
     __device__ __forceinline__ int rows(const Run& run, int i) const {
         const int64_t left = a.N - (int64_t)(run.from + i) * 16;
         return left < 16 ? (int)left : 16;
@@ -448,6 +449,7 @@ struct GateUpUnits {
     __device__ __forceinline__ const uint16_t* x(const MoeRun& run, int, int m, const Range& range) const {
         return m < run.pairs ? a.x + (t0 + r.token[run.row + m]) * a.ldx + range.k : nullptr;
     }
+    __device__ __forceinline__ bool takes(const Range&, int) const { return true; }
     __device__ __forceinline__ int rows(const MoeRun&, int) const { return 16; }  // H and I are multiples of 16
     __device__ __forceinline__ Tile tile(const MoeRun& run, int i, const Range& range) const {
         const int64_t n = (2 * (int64_t)run.expert + i % 2) * a.I + run.col + i / 2 * 16;
@@ -500,6 +502,7 @@ struct DownUnits {
     __device__ __forceinline__ const uint16_t* x(const MoeRun& run, int plane, int m, const Range& range) const {
         return m < run.pairs ? a.h + (plane * (a.T * a.topk) + first + run.row + m) * a.I + range.k : nullptr;
     }
+    __device__ __forceinline__ bool takes(const Range&, int) const { return true; }
     __device__ __forceinline__ int rows(const MoeRun&, int) const { return 16; }  // H and I are multiples of 16
     __device__ __forceinline__ Tile tile(const MoeRun& run, int i, const Range& range) const {
         const int64_t n = (int64_t)run.expert * a.H + run.col + i * 16;
@@ -554,8 +557,10 @@ struct DownFewUnits {
         const int e = __builtin_amdgcn_readfirstlane(r.expert[slot]);
         return {at, a.I - at, e, __builtin_amdgcn_readfirstlane(r.row[slot]), r.tokens[e]};
     }
+    // (a token's h is 0 in the parts of the experts that it did not choose)
+    __device__ __forceinline__ bool takes(const Range& range, int m) const { return (range.tokens >> m & 1) != 0; }
     __device__ __forceinline__ const uint16_t* x(const Run&, int plane, int m, const Range& range) const {
-        if ((range.tokens >> m & 1) == 0) return nullptr;
+        if (!takes(range, m)) return nullptr;
         const int row = range.row + __popcll(range.tokens & ((1ull << m) - 1));
         return a.h + (plane * (a.T * a.topk) + row) * a.I + range.k;
     }

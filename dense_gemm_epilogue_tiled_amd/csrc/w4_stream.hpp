@@ -238,10 +238,11 @@ __device__ __forceinline__ void multiply_fp4(const u32x4& wi, const Scales<ElemF
 }
 
 // The same for any codes, block by block: the groups that hold the other blocks put
-// zeros on both sides.
-template <typename E, int MT, int PL, int ST>
+// zeros on both sides.  takes(m): whether row m of X takes part in the range; a NaN scale
+// stays away from rows that only have zeros there because it does not.
+template <typename E, int MT, int PL, int ST, typename F>
 __device__ __forceinline__ void multiply_any(const u32x4& wi, const Scales<E, ST>& s, int i,
-                                             const Rows<E, MT, PL, ST>& r, f32x4 (&acc)[MT], int g) {
+                                             const Rows<E, MT, PL, ST>& r, f32x4 (&acc)[MT], int g, F takes) {
     const u32x4 zero = {0u, 0u, 0u, 0u};
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
@@ -261,7 +262,8 @@ __device__ __forceinline__ void multiply_any(const u32x4& wi, const Scales<E, ST
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                acc[mt][k] += code == 255 ? __builtin_nanf("") : __builtin_amdgcn_ldexpf(t[mt][k], code - s.ref);
+                acc[mt][k] += code == 255 && takes(mt * 16 + 4 * g + k) ? __builtin_nanf("")
+                                                                     : __builtin_amdgcn_ldexpf(t[mt][k], code - s.ref);
     }
 }
 
@@ -300,6 +302,7 @@ constexpr int rows_at_once(int MT) { return MT == 1 ? 1 : 4; }
 //                             is the first unit with other rows of X
 //   range(k)                  where the k from k on are: range.left of them from there
 //   x(run, plane, m, range)   row m of X from the range on, or nullptr
+//   takes(range, m)           whether row m of X, if there is one, has a part in the range
 //   tile(run, i, range)       the run's i-th unit from the range on
 //   rows(run, i)              the number of its rows
 //   K, ldw, lds               in k and bytes
@@ -411,7 +414,8 @@ __device__ __forceinline__ bool stream_units_by(const P& p, Lds<NW, MT, TB, BUFS
 #pragma unroll
                                 for (int i = 0; i < ST; ++i) {
                                     if constexpr (ANY)
-                                        multiply_any<E, MT, PL, ST>(w[d][i], scales, i, rows, acc, g);
+                                        multiply_any<E, MT, PL, ST>(w[d][i], scales, i, rows, acc, g,
+                                                                    [&](int m) { return p.takes(range, m); });
                                     else
                                         multiply<E, MT, PL, ST>(w[d][i], scales, i, rows, acc);
                                     more(i);

@@ -30,3 +30,25 @@ def test_one_wave_alone_meets_an_unusual_scale(K, waves):
         assert bool(out[:, 9].isnan().all())
         keep = [n for n in range(N) if n != 9]
         mx_ref.check16(out[:, keep], ref[:, keep], x.dtype, mag[:, keep] * mx_ref.sum_bound(K))
+
+
+@pytest.mark.parametrize("I", [64, 1280])
+@pytest.mark.parametrize("T", [1, 4, 16])
+def test_moe_nan_scale_of_few_tokens(T, I):
+    """A NaN scale of one expert stays with the tokens that chose it where all tokens share the second product's tile, in
+    one pass over the experts (I = 64) and in two (1280)."""
+    log("moe nan scale T=%d I=%d" % (T, I))
+    H, E = 128, 4
+    x = inputs(T, H, "bf16", 210)
+    (w13, s13), (w2, s2) = weights((E, 2 * I), H, 211), weights((E, H), I, 212)
+    s2[1, 3, 0] = 255
+    ids = torch.tensor([[(t + 1) % 4, 0 if (t + 1) % 4 else 2] for t in range(T)], dtype=torch.int32)
+    p = torch.rand(T, 2, generator=torch.Generator().manual_seed(213))
+    out = gr.moe_mxfp4(*(t.cuda() for t in (x, ids, p, w13, s13, w2, s2))).cpu()
+    want = torch.zeros(T, H, dtype=torch.bool)
+    want[(ids == 1).any(1), 3] = True
+    assert torch.equal(out.isnan(), want)
+    ref, bound = mx_ref.moe(x, ids, p, w13, s13, w2, s2, None, None, "silu")
+    zero = torch.zeros(T, H, dtype=torch.float64)
+    mx_ref.check16(torch.where(want, zero, out.double()), torch.where(want, zero, ref), x.dtype,
+                   torch.where(want, zero, bound))
