@@ -5,7 +5,8 @@
 //
 // Each function returns its tensors, or the C call's status if that is not GR_OK,
 // and raises TypeError or ValueError for tensors that do not fit.  The caller has
-// made the first tensor's device current and passes the stream's handle last.
+// made the first tensor's device current and passes the stream's handle last.  That the
+// tensors are on a GPU is checked after everything else that can be said of them.
 
 #include <Python.h>
 
@@ -64,12 +65,20 @@ void* stream_of(PyObject* o) {
 
 int format_of(at::ScalarType t) { return t == at::kBFloat16 ? GR_FMT_BF16 : (t == at::kHalf ? GR_FMT_F16 : -1); }
 
-// Row pitch of a 2-D tensor with unit column stride.
+// Row pitch of a 2-D tensor with unit column stride.  Rows that share memory (an
+// expanded tensor has the row stride 0) have no pitch.
 int64_t pitch_of(const Tensor& t, const char* what) {
     const int64_t rows = t.size(0), cols = t.size(1);
     if (cols > 1 && rows > 0 && t.stride(1) != 1) bad_value(std::string(what) + " needs unit column stride");
-    if (rows > 1) return t.stride(0) > 0 ? t.stride(0) : 1;
-    return cols > 0 ? cols : 1;
+    if (rows < 2 || cols == 0) return cols > 0 ? cols : 1;
+    if (t.stride(0) < cols)
+        bad_value(std::string(what) + " has rows that share memory: row stride " + std::to_string(t.stride(0)) + " for " +
+                  std::to_string(cols) + " columns");
+    return t.stride(0);
+}
+
+void on_gpu(const Tensor& t, const char* what) {
+    if (!t.is_cuda()) bad_value(std::string(what) + " must be a GPU tensor");
 }
 
 template <typename T>
@@ -77,7 +86,7 @@ T* data_of(const Tensor& t) {
     return static_cast<T*>(t.data_ptr());
 }
 
-// A 16-bit matrix on the GPU.
+// A 16-bit matrix.
 struct Matrix {
     const Tensor& t;
     int fmt;
@@ -88,7 +97,6 @@ struct Matrix {
         fmt = format_of(t.scalar_type());
         if (fmt < 0) bad_type(std::string(what) + " must be float16 or bfloat16, got " + c10::toString(t.scalar_type()));
         if (t.dim() != 2) bad_value(std::string(what) + " must be 2-D");
-        if (!t.is_cuda()) bad_value(std::string(what) + " must be a GPU tensor");
         rows = t.size(0);
         cols = t.size(1);
         ld = pitch_of(t, what);
@@ -128,6 +136,7 @@ const T* vector_of(PyObject* o, const Tensor& like, int64_t n, at::ScalarType ki
 // A new tensor next to `like`, by the function behind torch.empty: some of these calls
 // make three.
 Tensor empty_like(const Tensor& like, at::IntArrayRef shape, at::ScalarType kind) {
+    on_gpu(like, "the operand");
     return at::detail::empty_cuda(shape, kind, like.device(), c10::nullopt);
 }
 
@@ -259,6 +268,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
             bad_value("sum_out needs a residual");
         }
         const Rounded y(a[5], a[6], x.t, code);
+        on_gpu(x.t, "x");
         const int st = rms_norm_mx(x.rows, x.cols, x.data, x.ld, r ? data_of<uint16_t>(*r) : nullptr, ldr, w,
                                    (float)eps, r ? data_of<uint16_t>(sum) : nullptr, lds, y.y.data_ptr(), y.ldy,
                                    y.scales(), y.ld_sy, x.fmt, code, stream_of(a[8]));
@@ -274,6 +284,7 @@ PyObject* gated_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t ldu = u ? matching(*u, g.t, g.rows, g.cols, g.t.scalar_type(), "up") : 1;
         const int act = (int)int_of(a[2]), code = (int)int_of(a[3]);
         const Rounded y(a[4], a[5], g.t, code);
+        on_gpu(g.t, "gate");
         const int st = gated_act_mx(g.rows, g.cols, g.data, g.ld, u ? data_of<uint16_t>(*u) : nullptr, ldu, act,
                                     y.y.data_ptr(), y.ldy, y.scales(), y.ld_sy, g.fmt, code, stream_of(a[6]));
         return st == GR_OK ? tuple_of({&y.y, &y.scale}) : PyLong_FromLong(st);
@@ -313,6 +324,7 @@ PyObject* linear_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const uint16_t* bias = vector_of<uint16_t>(a[3], x.t, w.rows, kind, "bias");
         const int act = (int)int_of(a[4]);
         const Output c(a[5], x.t, x.rows, w.rows, kind, "out");
+        on_gpu(x.t, "x");
         int64_t need = 0;
         int st = gemm_w4_bt_workspace_size(x.rows, w.rows, x.cols, &need);
         if (st != GR_OK) return PyLong_FromLong(st);
@@ -328,7 +340,6 @@ PyObject* gemm_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return entry(n, 10, [&]() -> PyObject* {
         const Tensor& at_ = tensor_of(a[0], "a");
         if (at_.dim() != 2) bad_value("a must be 2-D");
-        if (!at_.is_cuda()) bad_value("a must be a GPU tensor");
         const int64_t K = at_.size(1) * 2;
         const Fp4 x(a[0], a[1], at_, K, "a"), w(a[2], a[3], at_, K, "bt");
         const int fmt = (int)int_of(a[6]);
@@ -336,6 +347,7 @@ PyObject* gemm_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Output c(a[7], at_, x.rows, w.rows, kind, "out");
         const uint16_t* bias = vector_of<uint16_t>(a[4], at_, w.rows, kind, "bias");
         const int act = (int)int_of(a[5]), path = (int)int_of(a[8]);
+        on_gpu(at_, "a");
         uint16_t* const to = data_of<uint16_t>(c.t);
         const int st = path < 0 ? gemm_mxfp4_linear_bt(x.rows, w.rows, K, x.data, x.ld, x.scale, x.ld_s, w.data, w.ld, w.scale,
                                                 w.ld_s, bias, act, to, c.ld, fmt, stream_of(a[9]))
@@ -357,6 +369,7 @@ PyObject* moe_route_(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t ldr = matching(r, x.t, E, H, x.t.scalar_type(), "router");
         const float* bias = vector_of<float>(a[3], x.t, E, at::kFloat, "bias");
         const int renorm = (int)int_of(a[4]);
+        on_gpu(x.t, "x");
         int64_t need = 0;
         int st = moe_route_workspace_size(T, H, E, &need);
         if (st != GR_OK) return PyLong_FromLong(st);
@@ -401,6 +414,7 @@ PyObject* moe_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const uint16_t* b2 = whole<uint16_t>(a[8], x.t, {E, H}, kind, "b2");
         const int act = (int)int_of(a[9]);
         const Output c(a[10], x.t, T, H, kind, "out");
+        on_gpu(x.t, "x");
         int64_t need = 0;
         int st = moe_w4_workspace_size(T, H, I, E, k, &need);
         if (st != GR_OK) return PyLong_FromLong(st);

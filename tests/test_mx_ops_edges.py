@@ -2,6 +2,9 @@
 import os
 import re
 
+import pytest
+import torch
+
 import dense_gemm_epilogue_tiled_amd as gr
 
 CSRC = os.path.join(os.path.dirname(gr.__file__), "csrc")
@@ -17,3 +20,78 @@ def test_flag_of_unusual_scales_is_written_by_its_wave_alone():
     assert writes == [("[wave]", "bad")]
     at = text.index("lds.again[wave] = bad")
     assert re.match(r"[^;]*;\s*\}?\s*lds_barrier\(\);", text[at:])
+
+
+# ---- the tensor helpers' checks, called as mx_ops calls them but with CPU tensors, which they refuse last -------------
+
+def helpers():
+    if gr.mx_ops._c is None:
+        gr.mx_ops._init()
+    return gr.mx_ops._c
+
+
+def zeros(*shape, dtype=torch.bfloat16):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def bytes_(*shape):
+    return zeros(*shape, dtype=torch.uint8)
+
+
+def norm(x=None, weight=None, residual=None, code=gr.GR_OUT_16, out=None, scale_out=None, sum_out=None):
+    return helpers().rms_norm(zeros(4, 1) if x is None else x, weight, residual, 1e-6, code, out, scale_out, sum_out, 0)
+
+
+def gated(gate=None, up=None, code=gr.GR_OUT_16, out=None, scale_out=None):
+    return helpers().gated_act(zeros(4, 1) if gate is None else gate, up, gr.GR_ACT_SILU, code, out, scale_out, 0)
+
+
+def linear(x=None, w=None, s=None, bias=None, out=None):
+    return helpers().linear_mxfp4(zeros(4, 32) if x is None else x, bytes_(8, 16) if w is None else w,
+                                  bytes_(8, 1) if s is None else s, bias, gr.GR_ACT_NONE, out, None, 0)
+
+
+def fp4(a=None, sa=None, b=None, sb=None, bias=None, out=None):
+    return helpers().gemm_mxfp4(bytes_(4, 16) if a is None else a, bytes_(4, 1) if sa is None else sa,
+                                bytes_(8, 16) if b is None else b, bytes_(8, 1) if sb is None else sb, bias,
+                                gr.GR_ACT_NONE, gr.GR_FMT_BF16, out, -1, 0)
+
+
+def route(x=None, router=None, bias=None):
+    return helpers().moe_route(zeros(4, 1) if x is None else x, zeros(8, 1) if router is None else router, 2, bias, 1,
+                               None, 0)
+
+
+def moe(x=None, p=None, b2=None, out=None):
+    return helpers().moe_mxfp4(zeros(4, 32) if x is None else x, zeros(4, 2, dtype=torch.int32),
+                               zeros(4, 2, dtype=torch.float32) if p is None else p, bytes_(3, 64, 16), bytes_(3, 64, 1),
+                               bytes_(3, 32, 16), bytes_(3, 32, 1), None, b2, gr.GR_ACT_SILU, out, None, 0)
+
+
+one = zeros(1, 1).expand(4, 1)  # four rows in one element
+one8 = bytes_(1, 1).expand(8, 1)
+
+SHARED_ROWS = [(norm, dict(x=one)), (norm, dict(residual=one)), (norm, dict(out=one)),
+               (norm, dict(residual=zeros(4, 1), sum_out=one)),
+               (norm, dict(x=zeros(4, 32), code=gr.GR_OUT_MXFP8, out=zeros(4, 32, dtype=torch.float8_e4m3fn), scale_out=one8[:4])),
+               (gated, dict(gate=one)), (gated, dict(up=one)), (gated, dict(out=one)),
+               (linear, dict(s=one8)), (linear, dict(w=bytes_(1, 16).expand(8, 16))),
+               (linear, dict(x=zeros(1, 32).expand(4, 32))),
+               (linear, dict(w=bytes_(1, 16), s=bytes_(1, 1), out=one)),
+               (linear, dict(out=torch.as_strided(zeros(64), (4, 8), (7, 1)))),
+               (fp4, dict(sa=one8[:4])), (fp4, dict(sb=one8)), (fp4, dict(b=bytes_(1, 16), sb=bytes_(1, 1), out=one)),
+               (route, dict(x=one)), (route, dict(router=zeros(1, 1).expand(8, 1))),
+               (moe, dict(x=zeros(1, 32).expand(4, 32))), (moe, dict(out=zeros(1, 32).expand(4, 32)))]
+
+
+@pytest.mark.parametrize("call,args", SHARED_ROWS, ids=lambda v: v.__name__ if callable(v) else "-".join(v))
+def test_rows_that_share_memory_are_refused(call, args):
+    """Expanded tensors have a row stride of 0: read as rows one after the other they would go out of their memory."""
+    with pytest.raises(ValueError, match="row stride"):
+        call(**args)
+
+
+@pytest.mark.parametrize("call", [norm, gated, linear, fp4, route, moe])
+def test_cpu_tensors_are_refused(call):
+    with pytest.raises(ValueError, match="GPU"):
+        call()
