@@ -474,6 +474,13 @@ def _stream_handle(stream):
     return stream.cuda_stream
 
 
+def _pitch(t):
+    """Row pitch of a 2-D tensor.  Rows that share memory keep their stride (0 where expanded), which the library
+    refuses."""
+    rows, cols = t.shape
+    return t.stride(0) if rows > 1 and cols > 0 else max(cols, 1)
+
+
 def gemm_relu_bt(a, bt, out=None, stream=None, path=None):
     """Tensor convenience: ``out = ReLU(a @ bt.T)`` with the second operand
     given transposed (``bt`` is N x K, as a linear layer's weight), 2-D fp16
@@ -490,9 +497,9 @@ def gemm_relu_bt(a, bt, out=None, stream=None, path=None):
     for t in (a, bt, out):
         if t.numel() and t.stride(1) != 1:
             raise ValueError("tensors need unit column stride")
-    lda = max(a.stride(0), 1) if M > 1 else max(K, 1)
-    ldbt = max(bt.stride(0), 1) if N > 1 else max(K, 1)
-    ldc = max(out.stride(0), 1) if M > 1 else max(N, 1)
+    lda = _pitch(a)
+    ldbt = _pitch(bt)
+    ldc = _pitch(out)
     h = _stream_handle(stream)
     args = (M, N, K, a.data_ptr(), lda, bt.data_ptr(), ldbt, out.data_ptr(), ldc, h)
     st = gemm_relu_f16_bt(*args) if path is None else gemm_relu_f16_bt_forced(*args, path)
@@ -525,9 +532,9 @@ def gemm_relu(a, b, out=None, stream=None, path=None, workspace="auto"):
     for t in (a, b, out):
         if t.numel() and t.stride(1) != 1:
             raise ValueError("tensors need unit column stride")
-    lda = max(a.stride(0), 1) if M > 1 else max(K, 1)
-    ldb = max(b.stride(0), 1) if K > 1 else max(N, 1)
-    ldc = max(out.stride(0), 1) if M > 1 else max(N, 1)
+    lda = _pitch(a)
+    ldb = _pitch(b)
+    ldc = _pitch(out)
     args = (M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb, out.data_ptr(), ldc)
     workspace = _workspace_for(torch, args, workspace, a.device, stream)
     ws_ptr, ws_bytes = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (0, 0)
@@ -590,9 +597,9 @@ def gemm_bias_act(a, b, bias=None, act="gelu", out=None, stream=None, path=None,
     for t in (a, b, out):
         if t.numel() and t.stride(1) != 1:
             raise ValueError("tensors need unit column stride")
-    lda = max(a.stride(0), 1) if M > 1 else max(K, 1)
-    ldb = max(b.stride(0), 1) if K > 1 else max(N, 1)
-    ldc = max(out.stride(0), 1) if M > 1 else max(N, 1)
+    lda = _pitch(a)
+    ldb = _pitch(b)
+    ldc = _pitch(out)
     bptr = bias.data_ptr() if bias is not None and bias.numel() else None
     h = _stream_handle(stream)
     ws = _workspace_for(torch, (M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb, out.data_ptr(), ldc), workspace,
@@ -636,9 +643,9 @@ def gemm_fp8(a, bt, scale_a=1.0, scale_b=1.0, bias=None, act="relu", out_dtype=N
     for t in (a, bt, out):
         if t.numel() and t.stride(1) != 1:
             raise ValueError("tensors need unit column stride")
-    lda = max(a.stride(0), 1) if M > 1 else max(K, 1)
-    ldbt = max(bt.stride(0), 1) if N > 1 else max(K, 1)
-    ldc = max(out.stride(0), 1) if M > 1 else max(N, 1)
+    lda = _pitch(a)
+    ldbt = _pitch(bt)
+    ldc = _pitch(out)
     code = ACT_CODES[act] if isinstance(act, str) else int(act)
     bptr = bias.data_ptr() if bias is not None and bias.numel() else None
     if isinstance(workspace, str):
@@ -693,11 +700,11 @@ def gemm_mxfp8(a, scale_a, bt, scale_b, bias=None, act="relu", out_dtype=None, o
     for t in (a, bt, scale_a, scale_b, out):
         if t.numel() and t.stride(1) != 1:
             raise ValueError("tensors need unit column stride")
-    lda = max(a.stride(0), 1) if M > 1 else max(K, 1)
-    ldbt = max(bt.stride(0), 1) if N > 1 else max(K, 1)
-    ldsa = max(scale_a.stride(0), 1) if M > 1 else max(K // 32, 1)
-    ldsb = max(scale_b.stride(0), 1) if N > 1 else max(K // 32, 1)
-    ldc = max(out.stride(0), 1) if M > 1 else max(N, 1)
+    lda = _pitch(a)
+    ldbt = _pitch(bt)
+    ldsa = _pitch(scale_a)
+    ldsb = _pitch(scale_b)
+    ldc = _pitch(out)
     code = ACT_CODES[act] if isinstance(act, str) else int(act)
     bptr = bias.data_ptr() if bias is not None and bias.numel() else None
     args = (M, N, K, a.data_ptr(), lda, scale_a.data_ptr(), ldsa, bt.data_ptr(), ldbt, scale_b.data_ptr(), ldsb, bptr,
@@ -732,9 +739,9 @@ def linear(x, weight, bias=None, act="none", out=None, stream=None, path=None):
     for t in (x, weight, out):
         if t.numel() and t.stride(1) != 1:
             raise ValueError("tensors need unit column stride")
-    lda = max(x.stride(0), 1) if M > 1 else max(K, 1)
-    ldbt = max(weight.stride(0), 1) if N > 1 else max(K, 1)
-    ldc = max(out.stride(0), 1) if M > 1 else max(N, 1)
+    lda = _pitch(x)
+    ldbt = _pitch(weight)
+    ldc = _pitch(out)
     bptr = bias.data_ptr() if bias is not None and bias.numel() else None
     fmt = GR_FMT_BF16 if x.dtype == torch.bfloat16 else GR_FMT_F16
     st = gemm_bias_act_bt(M, N, K, x.data_ptr(), lda, weight.data_ptr(), ldbt, bptr, code, out.data_ptr(), ldc, fmt,
