@@ -481,6 +481,11 @@ def _pitch(t):
     return t.stride(0) if rows > 1 and cols > 0 else max(cols, 1)
 
 
+def _holds(out, M, N):
+    if out.dim() != 2 or out.shape[0] < M or out.shape[1] < N:
+        raise ValueError("out %s does not hold %d x %d" % (tuple(out.shape), M, N))
+
+
 def gemm_relu_bt(a, bt, out=None, stream=None, path=None):
     """Tensor convenience: ``out = ReLU(a @ bt.T)`` with the second operand
     given transposed (``bt`` is N x K, as a linear layer's weight), 2-D fp16
@@ -494,6 +499,7 @@ def gemm_relu_bt(a, bt, out=None, stream=None, path=None):
     N = bt.shape[0]
     if out is None:
         out = torch.empty((M, N), dtype=torch.float16, device=a.device)
+    _holds(out, M, N)
     for t in (a, bt, out):
         if t.numel() and t.stride(1) != 1:
             raise ValueError("tensors need unit column stride")
@@ -529,6 +535,7 @@ def gemm_relu(a, b, out=None, stream=None, path=None, workspace="auto"):
         out = torch.empty((M, N), dtype=a.dtype, device=a.device)
     elif out.dtype != a.dtype:
         raise TypeError("out must have the operands' dtype")
+    _holds(out, M, N)
     for t in (a, b, out):
         if t.numel() and t.stride(1) != 1:
             raise ValueError("tensors need unit column stride")
@@ -594,6 +601,7 @@ def gemm_bias_act(a, b, bias=None, act="gelu", out=None, stream=None, path=None,
         out = torch.empty((M, N), dtype=a.dtype, device=a.device)
     elif out.dtype != a.dtype:
         raise TypeError("out must have the operands' dtype")
+    _holds(out, M, N)
     for t in (a, b, out):
         if t.numel() and t.stride(1) != 1:
             raise ValueError("tensors need unit column stride")
@@ -640,6 +648,7 @@ def gemm_fp8(a, bt, scale_a=1.0, scale_b=1.0, bias=None, act="relu", out_dtype=N
         raise ValueError("bias must be a contiguous 1-D tensor of N values of the output dtype")
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+    _holds(out, M, N)
     for t in (a, bt, out):
         if t.numel() and t.stride(1) != 1:
             raise ValueError("tensors need unit column stride")
@@ -697,6 +706,7 @@ def gemm_mxfp8(a, scale_a, bt, scale_b, bias=None, act="relu", out_dtype=None, o
         raise ValueError("bias must be a contiguous 1-D tensor of N values of the output dtype")
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+    _holds(out, M, N)
     for t in (a, bt, scale_a, scale_b, out):
         if t.numel() and t.stride(1) != 1:
             raise ValueError("tensors need unit column stride")
@@ -736,6 +746,7 @@ def linear(x, weight, bias=None, act="none", out=None, stream=None, path=None):
         out = torch.empty((M, N), dtype=x.dtype, device=x.device)
     elif out.dtype != x.dtype:
         raise TypeError("out must have x's dtype")
+    _holds(out, M, N)
     for t in (x, weight, out):
         if t.numel() and t.stride(1) != 1:
             raise ValueError("tensors need unit column stride")

@@ -48,3 +48,18 @@ def test_rows_that_share_memory_are_refused(name):
     with pytest.raises(gr.GemmReluError) as e:
         CASES[name]()
     assert e.value.status == gr.GR_ERR_INVALID_LD
+
+
+@pytest.mark.parametrize("shape", [(3, 5), (4, 4), (1, 1), (20,)])
+@pytest.mark.parametrize("name,call", [
+    ("gemm_relu_bt", lambda out: gr.gemm_relu_bt(z(4, 8), z(5, 8), out=out, stream=0)),
+    ("gemm_relu", lambda out: gr.gemm_relu(z(4, 8), z(8, 5), out=out, workspace=None, stream=0)),
+    ("gemm_bias_act", lambda out: gr.gemm_bias_act(z(4, 8), z(8, 5), out=out, workspace=None, stream=0)),
+    ("gemm_fp8", lambda out: gr.gemm_fp8(z(4, 8, dtype=E4), z(5, 8, dtype=E4), out=out, workspace=None, stream=0)),
+    ("gemm_mxfp8", lambda out: gr.gemm_mxfp8(z(4, 32, dtype=E4), z(4, 1, dtype=B8), z(5, 32, dtype=E4),
+                                             z(5, 1, dtype=B8), out=out, stream=0)),
+    ("linear", lambda out: gr.linear(z(4, 8), z(5, 8), out=out, stream=0))], ids=lambda v: v if isinstance(v, str) else "")
+def test_output_too_small_is_refused(name, call, shape):
+    """A 4 x 5 product does not go into fewer rows or columns."""
+    with pytest.raises(ValueError, match="out"):
+        call(z(*shape))
