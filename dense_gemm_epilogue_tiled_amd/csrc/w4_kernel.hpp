@@ -430,6 +430,8 @@ __device__ __forceinline__ Items items_of(int pair_tiles, int tiles) {
     return {tile * tiles + (int)((int64_t)tiles * part / each), tile * tiles + (int)((int64_t)tiles * (part + 1) / each)};
 }
 
+constexpr float kBf16Max = 0x1.FEp127f;
+
 // Units of the first product: 16 columns of h for a tile of pairs, gate and up.
 template <typename E>
 struct GateUpUnits {
@@ -465,10 +467,13 @@ struct GateUpUnits {
             v += E::widen(a.b13[(2 * (int64_t)run.expert + 1) * a.I + col]);
         }
         const float h = mx::exact_activate(g, a.act) * v * r.weight[run.row + m];
-        const uint16_t high = to_bf16(h);
+        // (a finite h never has an infinite high part, and an infinite one has no low part)
+        const float high = __builtin_amdgcn_fmed3f(h, -kBf16Max, kBf16Max);
+        const bool finite = __builtin_fabsf(h) < __builtin_inff();
+        const uint16_t part = to_bf16(finite ? high : h);
         const int64_t to = (t0 * a.topk + run.row + m) * a.I + col;
-        a.h[to] = high;
-        a.h[a.T * a.topk * a.I + to] = to_bf16(h - ElemBF16::widen(high));
+        a.h[to] = part;
+        a.h[a.T * a.topk * a.I + to] = finite ? to_bf16(h - ElemBF16::widen(part)) : 0;
     }
 };
 

@@ -52,3 +52,25 @@ def test_moe_nan_scale_of_few_tokens(T, I):
     zero = torch.zeros(T, H, dtype=torch.float64)
     mx_ref.check16(torch.where(want, zero, out.double()), torch.where(want, zero, ref), x.dtype,
                    torch.where(want, zero, bound))
+
+
+@pytest.mark.parametrize("T", [2, 20])
+def test_moe_hidden_value_beyond_bfloat16(T):
+    """h between the products next to fp32's largest value, which bfloat16 rounds to infinity, and infinite itself."""
+    log("moe large h T=%d" % T)
+    H = I = 32
+    x = torch.zeros(T, H, dtype=torch.bfloat16)
+    x[0, 0] = 2.0 ** 60
+    w13 = torch.full((1, 2 * I, H // 2), 0x22, dtype=torch.uint8)  # ones
+    s13 = torch.full((1, 2 * I, 1), 127 + 4, dtype=torch.uint8)    # g = 2^64
+    s13[0, I:] = 127 + 3                                           # u = 2^63
+    w2 = torch.full((1, H, I // 2), 0x22, dtype=torch.uint8)
+    s2 = torch.full((1, H, 1), 127 - 30, dtype=torch.uint8)
+    ids = torch.zeros(T, 1, dtype=torch.int32)
+    p = torch.full((T, 1), 2.0 - 2.0 ** -9)                        # h = 1.998 * 2^127
+    out = gr.moe_mxfp4(*(t.cuda() for t in (x, ids, p, w13, s13, w2, s2)), act="none").cpu()
+    ref, bound = mx_ref.moe(x, ids, p, w13, s13, w2, s2, None, None, "none")
+    mx_ref.check16(out, ref, x.dtype, bound)
+    s13[0, I:] = 127 + 5                                           # h = 2^129: infinite in fp32
+    out = gr.moe_mxfp4(*(t.cuda() for t in (x, ids, p, w13, s13, w2, s2)), act="none").cpu()
+    assert bool((out[0] == float("inf")).all()) and bool((out[1:] == 0).all())
