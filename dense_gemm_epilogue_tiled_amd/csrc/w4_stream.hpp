@@ -238,7 +238,8 @@ __device__ __forceinline__ void multiply_fp4(const u32x4& wi, const Scales<ElemF
 }
 
 // The same for any codes, block by block: the groups that hold the other blocks put
-// zeros on both sides.  takes(m): whether row m of X takes part in the range; a NaN scale
+// zeros on both sides.  acc is in units of 1 here: next to a small ref a large block would
+// pass fp32's range.  takes(m): whether row m of X takes part in the range; a NaN scale
 // stays away from rows that only have zeros there because it does not.
 template <typename E, int MT, int PL, int ST, typename F>
 __device__ __forceinline__ void multiply_any(const u32x4& wi, const Scales<E, ST>& s, int i,
@@ -263,7 +264,7 @@ __device__ __forceinline__ void multiply_any(const u32x4& wi, const Scales<E, ST
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 acc[mt][k] += code == 255 && takes(mt * 16 + 4 * g + k) ? __builtin_nanf("")
-                                                                     : __builtin_amdgcn_ldexpf(t[mt][k], code - s.ref);
+                                                                     : __builtin_amdgcn_ldexpf(t[mt][k], code - 127);
     }
 }
 
@@ -421,7 +422,7 @@ __device__ __forceinline__ bool stream_units_by(const P& p, Lds<NW, MT, TB, BUFS
                                     more(i);
                                 }
                             }
-                            if constexpr (E::kIsF16) {
+                            if constexpr (E::kIsF16 && !ANY) {
 #pragma unroll
                                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll

@@ -32,6 +32,20 @@ def test_one_wave_alone_meets_an_unusual_scale(K, waves):
         mx_ref.check16(out[:, keep], ref[:, keep], x.dtype, mag[:, keep] * mx_ref.sum_bound(K))
 
 
+def test_linear_far_scales_cancel_f16():
+    """fp16 rows that begin with a small scale: blocks with large ones are finite in fp32 and cancel exactly."""
+    M, N, K = 2, 16, 96
+    x = torch.zeros(M, K, dtype=torch.float16)
+    x[:, 40], x[:, 72] = 1.0, -1.0
+    w, s = weights((N,), K, 220)
+    w[:, 16:] = 0x22
+    s[:, 0], s[:, 1:] = 100, 240
+    out = gr.linear_mxfp4(x.cuda(), w.cuda(), s.cuda()).cpu()
+    assert bool((out == 0).all()), out
+
+
+# ---- experts -------------------------------------------------------------------------------
+
 @pytest.mark.parametrize("I", [64, 1280])
 @pytest.mark.parametrize("T", [1, 4, 16])
 def test_moe_nan_scale_of_few_tokens(T, I):
