@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(NormArgs a) {
 // v / (1 + e^-z) within about an ulp: the exponent's argument in two parts,
 // and the quotient mended by its remainder.  Above z = -126 ln 2 the divisor
 // stays finite; below it the 1 is nothing next to e^-z, and v e^z is taken in
-// two halves, since e^z itself is subnormal.
+// two halves, since e^z itself is subnormal, the second with the argument's second part.
 __device__ __forceinline__ float over_1p_exp(float v, float z) {
     constexpr float kLog2e = 1.44269504088896341f, kLog2eLow = 1.925963033500e-8f, kLn2 = 0.693147180559945309f;
     const float t = -z * kLog2e;
@@ -338,7 +338,7 @@ __device__ __forceinline__ float over_1p_exp(float v, float z) {
     const float q = v * r;
     const float m = __builtin_fmaf(__builtin_fmaf(-q, d, v), r, q);
     const float half = __builtin_amdgcn_exp2f(-0.5f * t);
-    return t > 126.0f ? v * half * half : (m == m ? m : q);
+    return t > 126.0f ? v * half * __builtin_fmaf(-half * kLn2, low, half) : (m == m ? m : q);
 }
 
 // The activations of the C ABI with relative errors of a few fp32 ulp, tails

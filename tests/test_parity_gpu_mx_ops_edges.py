@@ -12,6 +12,18 @@ pytestmark = pytest.mark.gpu
 U = mx_ref.U32
 
 
+# ---- activations -------------------------------------------------------------------------
+
+def test_silu_far_tail():
+    """SiLU below -87, where e^z leaves the normal numbers: 16 roundings as above, at products next to a rounding border."""
+    g = torch.arange(-1468, -1400).double().div(16).half()      # -91.75 .. -87.5
+    u = torch.arange(1024, 3072).half() * 16
+    ref = mx_ref.act(g.double(), "silu")[:, None] * u.double()
+    y, scale = gr.gated_act(g[:, None].expand(ref.shape).contiguous().cuda(), u.expand(ref.shape).contiguous().cuda(),
+                            "silu", "mxfp8")
+    mx_ref.check_mx(y.cpu(), scale.cpu(), ref, "mxfp8", 16 * U)
+
+
 # ---- scales that the conversion cannot apply ----------------------------------------------
 
 @pytest.mark.parametrize("K,waves", [(1024, 8), (8192, 16)])
