@@ -12,6 +12,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/hip/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -41,9 +42,15 @@ std::string shape_text(at::IntArrayRef s) {
 
 // ---- arguments ----------------------------------------------------------------------
 
+// These operators have no gradients: a tensor for which one is being recorded is refused,
+// since its gradient would be lost without a word.
 const Tensor& tensor_of(PyObject* o, const char* what) {
     if (!THPVariable_Check(o)) bad_type(std::string(what) + " must be a tensor");
-    return THPVariable_Unpack(o);
+    const Tensor& t = THPVariable_Unpack(o);
+    if ((c10::GradMode::is_enabled() && t.requires_grad()) || t._fw_grad(0).defined())
+        throw Raise{PyExc_RuntimeError, std::string(what) + " asks for a gradient, and this operator has no gradient: "
+                                            "call it under torch.no_grad() or with a detached tensor"};
+    return t;
 }
 
 // A tensor, or nullptr for None.
@@ -344,8 +351,8 @@ PyObject* gemm_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Fp4 x(a[0], a[1], at_, K, "a"), w(a[2], a[3], at_, K, "bt");
         const int fmt = (int)int_of(a[6]);
         const auto kind = fmt == GR_FMT_BF16 ? at::kBFloat16 : at::kHalf;
-        const Output c(a[7], at_, x.rows, w.rows, kind, "out");
         const uint16_t* bias = vector_of<uint16_t>(a[4], at_, w.rows, kind, "bias");
+        const Output c(a[7], at_, x.rows, w.rows, kind, "out");
         const int act = (int)int_of(a[5]), path = (int)int_of(a[8]);
         on_gpu(at_, "a");
         uint16_t* const to = data_of<uint16_t>(c.t);

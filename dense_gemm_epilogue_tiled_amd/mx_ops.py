@@ -6,7 +6,8 @@ Raw calls (``rms_norm_mx``, ``gated_act_mx``, ``gemm_w4_bt``, ``moe_route_raw``,
 ``moe_w4``) take device pointers and return the C status; the tensor helpers
 take GPU tensors with unit column stride and raise GemmReluError.  MX fp8 data
 is a torch.float8_e4m3fn tensor, MX fp4 data a uint8 tensor of E2M1 pairs (low
-nibble first), scales are uint8 E8M0 codes, one per 32 columns.
+nibble first), scales are uint8 E8M0 codes, one per 32 columns.  There are no
+gradients: in grad mode the tensor helpers refuse tensors that require one.
 """
 from __future__ import annotations
 

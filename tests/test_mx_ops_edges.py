@@ -95,3 +95,40 @@ def test_rows_that_share_memory_are_refused(call, args):
 def test_cpu_tensors_are_refused(call):
     with pytest.raises(ValueError, match="GPU"):
         call()
+
+
+# ---- gradients -----------------------------------------------------------------------------
+
+def wants(*shape, dtype=torch.bfloat16):
+    return zeros(*shape, dtype=dtype).requires_grad_()
+
+
+WANT_GRADIENTS = [(norm, lambda: dict(x=wants(4, 32))), (norm, lambda: dict(weight=wants(1))),
+                  (norm, lambda: dict(residual=wants(4, 1))), (norm, lambda: dict(out=wants(4, 1))),
+                  (gated, lambda: dict(gate=wants(4, 32))), (gated, lambda: dict(up=wants(4, 1))),
+                  (linear, lambda: dict(x=wants(4, 32))), (linear, lambda: dict(bias=wants(8))),
+                  (fp4, lambda: dict(bias=wants(8))), (route, lambda: dict(x=wants(4, 1))),
+                  (route, lambda: dict(router=wants(8, 1))), (route, lambda: dict(bias=wants(8, dtype=torch.float32))),
+                  (moe, lambda: dict(x=wants(4, 32))), (moe, lambda: dict(p=wants(4, 2, dtype=torch.float32))),
+                  (moe, lambda: dict(b2=wants(3, 32)))]
+
+
+@pytest.mark.parametrize("call,args", WANT_GRADIENTS, ids=lambda v: v.__name__ if v in (norm, gated, linear, fp4, route, moe)
+                         else "-".join(v()))
+def test_gradients_are_refused(call, args):
+    """The operators have no gradients: rather than lose one, they refuse a tensor that asks for it. Without recording
+    the call goes on (here to the check for a GPU)."""
+    with pytest.raises(RuntimeError, match="no gradient"):
+        call(**args())
+    with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
+        call(**args())
+
+
+def test_forward_gradients_are_refused():
+    import torch.autograd.forward_ad as fw
+    with fw.dual_level():
+        x = fw.make_dual(zeros(4, 32, dtype=torch.float16), zeros(4, 32, dtype=torch.float16))
+        with pytest.raises(RuntimeError, match="no gradient"):
+            norm(x=x)
+        with pytest.raises(RuntimeError, match="no gradient"):
+            gated(gate=x)
