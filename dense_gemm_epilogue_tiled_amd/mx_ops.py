@@ -96,12 +96,12 @@ def _init():
     import torch
     lib()
     from . import _tensors
-    _c = _tensors
     _FMT = {torch.float16: GR_FMT_F16, torch.bfloat16: GR_FMT_BF16}
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda device: torch.cuda.current_stream(device).cuda_stream)
     _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _torch = torch
+    _c = _tensors  # last: a set _c means that the others are
 
 
 def _run(name, status_name, stream, x, *args):

@@ -132,3 +132,28 @@ def test_forward_gradients_are_refused():
             norm(x=x)
         with pytest.raises(RuntimeError, match="no gradient"):
             gated(gate=x)
+
+
+# ---- first use -------------------------------------------------------------------------------
+
+def test_first_use_is_seen_whole_by_other_threads(monkeypatch):
+    """_run takes a set _c for "ready": at no line of _init may it be set before what _run uses beside it."""
+    import sys
+    ops = gr.mx_ops
+    names = ("_c", "_torch", "_FMT", "_raw_stream", "_device")
+    for n in names:
+        monkeypatch.setattr(ops, n, None)
+    seen = []
+
+    def line(frame, event, arg):
+        if ops._c is not None:
+            seen.append([n for n in names if getattr(ops, n) is None])
+        return line
+
+    before = sys.gettrace()
+    sys.settrace(lambda frame, event, arg: line if frame.f_code is ops._init.__code__ else None)
+    try:
+        ops._init()
+    finally:
+        sys.settrace(before)
+    assert seen and not any(seen), seen
