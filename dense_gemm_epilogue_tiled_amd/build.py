@@ -1,5 +1,6 @@
 """Compile the HIP library for gfx950 (``libgemm_relu.so``, in this package) and the
-tensor helpers on it (``_tensors.so``, host code on torch's headers).
+tensor helpers on it (``_tensors.so``, host code on torch's headers, only where
+torch is installed).
 
 Run as ``python -m dense_gemm_epilogue_tiled_amd.build``. The library is built
 in-tree so the shared object sits next to the Python binding that loads it.
@@ -90,6 +91,11 @@ def build(verbose: bool = False) -> str:
         for obj in objs:
             if os.path.exists(obj):
                 os.remove(obj)
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        print("torch is not there: built without the tensor helpers (%s)" % os.path.basename(EXT), flush=True)
+        return LIB
     build_tensors(verbose)
     return LIB
 

@@ -157,3 +157,36 @@ def test_first_use_is_seen_whole_by_other_threads(monkeypatch):
     finally:
         sys.settrace(before)
     assert seen and not any(seen), seen
+
+
+# ---- build -----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("with_torch", [True, False])
+def test_the_library_builds_without_torch(monkeypatch, tmp_path, with_torch):
+    """The C library and its ctypes binding do without torch, and so does their build; the tensor helpers need it."""
+    import sys
+    from dense_gemm_epilogue_tiled_amd import build as b
+    made = []
+
+    class Job:
+        returncode = 0
+
+        def __init__(self, cmd, **kw):
+            open(cmd[cmd.index("-o") + 1], "w").close()
+
+        def communicate(self):
+            return "", None
+
+    def run(cmd, verbose, what):
+        Job(cmd)
+        made.append(os.path.basename(what))
+
+    monkeypatch.setattr(b.subprocess, "Popen", Job)
+    monkeypatch.setattr(b, "_run", run)
+    monkeypatch.setattr(b, "LIB", str(tmp_path / "lib.so"))
+    monkeypatch.setattr(b, "EXT", str(tmp_path / "ext.so"))
+    if not with_torch:
+        monkeypatch.setitem(sys.modules, "torch", None)  # import torch raises ImportError
+    assert b.build() == b.LIB and os.path.exists(b.LIB)
+    assert made == (["lib.so", "ext.so"] if with_torch else ["lib.so"])
+    assert sorted(os.listdir(tmp_path)) == (["ext.so", "lib.so"] if with_torch else ["lib.so"])
