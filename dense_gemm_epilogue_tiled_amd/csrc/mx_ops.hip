@@ -280,11 +280,11 @@ int run_w4(const gr::w4::LinearArgs& a, const W4Plan& p, hipStream_t stream) {
 // 16 * MT rows a CU reads those rows once and takes `units` tiles of 16 rows of Bt.
 struct Fp4Plan {
     int MT;
-    int64_t units;
+    int64_t units, rounds;
 };
 
 Fp4Plan fp4_plan(int64_t M, int64_t N) {
-    Fp4Plan best{1, 0};
+    Fp4Plan best{1, 0, 0};
     int64_t least = 0;
     for (int MT = 1; MT <= 4; MT *= 2) {
         const int64_t tiles = (M + 16 * MT - 1) / (16 * MT), all = (N + 15) / 16;
@@ -293,23 +293,34 @@ Fp4Plan fp4_plan(int64_t M, int64_t N) {
         const int64_t rounds = (tiles * ((all + units - 1) / units) + kCus - 1) / kCus, rows = rounds * (MT + units);
         if (least == 0 || rows < least) {
             least = rows;
-            best = {MT, units};
+            best = {MT, units, rounds};
         }
     }
     return best;
 }
 
-// Whether the streaming kernel is the faster one: always where gemm_mxfp4_bt has only its
-// guarded kernel (200x4000x2080: 12.7 against 25.1 us); against its 128 x 128
-// tiles, one per CU, where it reads less (4x4096x4096: 4.9 against 10.0 us,
-// 512x4096x4096: 29.9 against 17.3); not where those tiles fill the chip.
+// Whether the streaming kernel is the faster one.  Where gemm_mxfp4_bt has only its guarded
+// kernel (K % 128 != 0, rows at odd addresses), 128 x 128 at a time: by what both were
+// seen to take over 486 sizes, to which the choice below comes within 1% on average.
+// Streaming wins with few tiles and a long K (200x4000x2080 13 against 24 us,
+// 4096x4096x4000 119 against 207), the guarded kernel with many and a short one
+// (4096x4096x544 26 against 79 us, 8192x8192x1056 169 against 302).
+// Against the 128 x 128 tiles without guards, one per CU, where it reads less (4x4096x4096:
+// 4.9 against 10.0 us, 512x4096x4096: 29.9 against 17.3); not where those tiles fill the
+// chip.
 bool fp4_streams(int64_t M, int64_t N, int64_t K, int64_t ldbt, int64_t ld_sb, int path) {
     if (ldbt > kW4MaxPitch || ld_sb > kW4MaxPitch || K < 32) return false;
-    if (path == GR_PATH_TILE_EDGE) return true;
-    if ((M + 127) / 128 * ((N + 127) / 128) > kCus) return false;
+    const int64_t tiles = (M + 127) / 128 * ((N + 127) / 128);
     const Fp4Plan p = fp4_plan(M, N);
     // (fitted: microseconds to start, KB per microsecond, and the sums of a unit)
     const double row = (double)K * 17 / 32 / 1024;  // KB
+    if (path == GR_PATH_TILE_EDGE) {
+        // (the waves that share a unit's K make its sums; the guarded kernel's tiles leave L2 with a long K)
+        const double sums = 0.22 + 0.02 * divide(K, 4, false).kw * p.MT, k = K <= 2304 ? 0.0105 : 0.0135;
+        return 4.5 + p.rounds * (16 * (p.MT + p.units) * row / 31 + sums * p.units) <
+               5.0 + (tiles + kCus - 1) / kCus * (1 + k * K);
+    }
+    if (tiles > kCus) return false;
     const double stream = 1.5 + 16 * (p.MT + p.units) * row / 26 + (0.4 + 0.27 * p.MT) * p.units;
     const double tile = 4.5 + (M < 128 ? M + 128 : 256) * row / 42;
     return stream < tile;

@@ -100,3 +100,37 @@ def test_moe_hidden_value_beyond_bfloat16(T):
     s13[0, I:] = 127 + 5                                           # h = 2^129: infinite in fp32
     out = gr.moe_mxfp4(*(t.cuda() for t in (x, ids, p, w13, s13, w2, s2)), act="none").cpu()
     assert bool((out[0] == float("inf")).all()) and bool((out[1:] == 0).all())
+
+
+# ---- MX fp4 x MX fp4 --------------------------------------------------------------------------
+
+def median_us(call, n=15):
+    call()
+    times = []
+    for _ in range(n):
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        for _ in range(8):
+            call()
+        end.record()
+        end.synchronize()
+        times.append(start.elapsed_time(end) / 8 * 1e3)
+    return sorted(times)[n // 2]
+
+
+@pytest.mark.parametrize("M,N,K,streams", [(4096, 4096, 544, False), (8192, 2048, 160, False), (200, 4000, 2080, True),
+                                           (300, 300, 8224, True)])
+def test_fp4_product_with_ragged_k_takes_the_faster_kernel(M, N, K, streams):
+    """Many tiles and a short K go to the guarded kernel (the streaming one takes 3.0 and 2.1 times as long for the first
+    two), few tiles or a long K to the streaming one (the guarded one takes 1.9 and 6 times as long). The results are
+    right either way."""
+    log("fp4 ragged M=%d N=%d K=%d" % (M, N, K))
+    (qa, sa), (qb, sb) = weights((M,), K, 230), weights((N,), K, 231)
+    dev = [t.cuda() for t in (qa, sa, qb, sb)]
+    out = torch.empty(M, N, dtype=torch.float16, device="cuda")
+    guarded = median_us(lambda: gr.gemm_mxfp4(*dev, act="none", out=out, path=gr.GR_PATH_TILE_EDGE))
+    chosen = median_us(lambda: gr.gemm_mxfp4(*dev, act="none", out=out))
+    log("chosen %.1f us, guarded %.1f us" % (chosen, guarded))
+    assert chosen < guarded * (0.75 if streams else 1.5)
+    a, w = mx_ref.weight(qa[:64], sa[:64]), mx_ref.weight(qb, sb)
+    mx_ref.check16(out[:64].cpu(), a @ w.T, torch.float16, (a.abs() @ w.abs().T) * (2.0 ** -16 + mx_ref.sum_bound(K)))
