@@ -306,8 +306,8 @@ Fp4Plan fp4_plan(int64_t M, int64_t N) {
 // 4096x4096x4000 119 against 207), the guarded kernel with many and a short one
 // (4096x4096x544 26 against 79 us, 8192x8192x1056 169 against 302).
 // Against the 128 x 128 tiles without guards, one per CU, where it reads less (4x4096x4096:
-// 4.9 against 10.0 us, 512x4096x4096: 29.9 against 17.3); not where those tiles fill the
-// chip.
+// 4.9 against 10.0 us, 512x4096x4096: 29.9 against 17.3, 512x2048x8192 30.7 against 22.1: the
+// fewer tiles, the more each reads a microsecond); not where those tiles fill the chip.
 bool fp4_streams(int64_t M, int64_t N, int64_t K, int64_t ldbt, int64_t ld_sb, int path) {
     if (ldbt > kW4MaxPitch || ld_sb > kW4MaxPitch || K < 32) return false;
     const int64_t tiles = (M + 127) / 128 * ((N + 127) / 128);
@@ -322,7 +322,7 @@ bool fp4_streams(int64_t M, int64_t N, int64_t K, int64_t ldbt, int64_t ld_sb, i
     }
     if (tiles > kCus) return false;
     const double stream = 1.5 + 16 * (p.MT + p.units) * row / 26 + (0.4 + 0.27 * p.MT) * p.units;
-    const double tile = 4.5 + (M < 128 ? M + 128 : 256) * row / 42;
+    const double tile = 4.5 + 256 * row / (tiles <= 64 ? 52 : (tiles <= 128 ? 42 : 33));
     return stream < tile;
 }
 

@@ -134,3 +134,18 @@ def test_fp4_product_with_ragged_k_takes_the_faster_kernel(M, N, K, streams):
     assert chosen < guarded * (0.75 if streams else 1.5)
     a, w = mx_ref.weight(qa[:64], sa[:64]), mx_ref.weight(qb, sb)
     mx_ref.check16(out[:64].cpu(), a @ w.T, torch.float16, (a.abs() @ w.abs().T) * (2.0 ** -16 + mx_ref.sum_bound(K)))
+
+
+@pytest.mark.parametrize("M,N,K,streams", [(512, 2048, 8192, False), (1024, 1024, 8192, False), (200, 2048, 3584, True),
+                                           (16, 8192, 8192, True)])
+def test_fp4_product_takes_the_faster_kernel(M, N, K, streams):
+    """64 tiles with a long K go to the 128 x 128 tiles (streaming takes 1.4 times as long), fewer rows or a shorter K to
+    the streaming kernel (the tiles take 1.2 and 1.6 times as long)."""
+    log("fp4 tiles or streaming M=%d N=%d K=%d" % (M, N, K))
+    (qa, sa), (qb, sb) = weights((M,), K, 232), weights((N,), K, 233)
+    dev = [t.cuda() for t in (qa, sa, qb, sb)]
+    out = torch.empty(M, N, dtype=torch.float16, device="cuda")
+    tiles = median_us(lambda: gr.gemm_mxfp4(*dev, act="none", out=out, path=gr.GR_PATH_TILE))
+    chosen = median_us(lambda: gr.gemm_mxfp4(*dev, act="none", out=out))
+    log("chosen %.1f us, tiles %.1f us" % (chosen, tiles))
+    assert chosen < tiles * (0.95 if streams else 1.2)
