@@ -56,6 +56,40 @@ def test_linear_far_scales_cancel_f16():
     assert bool((out == 0).all()), out
 
 
+def unusual(s, dtype, seed):
+    """Scales with codes in some rows and blocks that the conversion to dtype cannot apply."""
+    s = s.clone()
+    g = torch.Generator().manual_seed(seed)
+    flat = s.view(-1, s.shape[-1])
+    rows, blocks = flat.shape
+    for r in range(rows):
+        b = int(torch.randint(0, blocks, (1,), generator=g))
+        if dtype == "f16":  # more than 2^13 apart
+            if r % 3 == 0:
+                flat[r] = torch.randint(96, 126, (blocks,), generator=g, dtype=torch.uint8)
+            elif r % 3 == 1:
+                flat[r, b] = 0
+        elif r % 2 == 0:
+            flat[r, b] = (0, 1, 253, 254)[r // 2 % 4]
+    return s
+
+
+@pytest.mark.parametrize("workspace", ["auto", None])
+@pytest.mark.parametrize("M,N,K", [(3, 40, 8736), (16, 50, 16384), (20, 33, 4640), (64, 100, 6176), (64, 16, 1024)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_linear_unusual_scales(M, N, K, workspace, dtype):
+    """The second go over the units with several passes over K (the sums so far in LDS), with K split over workgroups, and
+    with 16 to 64 rows."""
+    log("linear unusual M=%d N=%d K=%d dtype=%s workspace=%s" % (M, N, K, dtype, workspace))
+    x = inputs(M, K, dtype, 250, 2.0 ** -30 if dtype == "bf16" else 1.0)
+    w, s = weights((N,), K, 251)
+    s = unusual(s, dtype, 252)
+    out = gr.linear_mxfp4(x.cuda(), w.cuda(), s.cuda(), workspace=workspace).cpu()
+    ref, mag = mx_ref.linear(x, w, s)
+    # products below fp32's normal range are lost: K of them at most
+    mx_ref.check16(out, ref, x.dtype, mag * mx_ref.sum_bound(K) + K * 2.0 ** -126)
+
+
 # ---- experts -------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("I", [64, 1280])
@@ -100,6 +134,61 @@ def test_moe_hidden_value_beyond_bfloat16(T):
     s13[0, I:] = 127 + 5                                           # h = 2^129: infinite in fp32
     out = gr.moe_mxfp4(*(t.cuda() for t in (x, ids, p, w13, s13, w2, s2)), act="none").cpu()
     assert bool((out[0] == float("inf")).all()) and bool((out[1:] == 0).all())
+
+
+@pytest.mark.parametrize("T,H,I,E,k", [(3, 8224, 64, 2, 1), (18, 8224, 64, 2, 1), (18, 32, 4160, 2, 2), (3, 64, 2080, 3, 3),
+                                       (5, 96, 160, 4, 2), (40, 256, 512, 3, 2), (1, 64, 96, 4, 2), (12, 4128, 32, 3, 2)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_moe_unusual_scales(T, H, I, E, k, dtype):
+    """The second go of the experts' products: pairs of gate and up units, h in two planes, experts side by side in one
+    long K (T <= 16) and not, one pass and several. With bfloat16 the second weight has the ends of E8M0 (its products
+    are bfloat16 for any x) and small shares keep the sums in range; with fp16 the first one is uneven."""
+    log("moe unusual T=%d H=%d I=%d E=%d k=%d dtype=%s" % (T, H, I, E, k, dtype))
+    g = torch.Generator().manual_seed(260)
+    x = inputs(T, H, dtype, 261)
+    (w13, s13), (w2, s2) = weights((E, 2 * I), H, 262, 110, 114), weights((E, H), I, 263)
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).int()
+    p = torch.rand(T, k, generator=g)
+    if dtype == "bf16":
+        s2, p = unusual(s2, dtype, 264), p * 2.0 ** -40
+    else:
+        s13 = unusual(s13, dtype, 264)
+    out = gr.moe_mxfp4(*(t.cuda() for t in (x, ids, p, w13, s13, w2, s2))).cpu()
+    ref, bound = mx_ref.moe(x, ids, p, w13, s13, w2, s2, None, None, "silu")
+    mx_ref.check16(out, ref, x.dtype, bound + I * 2.0 ** -126)
+
+
+def test_moe_most_experts_and_choices():
+    """1024 experts and 32 choices: the largest routing tables beside the sums in LDS."""
+    for T in (1, 3, 64, 70):
+        log("moe most T=%d" % T)
+        H, I, E, k = 64, 32, 1024, 32
+        g = torch.Generator().manual_seed(270 + T)
+        x = inputs(T, H, "bf16", 271)
+        (w13, s13), (w2, s2) = weights((E, 2 * I), H, 272), weights((E, H), I, 273)
+        ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).int()
+        p = torch.rand(T, k, generator=g)
+        out = gr.moe_mxfp4(*(t.cuda() for t in (x, ids, p, w13, s13, w2, s2))).cpu()
+        ref, bound = mx_ref.moe(x, ids, p, w13, s13, w2, s2, None, None, "silu")
+        mx_ref.check16(out, ref, x.dtype, bound)
+
+
+@pytest.mark.parametrize("T,H,E,k", [(513, 4096, 64, 8), (1030, 700, 129, 6), (2000, 96, 1000, 20), (5000, 33, 16, 2)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_many_tokens(T, H, E, k, renorm):
+    """Above 512 tokens one kernel does it: logits within the sums' bounds, weights from them."""
+    log("route many T=%d H=%d E=%d k=%d renorm=%s" % (T, H, E, k, renorm))
+    x, w = inputs(T, H, "bf16", 280), inputs(E, H, "bf16", 281, 2 * H ** -0.5)
+    ids, p = gr.moe_route(x.cuda(), w.cuda(), k, renormalize=renorm)
+    ids, p = ids.cpu().long(), p.cpu().double()
+    logits = x.double() @ w.double().T
+    off = (x.double().abs() @ w.double().abs().T * mx_ref.sum_bound(H)).max().item()
+    best = logits.sort(-1, descending=True).values[:, :k]
+    top = logits.gather(1, ids)
+    assert bool((top - best).abs().max() <= 2 * off) and all(len(set(r)) == k for r in ids.tolist())
+    e = torch.exp(top - best[:, :1])
+    total = e.sum(-1, keepdim=True) if renorm else torch.exp(logits - best[:, :1]).sum(-1, keepdim=True)
+    assert bool(((p - e / total).abs() <= (e / total) * (4 * off + 64 * U)).all())
 
 
 # ---- MX fp4 x MX fp4 --------------------------------------------------------------------------
@@ -149,3 +238,16 @@ def test_fp4_product_takes_the_faster_kernel(M, N, K, streams):
     chosen = median_us(lambda: gr.gemm_mxfp4(*dev, act="none", out=out))
     log("chosen %.1f us, tiles %.1f us" % (chosen, tiles))
     assert chosen < tiles * (0.95 if streams else 1.2)
+
+
+def test_repeated_calls_give_the_same_bits():
+    """Sums are added in a fixed order: the same call gives the same bits, one workgroup's K and split ones alike."""
+    for M, N, K in ((1, 4096, 4096), (5, 1001, 2080), (64, 1040, 8192)):
+        log("repeated M=%d N=%d K=%d" % (M, N, K))
+        x = inputs(M, K, "bf16", 240).cuda()
+        w, s = (t.cuda() for t in weights((N,), K, 241))
+        q, e = gr.mx_quantize(x, "mxfp4")
+        first = gr.linear_mxfp4(x, w, s), gr.gemm_mxfp4(q, e, w, s, act="none")
+        for _ in range(20):
+            again = gr.linear_mxfp4(x, w, s), gr.gemm_mxfp4(q, e, w, s, act="none")
+            assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
