@@ -341,8 +341,10 @@ __device__ __forceinline__ float over_1p_exp(float v, float z) {
     return t > 126.0f ? v * half * __builtin_fmaf(-half * kLn2, low, half) : (m == m ? m : q);
 }
 
-// The activations of the C ABI with relative errors of a few fp32 ulp, tails
-// included: an MX element is rounded relative to its block, not to 1.
+// The activations of the C ABI with small relative errors, tails included: an MX
+// element is rounded relative to its block, not to 1.  SiLU, sigmoid and tanh are within
+// a few fp32 ulp; the argument that GELU's erfc and the tanh form's exponential take is
+// rounded before, which costs some x^2 half steps more in their tails.
 template <int A>
 __device__ __forceinline__ float exact_act(float x) {
     if constexpr (A == kActRelu) {

@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(kSumThreads) linear_w4_sum_kernel(LinearArgs a
 // their weights is read once, and on chunks of 64 tokens (a bit each in an expert's
 // 64-bit set).  Pairs are numbered by expert, then token: the number is the row of
 // h and y.  h holds weight * act(g) * u in two bfloat16 parts (high and the
-// rest's high: 16 bits and fp32's range), so that the second product starts from
-// nearly fp32 values.
+// rest's high: 16 bits and fp32's range, infinities included), so that the second
+// product starts from nearly fp32 values.
 //
 // 32 tokens with 8 of 64 experts, 4096 x 2048: 113 us for the first product (561 MB,
 // 5.0 TB/s), 67 for the second (295 MB, 4.4 TB/s), 5 for the sum.  One token with 4

@@ -25,7 +25,10 @@
 //
 // A workgroup that meets other codes goes over its units again with multiply_any, which
 // multiplies each block's fp32 sum by its scale: exact for all codes; code 255 gives
-// NaN.  (In the loop itself that form cost 20 registers, which spilled.)
+// NaN.  (In the loop itself that form cost 20 registers, which spilled.  What spills still:
+// 15 to 25 registers of the MX fp4 x MX fp4 kernel with 64 rows and 4 steps, some read
+// again for each unit; 4 to 15 of kernels with several passes and of the experts' first
+// product, before and after their loops over units or in the second go.)
 #pragma once
 
 #include <type_traits>

@@ -890,9 +890,12 @@ int gated_act_mx(int64_t M, int64_t N,
  * gemm_w4_bt -- C := act(A * Bt~^T + bias) with A (M x K), bias and C in fmt and
  * Bt (N x K) in MX fp4 as for gemm_mxfp4_bt (E2M1 pairs, pitch ldbt in bytes;
  * scale_b N x K / 32 E8M0 bytes, pitch ld_sb).  Made for few rows of A: the
- * weights are read once per 64 rows.  Weights are widened exactly, products
- * accumulate in fp32 per block of 32 k, and the block's scale multiplies the fp32
- * sum: every scale 2^-127 .. 2^127 is exact, scale byte 255 gives NaN.  K % 32
+ * weights are read once per 64 rows.  Weights are widened to fmt with their block's
+ * scale where that is exact (bfloat16: scale bytes 2 to 252; fp16: within 2^13 of the
+ * first scale of the row in the range of k that a wave takes, which multiplies the fp32
+ * sum); where a workgroup meets other scales, the fp32 sum of each block of 32 k is
+ * multiplied by its scale.  Every scale 2^-127 .. 2^127 is exact either way, scale byte
+ * 255 gives NaN.  K % 32
  * != 0 is GR_ERR_INVALID_DIM; K == 0 gives act(bias); pitches of the weights above 2^26
  * bytes are GR_ERR_TOO_LARGE.  With a workspace of gemm_w4_bt_workspace_size bytes
  * (256-byte aligned) a K that one workgroup cannot hold goes to several; NULL or too
@@ -953,8 +956,8 @@ int moe_route(int64_t T, int64_t H, int64_t E, int64_t topk,
  * Made for few tokens: the weights of an expert that a token of a chunk of 64
  * chose are read once for the chunk, others not at all.  An id outside [0, E) is
  * passed over (an expert held elsewhere); a token with no expert gives zeros.  The
- * sums over k, over experts and h are held to 16 bits or more (fp32 sums, h in
- * two bfloat16 parts); the result is rounded once.
+ * sums over k and over the experts are fp32, h times its weight is held to 16 bits and
+ * fp32's range (two bfloat16 parts, an infinity stays one); the result is rounded once.
  *   X, C       T x H in fmt, pitches ldx, ldc
  *   ids, weights  T x topk, contiguous
  *   W13, S13   E x 2I x H / 2 and E x 2I x H / 32 bytes, contiguous; the rows of an
