@@ -53,6 +53,7 @@ GR_ACT_TANH = 6
 
 GR_FMT_F16 = 0
 GR_FMT_BF16 = 1
+GR_FMT_F32 = 2
 
 GR_OUT_16 = 0
 GR_OUT_MXFP8 = 1
@@ -196,6 +197,20 @@ def lib() -> ctypes.CDLL:
             for nm in ("gemm_mxfp4_bt", "gemm_mxfp4_bt_forced", "gemm_mxfp4_bt_plan"):
                 getattr(l, nm).argtypes = getattr(l, nm.replace("mxfp4", "mxfp8")).argtypes
                 getattr(l, nm).restype = i32
+            pi64 = ctypes.POINTER(i64)
+            l.gated_linear_workspace_size.argtypes = [i64, i64, i64, pi64]
+            l.gated_linear_bt.argtypes = [i64, i64, i64, p, i64, p, i64, p, i32, p, i64, p, i64, i32, p, i64, p]
+            l.linear_backward_workspace_size.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, p, i64, p, i64, p, pi64]
+            l.linear_backward.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, p, i64, p, i64, p, i32, p, i64, p]
+            l.gated_linear_backward_workspace_size.argtypes = [i64, i64, i64, p, i64, p, i64, p, p, pi64]
+            l.gated_linear_backward.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, p, i64, i32, p, i64, p, i64, p,
+                                                i32, p, i64, p]
+            l.sandwich_norm_fwd.argtypes = [i64, i64, p, i64, p, i64, p, p, p, i64, i64, f32, f32, p, i64, p, i64, i32, p]
+            l.sandwich_norm_bwd_workspace_size.argtypes = [i64, i64, i64, pi64]
+            l.sandwich_norm_bwd.argtypes = [i64, i64, p, i64, p, i64, p, i64, p, i64, p, p, p, i64, i64, f32, f32, p, i64,
+                                            p, i64, p, p, p, i64, i32, p, i64, p]
+            l.orthogonalize_workspace_size.argtypes = [i64, i64, i64, pi64]
+            l.orthogonalize_update.argtypes = [i64, i64, i64, p, i64, i64, i32, p, i32, f32, f32, p, i64, i64, p, i64, p]
             l.rms_norm_mx.argtypes = [i64, i64, p, i64, p, i64, p, f32, p, i64, p, i64, p, i64, i32, i32, p]
             l.gated_act_mx.argtypes = [i64, i64, p, i64, p, i64, i32, p, i64, p, i64, i32, i32, p]
             l.gemm_w4_bt.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, p, i32, p, i64, i32, p, i64, p]
@@ -766,3 +781,8 @@ from .mx_ops import (gated_act, gated_act_mx, gemm_mxfp4, gemm_mxfp4_linear_bt, 
                      gemm_w4_bt_workspace_size, linear_mxfp4, moe_mxfp4,
                      moe_route, moe_route_raw, moe_route_workspace_size, moe_w4, moe_w4_workspace_size, mx_quantize,
                      rms_norm, rms_norm_mx)
+from .train_ops import (gated_linear, gated_linear_backward, gated_linear_backward_raw,  # noqa: E402,F401
+                        gated_linear_backward_workspace_size, gated_linear_bt, gated_linear_workspace_size,
+                        linear_backward, linear_backward_raw, linear_backward_workspace_size, orthogonalize,
+                        orthogonalize_update, orthogonalize_workspace_size, sandwich_norm, sandwich_norm_backward,
+                        sandwich_norm_bwd, sandwich_norm_bwd_workspace_size, sandwich_norm_fwd)

@@ -15,7 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 # one translation unit per family of entry points, compiled side by side
 SRC = os.path.join(HERE, "csrc", "gemm_relu.hip")
-UNITS = [SRC, os.path.join(HERE, "csrc", "mx_ops.hip")]
+UNITS = [SRC] + [os.path.join(HERE, "csrc", u) for u in ("mx_ops.hip", "train_ops.hip", "update_ops.hip")]
 LIB = os.path.join(HERE, "libgemm_relu.so")
 TENSORS = os.path.join(HERE, "csrc", "tensors.cpp")
 EXT = os.path.join(HERE, "_tensors.so")

@@ -59,14 +59,21 @@ __device__ __forceinline__ uint16_t to_bf16(float x) {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+struct EpiArgs;
+
 // Element types of A, B and C.  Operands travel as 16-bit patterns (f16x8
 // registers); only the matrix-core instruction and the output rounding
 // depend on the type.  Accumulation is fp32 for both.  kGeneral selects the
 // epilogue: false is the fused ReLU; true (the Epi<> wrapper below) is bias
-// plus a run-time activation.
+// plus a run-time activation.  kOwn: the type brings an epilogue of its own with
+// arguments of its own, and may pair rows of Bt (kPairs) or map workgroups to
+// tiles in its own way (own_epilogue.hpp).
 struct ElemF16 {
     static constexpr bool kIsF16 = true;
     static constexpr bool kGeneral = false;
+    static constexpr bool kOwn = false;
+    static constexpr bool kPairs = false;
+    using Args = EpiArgs;
     static __device__ __forceinline__ float widen(uint16_t h) {
         return (float)__builtin_bit_cast(_Float16, h);
     }
@@ -85,6 +92,9 @@ struct ElemF16 {
 struct ElemBF16 {
     static constexpr bool kIsF16 = false;
     static constexpr bool kGeneral = false;
+    static constexpr bool kOwn = false;
+    static constexpr bool kPairs = false;
+    using Args = EpiArgs;
     static __device__ __forceinline__ float widen(uint16_t h) {
         return __builtin_bit_cast(float, (uint32_t)h << 16);
     }

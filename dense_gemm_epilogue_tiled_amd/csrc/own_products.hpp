@@ -1,0 +1,172 @@
+// Host side of the products with an epilogue of their own: argument checks, the choice of a
+// kernel and its launch.
+#pragma once
+
+#include "host.hpp"
+#include "own_epilogue.hpp"
+#include "smallm_kernel.hpp"
+#include "tile128_kernel.hpp"
+#include "tile3t_kernel.hpp"
+
+namespace {
+
+using gr::ElemBF16;
+using gr::ElemF16;
+
+constexpr int kStreamW = 4, kStreamR = 2, kStreamWOne = 8, kStreamNB = 64, kStreamRows = 64;
+constexpr int64_t kMaxPitch = gr::tile2::MAX_LDA;  // 32-bit copy offsets over 256 rows
+
+bool known_fmt(int fmt) { return fmt == GR_FMT_F16 || fmt == GR_FMT_BF16; }
+bool known_act(int act) { return act >= 0 && act < gr::kActCount; }
+bool dim_ok(int64_t v) { return v >= 0 && v <= kMaxDim; }
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+int64_t aligned(int64_t bytes) { return round_up(bytes, kWorkspaceAlign); }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t least(int64_t cols) { return cols > 1 ? cols : 1; }
+bool rows16(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
+
+struct Region {
+    uintptr_t at;
+    int64_t bytes;
+};
+Region matrix(const void* p, int64_t rows, int64_t cols, int64_t ld) {
+    return {reinterpret_cast<uintptr_t>(p), p ? span_bytes(rows, cols, ld) : 0};
+}
+Region vector(const void* p, int64_t n) { return {reinterpret_cast<uintptr_t>(p), p ? 2 * n : 0}; }
+
+// GR_OK if none of the written regions meets another or one that is read.
+template <int W, int R>
+int check_regions(const Region (&written)[W], const Region (&read)[R]) {
+    for (const Region& r : read)
+        if (r.bytes < 0) return GR_ERR_TOO_LARGE;
+    for (const Region& w : written)
+        if (w.bytes < 0) return GR_ERR_TOO_LARGE;
+    for (int i = 0; i < W; ++i) {
+        for (int j = i + 1; j < W; ++j)
+            if (overlaps(written[i].at, written[i].bytes, written[j].at, written[j].bytes)) return GR_ERR_ALIAS;
+        for (const Region& r : read)
+            if (overlaps(written[i].at, written[i].bytes, r.at, r.bytes)) return GR_ERR_ALIAS;
+    }
+    return GR_OK;
+}
+
+int check_workspace(const void* ws, int64_t bytes, int64_t need) {
+    if (bytes < 0 || reinterpret_cast<uintptr_t>(ws) % kWorkspaceAlign != 0) return GR_ERR_INVALID_ARG;
+    if (need == 0) return GR_OK;
+    if (!ws) return GR_ERR_NULL_PTR;
+    return bytes < need ? GR_ERR_SCRATCH : GR_OK;
+}
+
+// The kernels of C (M x N) = own epilogue of A Bt^T, both operands k-contiguous, for a
+// type with an epilogue of its own.  `rows` of Bt make a column of C (2: paired).
+enum Kernel { kTile256, kTile128, kStream4, kStream8, kSmallM };
+
+// Which of them, for B products at once: up to 64 rows, and products of at most 512 blocks of 64 x 64 (sums of
+// N x rows) with a K long enough to fill them, are streamed; 256 x 256 tiles where there
+// are more than half as many as CUs; else 128 x 128 tiles.  The borders between them are
+// those of the transposed-B ReLU kernels, whose main loops these are.
+Kernel choose(int64_t B, int64_t M, int64_t N, int64_t K, int rows) {
+    const int64_t on = kStreamNB / rows;
+    const int64_t blocks = B * ceil_div(M, kStreamRows) * ceil_div(N, on);
+    if (N >= on && (M <= kStreamRows || (blocks <= 256 && K >= 256) || (blocks <= 512 && K >= 1024)))
+        return blocks <= 256 ? kStream8 : kStream4;
+    if (K % gr::tile3t::BKS == 0 && M >= gr::tile3t::BM &&
+        B * ceil_div(M, gr::tile3t::BM) * ceil_div(N, gr::tile3t::BN / rows) > 128)
+        return kTile256;
+    return kTile128;
+}
+
+constexpr uint32_t kGroupM = 4;  // tile rows that walk the columns together (see tile_of_workgroup)
+
+template <typename E>
+int product(Kernel kernel, int64_t B, int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, const uint16_t* Bt,
+            int64_t ldb, uint16_t* C, int64_t ldc, const typename E::Args& ep, hipStream_t stream) {
+    constexpr int rows = E::kPairs ? 2 : 1;
+    const typename E::Args args = ep;
+    const int vec = 8;
+    switch (kernel) {
+        case kTile256: {
+            using namespace gr::tile3t;
+            constexpr int on = BN / rows;
+            const uint32_t tm = (uint32_t)ceil_div(M, BM), tn = (uint32_t)ceil_div(N, on);
+            if (M % BM == 0 && N % on == 0)
+                return launch_grid(gemm_relu_tile3t_kernel<false, E>, dim3(tm * tn, (uint32_t)B), THREADS, stream, A, Bt, C, M, N, K, lda,
+                              ldb, ldc, tm, tn, kGroupM, vec, args);
+            return launch_grid(gemm_relu_tile3t_kernel<true, E>, dim3(tm * tn, (uint32_t)B), THREADS, stream, A, Bt, C, M, N, K, lda, ldb,
+                          ldc, tm, tn, kGroupM, vec, args);
+        }
+        case kTile128: {
+            using namespace gr::tile128;
+            constexpr int on = BN / rows;
+            const uint32_t tm = (uint32_t)ceil_div(M, BM), tn = (uint32_t)ceil_div(N, on);
+            float* const part = nullptr;
+            const int64_t whole = 0;
+            if (M % BM == 0 && N % on == 0)
+                return launch_grid(gemm_relu_tile128_kernel<false, false, true, E>, dim3(tm * tn, (uint32_t)B), THREADS, stream, A, Bt, C,
+                              M, N, K, lda, ldb, ldc, tm, tn, kGroupM, vec, part, whole, args);
+            return launch_grid(gemm_relu_tile128_kernel<true, false, true, E>, dim3(tm * tn, (uint32_t)B), THREADS, stream, A, Bt, C, M, N,
+                          K, lda, ldb, ldc, tm, tn, kGroupM, vec, part, whole, args);
+        }
+        default: {
+            using namespace gr::smallm;
+            const uint32_t nb = (uint32_t)ceil_div(N, kStreamNB / rows);
+            const int64_t blocks = ceil_div(M, kStreamRows) * nb;
+            // plain order where the column blocks fall on the XCDs evenly
+            const uint32_t order = nb % 4 == 0 ? (gr::kNoXcdRemap | 1u) : kGroupM;
+            float* const part = nullptr;
+            if (kernel == kStream8)
+                return launch_grid(gemm_relu_smallm_stream_kernel<kStreamNB, kStreamWOne, kStreamR, stream::WHOLE, E, false, 4,
+                                                             true, true>,
+                              dim3((uint32_t)blocks, (uint32_t)B), 64 * kStreamWOne, stream, A, Bt, C, part, M, N, K, lda, ldb, ldc, K, nb, order, args);
+            return launch_grid(
+                gemm_relu_smallm_stream_kernel<kStreamNB, kStreamW, kStreamR, stream::WHOLE, E, false, 4, true, true>,
+                dim3((uint32_t)blocks, (uint32_t)B), 64 * kStreamW, stream, A, Bt, C, part, M, N, K, lda, ldb, ldc, K, nb, order, args);
+        }
+    }
+}
+
+// The same for B products of one shape (grid y), and for symmetric ones C = own
+// epilogue of A A^T, A N x K.
+template <typename E>
+int batched(int64_t B, int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, const uint16_t* Bt, int64_t ldb,
+            uint16_t* C, int64_t ldc, const typename E::Args& ep, hipStream_t stream) {
+    return product<E>(choose(B, M, N, K, 1), B, M, N, K, A, lda, Bt, ldb, C, ldc, ep, stream);
+}
+
+// Below the diagonal half of the tiles are left out; ep.ct is C, which gets the others from
+// their mirror images.  The streamed blocks are computed all: they fit the chip at once
+// either way.
+template <typename In>
+int symmetric(int64_t B, int64_t N, int64_t K, const uint16_t* A, int64_t lda, uint16_t* C, int64_t ldc,
+              gr::own::PolyArgs ep, hipStream_t stream) {
+    using namespace gr::own;
+    const Kernel kernel = choose(B, N, N, K, 1);
+    if (kernel == kStream4 || kernel == kStream8) {
+        ep.ct = nullptr;
+        return product<Poly<In, In, false>>(kernel, B, N, N, K, A, lda, A, lda, C, ldc, ep, stream);
+    }
+    using E = Poly<In, In, true>;
+    const int vec = 8;
+    if (kernel == kTile256) {
+        using namespace gr::tile3t;
+        const uint32_t t = (uint32_t)ceil_div(N, BM);
+        const dim3 grid(t * (t + 1) / 2, (uint32_t)B);
+        if (N % BM == 0)
+            return launch_grid(gemm_relu_tile3t_kernel<false, E>, grid, THREADS, stream, A, A, C, N, N, K, lda, lda, ldc, t, t,
+                               kGroupM, vec, ep);
+        return launch_grid(gemm_relu_tile3t_kernel<true, E>, grid, THREADS, stream, A, A, C, N, N, K, lda, lda, ldc, t, t,
+                           kGroupM, vec, ep);
+    }
+    using namespace gr::tile128;
+    const uint32_t t = (uint32_t)ceil_div(N, BM);
+    const dim3 grid(t * (t + 1) / 2, (uint32_t)B);
+    float* const part = nullptr;
+    const int64_t whole = 0;
+    if (N % BM == 0)
+        return launch_grid(gemm_relu_tile128_kernel<false, false, true, E>, grid, THREADS, stream, A, A, C, N, N, K, lda, lda,
+                           ldc, t, t, kGroupM, vec, part, whole, ep);
+    return launch_grid(gemm_relu_tile128_kernel<true, false, true, E>, grid, THREADS, stream, A, A, C, N, N, K, lda, lda, ldc,
+                       t, t, kGroupM, vec, part, whole, ep);
+}
+
+}  // namespace

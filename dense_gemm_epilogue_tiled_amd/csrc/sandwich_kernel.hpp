@@ -1,0 +1,332 @@
+// The end of a residual block and the beginning of the next in one pass, and back:
+//
+//   p = y r(y),  r(v) = 1 / sqrt(mean(v^2) + eps)
+//   total  = round(residual + scale * gate * (p * w))
+//   normed = round(total r(total) * w_next)
+//
+// with a gate of N values for each group of consecutive rows.  Backward, with q =
+// total r(total) and the row means over the columns:
+//
+//   dq = dnormed * w_next
+//   d  = dtotal + r(total) (dq - q mean(dq q))             (= dresidual)
+//   dp = d * scale * gate * w
+//   dy = r(y) (dp - p mean(dp p))
+//   dw = sum over rows of d scale gate p,  dgate = sum over its rows of d scale p w,
+//   dw_next = sum over rows of dnormed q
+//
+// in fp32 from the 16-bit inputs, each output rounded once.  Both passes are bound by
+// memory: a row is held in registers, every input is read once and every output
+// written once (forward 4, backward 6 matrices of M x N).  TPR threads hold a row, at
+// most C chunks of 8 columns each.  Backward, a thread keeps its columns' sums in
+// registers over the rows of its workgroup, so that only one partial sum per workgroup (or wave,
+// where a wave holds a row) and column goes through memory; a second kernel adds
+// those in a fixed order.
+#pragma once
+
+#include "norm_kernel.hpp"
+#include "own_epilogue.hpp"
+
+namespace gr {
+namespace sandwich {
+
+constexpr int64_t MAX_N = 32768;
+
+struct Args {
+    const uint16_t *y, *residual, *w, *next_w, *gate;  // w, next_w, gate: nullptr for ones
+    uint16_t *total, *normed;                          // normed: nullptr if not wanted
+    int64_t M, N, ldy, ldr, ldt, ldn, ld_gate;
+    int64_t group;                                     // rows per gate
+    float scale, eps;
+};
+
+// The chunks of 8 columns that thread t of TPR has of rows of N: how many columns
+// each holds.
+template <int TPR, int C>
+struct Columns {
+    int n[C];
+    bool more;  // 8 columns or more: a short chunk has 8 - n before it
+    int64_t at[C];
+    __device__ __forceinline__ Columns(int t, int64_t N) : more(N > 8) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            at[c] = 8 * (t + (int64_t)c * TPR);
+            n[c] = at[c] < N ? (N - at[c] < 8 ? (int)(N - at[c]) : 8) : 0;
+        }
+    }
+    __device__ __forceinline__ void load(const uint16_t* row, u32x4 (&v)[C]) const {
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[c] = n[c] > 0 ? mx::load8(row + at[c], n[c], more) : u32x4{0u, 0u, 0u, 0u};
+    }
+};
+
+__device__ __forceinline__ float half_up(float sum, int64_t N, float eps) { return mx::inv_sqrt(sum / (float)N + eps); }
+
+// Sums of K values over the TPR threads of a row, the same bits in each of them.  red:
+// K * TPR / 64 floats of this call's own.
+template <int TPR, int K>
+__device__ __forceinline__ void row_sums(float (&v)[K], float* red) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = mx::wave_sum(v[k]);
+    if constexpr (TPR > 64) {
+        constexpr int W = TPR / 64;
+        if (threadIdx.x % 64 == 0) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) red[k * W + threadIdx.x / 64] = v[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float t = 0.0f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) t += red[k * W + i];
+            v[k] = t;
+        }
+    }
+}
+
+template <typename E, int TPR, int C>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) forward_kernel(Args a) {
+    constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
+    __shared__ float red[2][TPR > 64 ? TPR / 64 : 1];
+    const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+    if (row >= a.M) return;  // whole waves, and no barrier where TPR is 64
+    const Columns<TPR, C> col(threadIdx.x % TPR, a.N);
+    u32x4 y[C], s[C], w[C], g[C], w2[C];
+    col.load(a.y + row * a.ldy, y);
+    col.load(a.residual + row * a.ldr, s);
+    if (a.w != nullptr) col.load(a.w, w);
+    if (a.gate != nullptr) col.load(a.gate + row / a.group * a.ld_gate, g);
+    if (a.next_w != nullptr) col.load(a.next_w, w2);
+    float sum[1] = {0.0f};
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float v = own::widen8<E>(y[c], i);
+            sum[0] = __builtin_fmaf(v, v, sum[0]);
+        }
+    row_sums<TPR>(sum, red[0]);
+    const float r = half_up(sum[0], a.N, a.eps) * a.scale;
+    sum[0] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float b = own::widen8<E>(y[c], i) * r;
+            if (a.w != nullptr) b *= own::widen8<E>(w[c], i);
+            if (a.gate != nullptr) b *= own::widen8<E>(g[c], i);
+            v[i] = own::widen8<E>(s[c], i) + b;
+        }
+        s[c] = own::round8<E>(v);
+        if (col.n[c] > 0) {
+            own::put8<true, false>(a.total + row * a.ldt + col.at[c], s[c], 0, 0, col.n[c]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float z = i < col.n[c] ? own::widen8<E>(s[c], i) : 0.0f;
+                sum[0] = __builtin_fmaf(z, z, sum[0]);
+            }
+        }
+    }
+    if (a.normed == nullptr) return;
+    row_sums<TPR>(sum, red[1]);
+    const float r2 = half_up(sum[0], a.N, a.eps);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        if (col.n[c] == 0) continue;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] = own::widen8<E>(s[c], i) * r2;
+            if (a.next_w != nullptr) v[i] *= own::widen8<E>(w2[c], i);
+        }
+        own::put8<true, false>(a.normed + row * a.ldn + col.at[c], own::round8<E>(v), 0, 0, col.n[c]);
+    }
+}
+
+struct BwdArgs {
+    const uint16_t *dtotal, *dnormed, *y, *total, *w, *next_w, *gate;  // dtotal, dnormed: nullptr for zeros
+    uint16_t *dy, *dresidual, *dw, *dnext_w, *dgate;                   // dw, dnext_w, dgate: nullptr if not wanted
+    float* part;         // slots x 2 x N partial sums
+    int64_t M, N, ld_dt, ld_dn, ldy, ldt, ld_dy, ld_dr, ld_gate, ld_dgate;
+    int64_t group;       // rows per gate
+    int64_t groups;      // gates (1 without a gate)
+    int64_t split;       // slots per gate where that is at least 1, else 0
+    int64_t slots;       // partial sums of a column
+    float scale, eps;
+};
+
+// The rows [first, end) of a slot, which belong to one gate, or to whole gates
+// where there are fewer slots than gates (split 0).
+struct Rows {
+    int64_t first, end;
+};
+__device__ __forceinline__ Rows rows_of(const BwdArgs& a, int64_t slot) {
+    if (a.split > 0) {
+        const int64_t g = slot / a.split, s = slot % a.split;
+        return {g * a.group + a.group * s / a.split, g * a.group + a.group * (s + 1) / a.split};
+    }
+    return {a.groups * slot / a.slots * a.group, a.groups * (slot + 1) / a.slots * a.group};
+}
+
+// SPLIT: a slot's rows have one gate, and its first partial sum is that of d scale
+// p; else that times the gate, and dgate is written here.
+template <typename E, int TPR, int C, bool SPLIT>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) backward_kernel(BwdArgs a) {
+    constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
+    constexpr int W = TPR > 64 ? TPR / 64 : 1;
+    __shared__ float red[2][4 * W];
+    const int64_t slot = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+    if (slot >= a.slots) return;  // whole waves, and no barrier where TPR is 64
+    const Columns<TPR, C> col(threadIdx.x % TPR, a.N);
+    const Rows rows = rows_of(a, slot);
+    u32x4 w[C], w2[C], g[C];
+    if (a.w != nullptr) col.load(a.w, w);
+    if (a.next_w != nullptr) col.load(a.next_w, w2);
+    if (SPLIT && a.gate != nullptr) col.load(a.gate + rows.first / a.group * a.ld_gate, g);
+    float s1[C][8], s2[C][8], sw[SPLIT ? 1 : C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            s1[c][i] = s2[c][i] = 0.0f;
+            if constexpr (!SPLIT) sw[c][i] = 0.0f;
+        }
+    for (int64_t row = rows.first; row < rows.end; ++row) {
+        u32x4 y[C], z[C], dt[C], dn[C];
+        col.load(a.y + row * a.ldy, y);
+        col.load(a.total + row * a.ldt, z);
+        if (a.dtotal != nullptr) col.load(a.dtotal + row * a.ld_dt, dt);
+        if (a.dnormed != nullptr) col.load(a.dnormed + row * a.ld_dn, dn);
+        if (!SPLIT && a.gate != nullptr && row % a.group == 0) col.load(a.gate + row / a.group * a.ld_gate, g);
+        float sum[3] = {0.0f, 0.0f, 0.0f};  // of y^2, total^2, dq total
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float yv = own::widen8<E>(y[c], i), zv = own::widen8<E>(z[c], i);
+                sum[0] = __builtin_fmaf(yv, yv, sum[0]);
+                sum[1] = __builtin_fmaf(zv, zv, sum[1]);
+                if (a.dnormed != nullptr) {
+                    float v = own::widen8<E>(dn[c], i);
+                    if (a.next_w != nullptr) v *= own::widen8<E>(w2[c], i);
+                    sum[2] = __builtin_fmaf(v, zv, sum[2]);
+                }
+            }
+        row_sums<TPR>(sum, red[0]);
+        const float r1 = half_up(sum[0], a.N, a.eps), r2 = half_up(sum[1], a.N, a.eps);
+        const float mean2 = sum[2] * r2 / (float)a.N;
+        float d[C][8], dot[1] = {0.0f};
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float v = a.dtotal != nullptr ? own::widen8<E>(dt[c], i) : 0.0f;
+                if (a.dnormed != nullptr) {
+                    const float dnv = own::widen8<E>(dn[c], i), q = own::widen8<E>(z[c], i) * r2;
+                    const float dq = a.next_w != nullptr ? dnv * own::widen8<E>(w2[c], i) : dnv;
+                    v = __builtin_fmaf(r2, __builtin_fmaf(-q, mean2, dq), v);
+                    s2[c][i] = __builtin_fmaf(dnv, q, s2[c][i]);
+                }
+                d[c][i] = v;
+            }
+            if (col.n[c] > 0)
+                own::put8<true, false>(a.dresidual + row * a.ld_dr + col.at[c], own::round8<E>(d[c]), 0, 0, col.n[c]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float p = own::widen8<E>(y[c], i) * r1;
+                float v = d[c][i] * a.scale;
+                s1[c][i] = __builtin_fmaf(v, p, s1[c][i]);
+                if (a.gate != nullptr) v *= own::widen8<E>(g[c], i);
+                if (a.w != nullptr) v *= own::widen8<E>(w[c], i);
+                d[c][i] = v;  // dp from here on
+                dot[0] = __builtin_fmaf(v, p, dot[0]);
+            }
+        }
+        row_sums<TPR>(dot, red[1]);
+        const float mean1 = dot[0] / (float)a.N;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            if (col.n[c] == 0) continue;
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = r1 * __builtin_fmaf(-(own::widen8<E>(y[c], i) * r1), mean1, d[c][i]);
+            own::put8<true, false>(a.dy + row * a.ld_dy + col.at[c], own::round8<E>(v), 0, 0, col.n[c]);
+        }
+        if constexpr (!SPLIT) {
+            if ((row + 1) % a.group == 0) {  // the gate's last row
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        v[i] = a.w != nullptr ? s1[c][i] * own::widen8<E>(w[c], i) : s1[c][i];
+                        sw[c][i] = __builtin_fmaf(own::widen8<E>(g[c], i), s1[c][i], sw[c][i]);
+                        s1[c][i] = 0.0f;
+                    }
+                    if (col.n[c] > 0 && a.dgate != nullptr)
+                        own::put8<true, false>(a.dgate + row / a.group * a.ld_dgate + col.at[c], own::round8<E>(v), 0, 0,
+                                               col.n[c]);
+                }
+            }
+        }
+    }
+    if (a.part == nullptr) return;
+    float* const to = a.part + slot * 2 * a.N;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < col.n[c]) {
+                to[col.at[c] + i] = SPLIT ? s1[c][i] : sw[SPLIT ? 0 : c][i];
+                to[a.N + col.at[c] + i] = s2[c][i];
+            }
+}
+
+// The sums of the slots' partial sums, a workgroup for 32 columns: 8 threads of a column
+// take every 8th slot and meet in LDS in order.
+constexpr int REDUCE_COLS = 32;
+template <typename E>
+__global__ void __launch_bounds__(256) reduce_kernel(BwdArgs a) {
+    __shared__ float red[8][REDUCE_COLS];
+    const int lane = threadIdx.x % REDUCE_COLS, part = threadIdx.x / REDUCE_COLS;  // 8 parts
+    const int64_t n = (int64_t)blockIdx.x * REDUCE_COLS + lane;
+    const bool in = n < a.N;
+    // Each part takes every 8th slot of [first, end); which: the first or second sums.
+    auto total = [&](int64_t first, int64_t end, int which) {
+        float s = 0.0f;
+        if (end > a.slots) end = a.slots;  // no rows: no slots
+        if (in)
+            for (int64_t k = first + part; k < end; k += 8) s += a.part[(k * 2 + which) * a.N + n];
+        __syncthreads();
+        red[part][lane] = s;
+        __syncthreads();
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t += red[i][lane];
+        return t;
+    };
+    if (a.dnext_w != nullptr) {
+        const float s = total(0, a.slots, 1);
+        if (in && part == 0) a.dnext_w[n] = E::round(s);
+    }
+    if (a.split == 0) {
+        if (a.dw != nullptr) {
+            const float s = total(0, a.slots, 0);
+            if (in && part == 0) a.dw[n] = E::round(s);
+        }
+        return;
+    }
+    if (a.dw == nullptr && a.dgate == nullptr) return;
+    const float w = in && a.w != nullptr ? E::widen(a.w[n]) : 1.0f;
+    float dw = 0.0f;
+    for (int64_t g = 0; g < a.groups; ++g) {
+        const float s = total(g * a.split, (g + 1) * a.split, 0);
+        dw = __builtin_fmaf(in && a.gate != nullptr ? E::widen(a.gate[g * a.ld_gate + n]) : 1.0f, s, dw);
+        if (a.dgate != nullptr && in && part == 0) a.dgate[g * a.ld_dgate + n] = E::round(s * w);
+    }
+    if (a.dw != nullptr && in && part == 0) a.dw[n] = E::round(dw);
+}
+
+}  // namespace sandwich
+}  // namespace gr

@@ -256,7 +256,7 @@ template <int NB, int W, int R, int MODE, typename E = ElemF16, bool AT = false,
 __global__ __launch_bounds__(64 * W, 1) void gemm_relu_smallm_stream_kernel(
     const uint16_t* __restrict__ A, const uint16_t* __restrict__ B, uint16_t* __restrict__ C,
     float* __restrict__ part, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc,
-    int64_t k_per_split, uint32_t n_blocks, uint32_t order, EpiArgs ep) {
+    int64_t k_per_split, uint32_t n_blocks, uint32_t order, typename E::Args ep) {
     // RBLK: blocks of 16 MB rows over all of M, all of K, the copies cached
     // (every operand block is read by several workgroups).  The grid is
     // ceil(M / 16 MB) row blocks x n_blocks column blocks; the workgroup's
@@ -307,14 +307,24 @@ __global__ __launch_bounds__(64 * W, 1) void gemm_relu_smallm_stream_kernel(
         cb = blockIdx.x % n_blocks;
         s = blockIdx.x / n_blocks;
     }
+    // columns of C per block (half as many where rows of Bt are paired: blocks
+    // 0 and 1 of 16 rows from Bt's first half, 2 and 3 the same rows of its second)
+    constexpr int ON = E::kPairs ? NB / 2 : NB;
+    static_assert(!E::kPairs || (BT && NB == 64), "paired rows: B transposed, four blocks of 16");
+    int64_t row0 = 0;
+    if constexpr (E::kOwn) {
+        static_assert(RBLK && BT, "own epilogues: row blocks, B transposed");
+        row0 = s * ROWS;
+        E::batch(ep, A, B, C);
+    }
     if constexpr (RBLK) {
         A += s * ROWS * lda;
         C += s * ROWS * ldc;
         M = M - s * ROWS < ROWS ? M - s * ROWS : ROWS;
         s = 0;
     }
-    const int64_t n_own = (int64_t)cb * NB;
-    const int64_t n0 = n_own + NB <= N ? n_own : N - NB;  // the last block ends at column N
+    const int64_t n_own = (int64_t)cb * ON;
+    const int64_t n0 = n_own + ON <= N ? n_own : N - ON;  // the last block ends at column N
     const int64_t k_begin = s * k_per_split;
     const int64_t k_end = k_begin + k_per_split < K ? k_begin + k_per_split : K;
     const int64_t slots = (k_end - k_begin) / stream::SLOT_ROWS;
@@ -333,7 +343,8 @@ __global__ __launch_bounds__(64 * W, 1) void gemm_relu_smallm_stream_kernel(
 #pragma unroll
     for (int i = 0; i < DPS; ++i) {
         if constexpr (BT) {
-            voff[i] = (uint32_t)(((16 * i + arow) * ldb + 8 * (apos ^ ((arow >> 2) & 3u))) * 2);
+            const int block = E::kPairs ? i % 2 : i;
+            voff[i] = (uint32_t)(((16 * block + arow) * ldb + 8 * (apos ^ ((arow >> 2) & 3u))) * 2);
         } else {
             const uint32_t row = i * RPI + lane / CH;
             voff[i] = (uint32_t)((row * ldb + 8 * stream::chunk_slot(row, lane % CH)) * 2);
@@ -366,7 +377,10 @@ __global__ __launch_bounds__(64 * W, 1) void gemm_relu_smallm_stream_kernel(
         const uint32_t dst = ring + (uint32_t)(q % R) * SLOT;
         const uint8_t* src = reinterpret_cast<const uint8_t*>(b_range + t * stream::SLOT_ROWS * (BT ? 1 : ldb));
 #pragma unroll
-        for (int i = 0; i < DPS; ++i) copy16(src, voff[i], dst + i * 1024);
+        for (int i = 0; i < DPS; ++i) {
+            if constexpr (E::kPairs) copy16(src + (i >= 2 ? ep.half * ldb * 2 : 0), voff[i], dst + i * 1024);
+            else copy16(src, voff[i], dst + i * 1024);
+        }
         if constexpr (ADMA) {
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb)
@@ -439,15 +453,31 @@ __global__ __launch_bounds__(64 * W, 1) void gemm_relu_smallm_stream_kernel(
             *reinterpret_cast<f32x4*>(red + w * (R * SLOT / 4) +
                                       red_at(16 * mb + (lane & 15u), 16 * j + 4 * (lane >> 4))) = acc[mb][j];
     __syncthreads();
-    for (uint32_t o = tid; o < (uint32_t)(ROWS * NB); o += T) {
-        const uint32_t m = o / NB, nl = o % NB;
-        const int64_t n = n0 + nl;
-        if ((int64_t)m >= M || n < n_own) continue;
-        float v = 0.0f;
+    if constexpr (E::kOwn) {
+        // four columns of a row at a time: the sum of the waves' partials
+        auto sum4 = [&](uint32_t m, uint32_t c) {
+            f32x4 v = f32x4{};
 #pragma unroll
-        for (int ww = 0; ww < W; ++ww) v += red[ww * (R * SLOT / 4) + red_at(m, nl)];
-        if constexpr (MODE == stream::WHOLE) C[(int64_t)m * ldc + n] = epi_value<E>(v, n, N, ep);
-        else part[(s * M + m) * N + n] = v;
+            for (int ww = 0; ww < W; ++ww) {
+                const f32x4 p = *reinterpret_cast<const f32x4*>(red + ww * (R * SLOT / 4) + red_at(m, c));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] += p[e];
+            }
+            return v;
+        };
+        auto keep4 = [&](uint32_t m, uint32_t c) { return reinterpret_cast<f32x4*>(red + red_at(m, c)); };
+        E::template store_block<ROWS, ON, T>(sum4, keep4, C, ldc, row0, M, N, n0, n_own, ep);
+    } else {
+        for (uint32_t o = tid; o < (uint32_t)(ROWS * NB); o += T) {
+            const uint32_t m = o / NB, nl = o % NB;
+            const int64_t n = n0 + nl;
+            if ((int64_t)m >= M || n < n_own) continue;
+            float v = 0.0f;
+#pragma unroll
+            for (int ww = 0; ww < W; ++ww) v += red[ww * (R * SLOT / 4) + red_at(m, nl)];
+            if constexpr (MODE == stream::WHOLE) C[(int64_t)m * ldc + n] = epi_value<E>(v, n, N, ep);
+            else part[(s * M + m) * N + n] = v;
+        }
     }
 }
 
@@ -769,7 +799,7 @@ constexpr int BTS_ROWB = BTS_KC * 2;  // 512 bytes of a row per chunk
 template <bool GUARD, typename E = ElemF16, int W = 4, int MA = 16, int R = 2>
 __global__ __launch_bounds__(64 * W, 1) void gemm_relu_smallm_bt_stream_kernel(
     const uint16_t* __restrict__ A, const uint16_t* __restrict__ Bt, uint16_t* __restrict__ C, int64_t M, int64_t N,
-    int64_t K, int64_t lda, int64_t ldbt, int64_t ldc, EpiArgs ep) {
+    int64_t K, int64_t lda, int64_t ldbt, int64_t ldc, typename E::Args ep) {
     static_assert(MA == 2 || MA == 4 || MA == 8 || MA == 16, "rows of A per slot");
     static_assert(R >= 2 && R <= 4, "ring entries per wave");
     constexpr int BT_BYTES = 16 * BTS_ROWB;                // 8 KiB: the wave's 16 Bt rows
@@ -780,7 +810,10 @@ __global__ __launch_bounds__(64 * W, 1) void gemm_relu_smallm_bt_stream_kernel(
 
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t n_w = (int64_t)blockIdx.x * (16 * W) + 16 * wave;  // this wave's first column
+    // Paired rows: the wave's 16 rows are 8 of Bt's first half and the same 8 of
+    // its second, 8 columns of C.
+    constexpr int ON = E::kPairs ? 8 : 16;
+    const int64_t n_w = (int64_t)blockIdx.x * (ON * W) + ON * wave;  // this wave's first column
 
     // Copy i of a chunk: rows 2i, 2i+1 (of the wave's 16 Bt rows, or of the
     // MA rows of A); lane -> row 2i + lane/32, LDS piece lane%32, which
@@ -794,7 +827,7 @@ __global__ __launch_bounds__(64 * W, 1) void gemm_relu_smallm_bt_stream_kernel(
     for (int i = 0; i < 8; ++i) {
         const uint32_t row = 2u * i + (lane >> 5);
         const uint32_t piece = (lane & 31u) ^ (row & 15u);
-        int64_t n = n_w + row;
+        int64_t n = n_w + (E::kPairs ? row & 7u : row);
         if (GUARD && n >= N) n = N - 1;
         off_bt[i] = past ? piece * 16u : (uint32_t)((n - n_w) * ldbt * 2 + piece * 16);
     }
@@ -813,7 +846,10 @@ __global__ __launch_bounds__(64 * W, 1) void gemm_relu_smallm_bt_stream_kernel(
         const uint32_t dst = ring + (uint32_t)(kc % R) * WSLOT;
         const int64_t kb = kc * BTS_ROWB;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) tile2::dma16(base_bt + kb, off_bt[i], dst + i * 1024u);
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (E::kPairs) tile2::dma16(base_bt + kb + (i >= 4 ? ep.half * ldbt * 2 : 0), off_bt[i], dst + i * 1024u);
+            else tile2::dma16(base_bt + kb, off_bt[i], dst + i * 1024u);
+        }
 #pragma unroll
         for (int i = 0; i < CP_A; ++i) tile2::dma16(base_a + kb, off_a[i], dst + BT_BYTES + i * 1024u);
     };
@@ -846,7 +882,16 @@ __global__ __launch_bounds__(64 * W, 1) void gemm_relu_smallm_bt_stream_kernel(
     // acc holds C^T: lane l, register r is C[m][n] with m = l%16 and
     // n = n_w + 4(l/16) + r.
     const int64_t m = li;
-    if (m < M) {
+    if constexpr (E::kOwn) {
+        // the pair of column 4(l/16) + r, l < 32, is in this lane and in lane l + 32
+        f32x4 v, pair;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            v[r] = acc0[r] + acc1[r];
+            pair[r] = __shfl_xor(v[r], 32);
+        }
+        if (lane < 32u && m < M) E::store4(v, pair, C, ldc, m, n_w + 4 * lg, N, ep);
+    } else if (m < M) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int64_t n = n_w + 4 * lg + r;

@@ -1,4 +1,4 @@
-// The tensor helpers of mx_ops.py: checks of the tensors' types, shapes and
+// The tensor helpers of mx_ops.py and train_ops.py: checks of the tensors' types, shapes and
 // pitches, new outputs and scratch, and the call of the C ABI.  In C++ because a
 // decoding step calls them for microseconds of GPU work: the same steps took 11.5
 // us for rms_norm in Python, 4 us of which were the launch, and take 5.3 here.
@@ -433,10 +433,277 @@ PyObject* moe_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// ---- training -----------------------------------------------------------------------------
+
+double double_of(PyObject* o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw Raise{nullptr, ""};
+    return v;
+}
+
+// A matrix next to `like`, of its type; nothing for None.
+struct Maybe {
+    int64_t ld = 1;
+    uint16_t* data = nullptr;
+
+    Maybe(PyObject* o, const Tensor& like, int64_t rows, int64_t cols, const char* what) {
+        const Tensor* t = maybe_tensor(o, what);
+        if (!t) {
+            ld = cols > 0 ? cols : 1;
+            return;
+        }
+        ld = matching(*t, like, rows, cols, like.scalar_type(), what);
+        data = data_of<uint16_t>(*t);
+    }
+};
+
+// An output that may not be wanted: new or given if `wanted`, else None must be given.
+struct Wanted {
+    Tensor t;
+    int64_t ld = 1;
+    uint16_t* data = nullptr;
+
+    Wanted(PyObject* o, bool wanted, const Tensor& like, int64_t rows, int64_t cols, const char* what) {
+        if (!wanted) {
+            if (o != Py_None) bad_value(std::string(what) + " is given for what is not asked for");
+            ld = cols > 0 ? cols : 1;
+            return;
+        }
+        Output out(o, like, rows, cols, like.scalar_type(), what);
+        t = out.t;
+        ld = out.ld;
+        data = data_of<uint16_t>(t);
+    }
+};
+
+// A new vector of n values like `like`, if wanted.
+Tensor vector_like(bool wanted, const Tensor& like, int64_t n) {
+    return wanted ? empty_like(like, {n}, like.scalar_type()) : Tensor();
+}
+uint16_t* data_or_null(const Tensor& t) { return t.defined() ? data_of<uint16_t>(t) : nullptr; }
+
+PyObject* failed(int st) { return PyLong_FromLong(st); }
+
+// x, w13, b13, act, keep, out, gu_out, workspace, stream
+PyObject* gated_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return entry(n, 9, [&]() -> PyObject* {
+        const Matrix x(a[0], "x"), w(a[1], "w13");
+        if (w.fmt != x.fmt) bad_type("w13 must have x's type");
+        if (w.rows % 2 || w.cols != x.cols) bad_value("w13 must be 2I x " + std::to_string(x.cols) + ", got " + shape_text(w.t.sizes()));
+        check_place(w.t, x.t, "w13");
+        const int64_t I = w.rows / 2;
+        const uint16_t* bias = vector_of<uint16_t>(a[2], x.t, 2 * I, x.t.scalar_type(), "b13");
+        const int act = (int)int_of(a[3]);
+        const bool keep = int_of(a[4]) != 0;
+        on_gpu(x.t, "x");
+        const Wanted c(a[5], true, x.t, x.rows, I, "out"), gu(a[6], keep, x.t, x.rows, 2 * I, "gu_out");
+        int64_t need = 0;
+        int st = gated_linear_workspace_size(x.rows, I, x.cols, &need);
+        if (st != GR_OK) return failed(st);
+        const Scratch ws(a[7], x.t, need);
+        st = gated_linear_bt(x.rows, I, x.cols, x.data, x.ld, w.data, w.ld, bias, act, c.data, c.ld, gu.data, gu.ld, x.fmt,
+                             ws.data, ws.bytes, stream_of(a[8]));
+        return st == GR_OK ? tuple_of({&c.t, &gu.t}) : failed(st);
+    });
+}
+
+// dy, x, weight, bias, input gradient, weight gradient, dx_out, dw_out, workspace, stream
+PyObject* linear_backward_(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return entry(n, 10, [&]() -> PyObject* {
+        const Matrix dy(a[0], "dy"), w(a[2], "weight");
+        if (w.fmt != dy.fmt) bad_type("weight must have dy's type");
+        if (w.rows != dy.cols) bad_value("weight must be " + std::to_string(dy.cols) + " x K, got " + shape_text(w.t.sizes()));
+        check_place(w.t, dy.t, "weight");
+        const int64_t M = dy.rows, N = dy.cols, K = w.cols;
+        const bool bias = int_of(a[3]) != 0, want_x = int_of(a[4]) != 0, want_w = int_of(a[5]) != 0;
+        if (want_w && a[1] == Py_None) bad_value("the weight's gradient needs x");
+        const Maybe x(a[1], dy.t, M, K, "x");
+        on_gpu(dy.t, "dy");
+        const Wanted dx(a[6], want_x, dy.t, M, K, "dx_out"), dw(a[7], want_w, dy.t, N, K, "dw_out");
+        const Tensor db = vector_like(bias, dy.t, N);
+        int64_t need = 0;
+        int st = linear_backward_workspace_size(M, N, K, dy.data, dy.ld, x.data, x.ld, w.data, w.ld, dx.data, dx.ld, dw.data,
+                                                dw.ld, data_or_null(db), &need);
+        if (st != GR_OK) return failed(st);
+        const Scratch ws(a[8], dy.t, need);
+        st = linear_backward(M, N, K, dy.data, dy.ld, x.data, x.ld, w.data, w.ld, dx.data, dx.ld, dw.data, dw.ld,
+                             data_or_null(db), dy.fmt, ws.data, ws.bytes, stream_of(a[9]));
+        return st == GR_OK ? tuple_of({&dx.t, &dw.t, &db}) : failed(st);
+    });
+}
+
+// dh, x, w13, gu, act, bias, input gradient, weight gradient, dx_out, dw_out, workspace, stream
+PyObject* gated_linear_backward_(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return entry(n, 12, [&]() -> PyObject* {
+        const Matrix dh(a[0], "dh"), w(a[2], "w13");
+        const int64_t M = dh.rows, I = dh.cols, H = w.cols;
+        if (w.fmt != dh.fmt) bad_type("w13 must have dh's type");
+        if (w.rows != 2 * I) bad_value("w13 must be " + std::to_string(2 * I) + " x H, got " + shape_text(w.t.sizes()));
+        check_place(w.t, dh.t, "w13");
+        const Matrix gu(a[3], "gu");
+        const int64_t ldgu = matching(gu.t, dh.t, M, 2 * I, dh.t.scalar_type(), "gu");
+        const int act = (int)int_of(a[4]);
+        const bool bias = int_of(a[5]) != 0, want_x = int_of(a[6]) != 0, want_w = int_of(a[7]) != 0;
+        if (want_w && a[1] == Py_None) bad_value("the weight's gradient needs x");
+        const Maybe x(a[1], dh.t, M, H, "x");
+        on_gpu(dh.t, "dh");
+        const Wanted dx(a[8], want_x, dh.t, M, H, "dx_out"), dw(a[9], want_w, dh.t, 2 * I, H, "dw_out");
+        const Tensor db = vector_like(bias, dh.t, 2 * I);
+        int64_t need = 0;
+        int st = gated_linear_backward_workspace_size(M, I, H, w.data, w.ld, dx.data, dx.ld, dw.data, data_or_null(db), &need);
+        if (st != GR_OK) return failed(st);
+        const Scratch ws(a[10], dh.t, need);
+        st = gated_linear_backward(M, I, H, dh.data, dh.ld, x.data, x.ld, w.data, w.ld, gu.data, ldgu, act, dx.data, dx.ld,
+                                   dw.data, dw.ld, data_or_null(db), dh.fmt, ws.data, ws.bytes, stream_of(a[11]));
+        return st == GR_OK ? tuple_of({&dx.t, &dw.t, &db}) : failed(st);
+    });
+}
+
+// The gates of a sandwich norm: N values, or G x N with G a divisor of the rows.
+struct Gates {
+    int64_t count = 0, ld = 1;
+    const uint16_t* data = nullptr;
+    bool flat = false;
+
+    Gates(PyObject* o, const Tensor& like) {
+        const Tensor* t = maybe_tensor(o, "gate");
+        const int64_t M = like.size(0), N = like.size(1);
+        ld = N > 0 ? N : 1;
+        if (!t) return;
+        flat = t->dim() == 1;
+        if (flat) {
+            data = vector_of<uint16_t>(o, like, N, like.scalar_type(), "gate");
+            count = 1;
+            return;
+        }
+        if (t->dim() != 2) bad_value("gate must be N values or G x N");
+        count = t->size(0);
+        ld = matching(*t, like, count, N, like.scalar_type(), "gate");
+        if (count < 1 || M % count) bad_value("the rows must be a multiple of the gates: " + std::to_string(M) + " rows, " + std::to_string(count) + " gates");
+        data = data_of<const uint16_t>(*t);
+    }
+};
+
+// y, residual, weight, next_weight, gate, scale, eps, next norm, total_out, normed_out, stream
+PyObject* sandwich_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return entry(n, 11, [&]() -> PyObject* {
+        const Matrix y(a[0], "y");
+        const auto kind = y.t.scalar_type();
+        const int64_t M = y.rows, N = y.cols;
+        const Tensor& res = tensor_of(a[1], "residual");
+        const int64_t ldr = matching(res, y.t, M, N, kind, "residual");
+        const uint16_t *w = vector_of<uint16_t>(a[2], y.t, N, kind, "weight"),
+                       *next = vector_of<uint16_t>(a[3], y.t, N, kind, "next_weight");
+        const Gates gate(a[4], y.t);
+        const double scale = double_of(a[5]), eps = double_of(a[6]);
+        const bool norm = int_of(a[7]) != 0;
+        if (!norm && next) bad_value("next_weight is given for a norm that is not asked for");
+        on_gpu(y.t, "y");
+        const Wanted total(a[8], true, y.t, M, N, "total_out"), normed(a[9], norm, y.t, M, N, "normed_out");
+        const int st = sandwich_norm_fwd(M, N, y.data, y.ld, data_of<uint16_t>(res), ldr, w, next, gate.data, gate.count, gate.ld,
+                                         (float)scale, (float)eps, total.data, total.ld, normed.data, normed.ld, y.fmt,
+                                         stream_of(a[10]));
+        return st == GR_OK ? tuple_of({&total.t, &normed.t}) : failed(st);
+    });
+}
+
+// y, dtotal, dnormed, total, weight, next_weight, gate, scale, eps, workspace, stream
+PyObject* sandwich_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return entry(n, 11, [&]() -> PyObject* {
+        const Matrix y(a[0], "y");
+        const auto kind = y.t.scalar_type();
+        const int64_t M = y.rows, N = y.cols;
+        const Maybe dt(a[1], y.t, M, N, "dtotal"), dn(a[2], y.t, M, N, "dnormed");
+        if (a[1] == Py_None && a[2] == Py_None) bad_value("dtotal or dnormed is needed");
+        const Matrix total(a[3], "total");
+        const int64_t ldt = matching(total.t, y.t, M, N, kind, "total");
+        const uint16_t *w = vector_of<uint16_t>(a[4], y.t, N, kind, "weight"),
+                       *next = vector_of<uint16_t>(a[5], y.t, N, kind, "next_weight");
+        const Gates gate(a[6], y.t);
+        const double scale = double_of(a[7]), eps = double_of(a[8]);
+        on_gpu(y.t, "y");
+        const Wanted dy(Py_None, true, y.t, M, N, "dy"), dr(Py_None, true, y.t, M, N, "dresidual");
+        const Tensor dw = vector_like(a[4] != Py_None, y.t, N), dnext = vector_like(a[5] != Py_None && a[2] != Py_None, y.t, N);
+        Tensor dgate;
+        if (gate.flat) dgate = empty_like(y.t, {N}, kind);
+        else if (gate.count > 0) dgate = empty_like(y.t, {gate.count, N}, kind);
+        int64_t need = 0;
+        int st = GR_OK;
+        if (dw.defined() || dnext.defined() || dgate.defined()) {
+            st = sandwich_norm_bwd_workspace_size(M, N, gate.count, &need);
+            if (st != GR_OK) return failed(st);
+        }
+        const Scratch ws(a[9], y.t, need);
+        st = sandwich_norm_bwd(M, N, dt.data, dt.ld, dn.data, dn.ld, y.data, y.ld, total.data, ldt, w, next, gate.data, gate.count,
+                               gate.ld, (float)scale, (float)eps, dy.data, dy.ld, dr.data, dr.ld, data_or_null(dw),
+                               data_or_null(dnext), data_or_null(dgate), N > 0 ? N : 1, y.fmt, ws.data, ws.bytes,
+                               stream_of(a[10]));
+        return st == GR_OK ? tuple_of({&dy.t, &dr.t, &dw, &dnext, &dgate}) : failed(st);
+    });
+}
+
+// A batch of matrices (or one) with unit column stride: B x rows x cols.
+struct Batch {
+    int64_t count = 1, rows, cols, ld, stride;
+
+    Batch(const Tensor& t, const char* what) {
+        if (t.dim() != 2 && t.dim() != 3) bad_value(std::string(what) + " must be a matrix or a batch of matrices");
+        const int d = (int)t.dim();
+        rows = t.size(d - 2);
+        cols = t.size(d - 1);
+        if (cols > 1 && rows > 0 && t.stride(d - 1) != 1) bad_value(std::string(what) + " needs unit column stride");
+        ld = cols > 0 ? cols : 1;
+        if (rows > 1 && cols > 0) ld = t.stride(d - 2);
+        const int64_t span = rows > 0 ? (rows - 1) * ld + cols : 0;
+        stride = span;
+        if (d == 3) {
+            count = t.size(0);
+            if (count > 1 && span > 0) stride = t.stride(0);
+        }
+        if (span > 0 && (ld < cols || stride < span)) bad_value(std::string(what) + " has rows or matrices that share memory");
+    }
+};
+
+// update, steps, a, b, c, scale, eps, out, workspace, stream
+PyObject* orthogonalize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return entry(n, 10, [&]() -> PyObject* {
+        const Tensor& g = tensor_of(a[0], "update");
+        const int fmt = g.scalar_type() == at::kFloat ? GR_FMT_F32 : format_of(g.scalar_type());
+        if (fmt < 0) bad_type(std::string("update must be float16, bfloat16 or float32, got ") + c10::toString(g.scalar_type()));
+        const Batch in(g, "update");
+        const int64_t steps = int_of(a[1]);
+        const float k[3] = {(float)double_of(a[2]), (float)double_of(a[3]), (float)double_of(a[4])};
+        const double scale = double_of(a[5]), eps = double_of(a[6]);
+        on_gpu(g, "update");
+        Tensor out;
+        if (const Tensor* given = maybe_tensor(a[7], "out")) {
+            check_kind(*given, g.sizes(), at::kBFloat16, "out");
+            check_place(*given, g, "out");
+            out = *given;
+        } else {
+            out = empty_like(g, g.sizes(), at::kBFloat16);
+        }
+        const Batch to(out, "out");
+        int64_t need = 0;
+        int st = orthogonalize_workspace_size(in.count, in.rows, in.cols, &need);
+        if (st != GR_OK) return failed(st);
+        const Scratch ws(a[8], g, need);
+        st = orthogonalize_update(in.count, in.rows, in.cols, g.data_ptr(), in.ld, in.stride, fmt, k,
+                                  steps > 0 && steps < 1000 ? (int)steps : 0, (float)scale, (float)eps, data_of<uint16_t>(out),
+                                  to.ld, to.stride, ws.data, ws.bytes, stream_of(a[9]));
+        return st == GR_OK ? THPVariable_Wrap(out) : failed(st);
+    });
+}
+
 #define CALL(name, fn) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(fn)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {CALL("rms_norm", rms_norm),         CALL("gated_act", gated_act),
                           CALL("linear_mxfp4", linear_mxfp4), CALL("gemm_mxfp4", gemm_mxfp4),
                           CALL("moe_route", moe_route_),      CALL("moe_mxfp4", moe_mxfp4),
+                          CALL("gated_linear", gated_linear), CALL("linear_backward", linear_backward_),
+                          CALL("gated_linear_backward", gated_linear_backward_),
+                          CALL("sandwich_norm", sandwich_norm),
+                          CALL("sandwich_norm_backward", sandwich_norm_backward),
+                          CALL("orthogonalize", orthogonalize),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

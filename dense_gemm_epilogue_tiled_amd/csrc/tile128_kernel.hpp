@@ -75,7 +75,7 @@ template <bool EDGE, bool SPLIT, bool BT = false, typename E = ElemF16>
 __global__ __launch_bounds__(THREADS, 2) void gemm_relu_tile128_kernel(
     const uint16_t* __restrict__ A, const uint16_t* __restrict__ B, uint16_t* __restrict__ C, int64_t M, int64_t N,
     int64_t K, int64_t lda, int64_t ldb, int64_t ldc, uint32_t tiles_m, uint32_t tiles_n, uint32_t group_m,
-    int vec_c, float* __restrict__ part, int64_t k_per_split, EpiArgs ep) {
+    int vec_c, float* __restrict__ part, int64_t k_per_split, typename E::Args ep) {
     using tile2::barrier;
     using tile2::dma16;
     using tile2::read_a_operand;
@@ -93,9 +93,20 @@ __global__ __launch_bounds__(THREADS, 2) void gemm_relu_tile128_kernel(
     const uint32_t wg = SPLIT ? blockIdx.x % tiles : blockIdx.x;
     const int64_t split = SPLIT ? blockIdx.x / tiles : 0;
     uint32_t tm, tn;
-    tile_of_workgroup(wg, SPLIT ? tiles : gridDim.x, tiles_m, tiles_n, group_m, tm, tn);
+    if constexpr (E::kOwn) {
+        static_assert(BT && !SPLIT, "own epilogues: B transposed, all of K");
+        E::tile(ep, tiles_m, tiles_n, group_m, tm, tn);
+        E::batch(ep, A, B, C);
+    } else {
+        tile_of_workgroup(wg, SPLIT ? tiles : gridDim.x, tiles_m, tiles_n, group_m, tm, tn);
+    }
+    // columns of C per tile and per wave (half as many where rows of Bt are
+    // paired: LDS rows 64 wn .. + 31 are rows of Bt's first half, the next 32 the
+    // same rows of its second half, in accumulator blocks 0 and 1)
+    constexpr int ON = E::kPairs ? BN / 2 : BN;
+    constexpr int WAVE_ON = E::kPairs ? WAVE_TN / 2 : WAVE_TN;
     const int64_t m0 = (int64_t)tm * BM;
-    const int64_t n0 = (int64_t)tn * BN;
+    const int64_t n0 = (int64_t)tn * ON;
     // K range of this workgroup (all of K unless split).
     const int64_t k_begin = SPLIT ? split * k_per_split : 0;
     const int64_t k_rest = K - k_begin > 0 ? K - k_begin : 0;
@@ -105,7 +116,9 @@ __global__ __launch_bounds__(THREADS, 2) void gemm_relu_tile128_kernel(
     // A block = 16 rows x 64 bytes; lane -> row lane/4, slot lane%4.
     // B block = 4 rows x 256 bytes; lane -> row lane/16, slot lane%16.
     const uint8_t* base_a = reinterpret_cast<const uint8_t*>(A + m0 * lda + k_begin);
-    const uint8_t* base_b = reinterpret_cast<const uint8_t*>(BT ? B + n0 * ldb + k_begin : B + k_begin * ldb + n0);
+    const uint8_t* base_b;
+    if constexpr (E::kPairs) base_b = reinterpret_cast<const uint8_t*>(B + (n0 + (int64_t)(wave & 1u) * ep.half) * ldb);
+    else base_b = reinterpret_cast<const uint8_t*>(BT ? B + n0 * ldb + k_begin : B + k_begin * ldb + n0);
     const int64_t step_a = BK * 2;
     const int64_t step_b = BT ? (int64_t)BK * 2 : (int64_t)BK * ldb * 2;
     uint32_t off_a[COPIES], off_b[COPIES];
@@ -118,8 +131,9 @@ __global__ __launch_bounds__(THREADS, 2) void gemm_relu_tile128_kernel(
         if constexpr (EDGE) ra_src = m0 + ra < M ? ra : (uint32_t)(M - 1 - m0);
         off_a[i] = (uint32_t)((ra_src * lda + 8u * ca) * 2);
         if constexpr (BT) {
-            uint32_t rb_src = ra;  // row n0 + ra of Bt, clamped to N-1
-            if constexpr (EDGE) rb_src = n0 + ra < N ? ra : (uint32_t)(N - 1 - n0);
+            uint32_t rb_src = ra;  // row n0 + rb_src of Bt (or of its half), clamped to N-1
+            if constexpr (E::kPairs) rb_src = 32u * (wave >> 1) + 16u * (uint32_t)i + (lane >> 2);
+            if constexpr (EDGE) rb_src = n0 + rb_src < N ? rb_src : (uint32_t)(N - 1 - n0);
             off_b[i] = (uint32_t)((rb_src * ldb + 8u * ca) * 2);
         } else {
             const uint32_t rb = 4u * blk + (lane >> 4);
@@ -203,7 +217,10 @@ __global__ __launch_bounds__(THREADS, 2) void gemm_relu_tile128_kernel(
                     acc[i][j] = E::mfma32(fb[s][j], fa[s][i], acc[i][j]);
     }
 
-    if constexpr (SPLIT) {
+    if constexpr (E::kOwn) {
+        E::template store_tile<EDGE>(acc, lds + wave * epi::WaveTile<FM, FN>::REGION_BYTES, lane, C, ldc,
+                                     m0 + wm * WAVE_TM, n0 + wn * WAVE_ON, m0, M, N, ep);
+    } else if constexpr (SPLIT) {
         epi::store_partials<EDGE>(acc, part + split * M * N, lane, m0 + wm * WAVE_TM, n0 + wn * WAVE_TN, M, N);
         (void)C;
         (void)ldc;

@@ -73,7 +73,7 @@ template <bool EDGE, typename E = ElemF16>
 __global__ __launch_bounds__(THREADS, 1) void gemm_relu_tile3t_kernel(
     const uint16_t* __restrict__ A, const uint16_t* __restrict__ Bt, uint16_t* __restrict__ C, int64_t M, int64_t N,
     int64_t K, int64_t lda, int64_t ldb, int64_t ldc, uint32_t tiles_m, uint32_t tiles_n, uint32_t group_m,
-    int vec_c, EpiArgs ep) {
+    int vec_c, typename E::Args ep) {
     using tile2::barrier;
     using tile2::dma16;
     using tile2::pin;
@@ -90,10 +90,19 @@ __global__ __launch_bounds__(THREADS, 1) void gemm_relu_tile3t_kernel(
     const uint32_t wn = wave & 1u;
 
     uint32_t tm, tn;
-    tile_of_workgroup(blockIdx.x, gridDim.x, tiles_m, tiles_n, group_m, tm, tn);
+    if constexpr (E::kOwn) {
+        E::tile(ep, tiles_m, tiles_n, group_m, tm, tn);
+        E::batch(ep, A, Bt, C);
+    } else {
+        tile_of_workgroup(blockIdx.x, gridDim.x, tiles_m, tiles_n, group_m, tm, tn);
+    }
+    // columns of C per tile and per wave: half as many as rows of Bt where
+    // those are paired
+    constexpr int ON = E::kPairs ? BN / 2 : BN;
+    constexpr int WAVE_ON = E::kPairs ? WAVE_TN / 2 : WAVE_TN;
     const int64_t m_tile = (int64_t)tm * BM;
     const int64_t m0 = EDGE ? edge::shifted_row0(m_tile, M, BM) : m_tile;
-    const int64_t n0 = (int64_t)tn * BN;
+    const int64_t n0 = (int64_t)tn * ON;
 
     // ---- copies -------------------------------------------------------------
     // A strip = 32 blocks of 8 rows x 128 bytes; this wave fills blocks
@@ -102,7 +111,13 @@ __global__ __launch_bounds__(THREADS, 1) void gemm_relu_tile3t_kernel(
     // which leaves the XOR term unchanged: for A that is a wave-uniform base
     // offset; rows of Bt past N are clamped to row N-1, so Bt keeps 8 offsets.
     const uint8_t* base_a = reinterpret_cast<const uint8_t*>(A + m0 * lda);
-    const uint8_t* base_b = reinterpret_cast<const uint8_t*>(Bt + n0 * ldb);
+    // Paired rows: LDS rows 128 wn .. + 63 are rows n0 + 64 wn .. of Bt's first
+    // half, the next 64 the same rows of its second half, so that this wave's 64
+    // rows come from one half and a lane holds both values of a pair
+    // (accumulator blocks j and j + 4).
+    const uint8_t* base_b;
+    if constexpr (E::kPairs) base_b = reinterpret_cast<const uint8_t*>(Bt + (n0 + (int64_t)(wave & 1u) * ep.half) * ldb);
+    else base_b = reinterpret_cast<const uint8_t*>(Bt + n0 * ldb);
     constexpr int64_t step_k = BKS * 2;  // bytes per strip along a row
     uint32_t off_a[4], off_b[8];
 #pragma unroll
@@ -111,7 +126,8 @@ __global__ __launch_bounds__(THREADS, 1) void gemm_relu_tile3t_kernel(
         const uint32_t c = (lane & 7u) ^ ((r >> 1) & 7u);
         if (i < 4) off_a[i] = (uint32_t)((r * lda + 8u * c) * 2);
         uint32_t rn = r;
-        if constexpr (EDGE) rn = n0 + r < N ? r : (uint32_t)(N - 1 - n0);
+        if constexpr (E::kPairs) rn = 64u * (wave >> 1) + 8u * (uint32_t)i + (lane >> 3);
+        if constexpr (EDGE) rn = n0 + rn < N ? rn : (uint32_t)(N - 1 - n0);
         off_b[i] = (uint32_t)((rn * ldb + 8u * c) * 2);
     }
     const int64_t half_a = 32 * lda * 2;
@@ -292,6 +308,12 @@ __global__ __launch_bounds__(THREADS, 1) void gemm_relu_tile3t_kernel(
     // index is then marked as redefined so the epilogue's lane addresses are
     // computed here, not kept from before the main loop (a spilled register
     // otherwise).
+    if constexpr (E::kOwn) {
+        uint32_t elane = lane;
+        asm volatile("" : "+v"(elane));
+        E::template store_tile<EDGE>(acc, lds + wave * epi::REGION_BYTES, elane, C, ldc, m0 + wm * WAVE_TM,
+                                     n0 + wn * WAVE_ON, m_tile, M, N, ep);
+    } else {
     if constexpr (!EDGE && !E::kGeneral) {
         if (vec_c == 8) {
             barrier();
@@ -304,6 +326,7 @@ __global__ __launch_bounds__(THREADS, 1) void gemm_relu_tile3t_kernel(
     asm volatile("" : "+v"(elane));
     epi::store_wave_tile<EDGE, E>(acc, lds + wave * epi::REGION_BYTES, elane, C, ldc, m0 + wm * WAVE_TM,
                                   n0 + wn * WAVE_TN, m_tile, M, N, vec_c, ep);
+    }
 }
 
 #undef GR_LDS

@@ -978,6 +978,146 @@ int moe_w4(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk,
            int act, uint16_t* C, int64_t ldc, int fmt,
            void* workspace, int64_t workspace_bytes, void* stream);
 
+/*
+ * ---- training the feed-forward block ---------------------------------------------
+ * The gated linear layer, the gradients of linear layers, the norms around a block and
+ * an optimizer's orthogonalised update.  The conventions above hold.  A workspace is scratch
+ * of at least the *_workspace_size bytes (256-byte aligned; GR_ERR_SCRATCH if smaller,
+ * GR_ERR_NULL_PTR if NULL where bytes are needed); nothing in it has to be kept between calls.
+ * An output overlapping an input, another output or the workspace is GR_ERR_ALIAS.
+ */
+
+/*
+ * gated_linear_bt -- C := act(g) * u with (g, u) = X * W13^T + b13 in fp32, rounded once:
+ * both projections of a gated feed-forward block, the activation and the product.
+ *   X          M x H in fmt, pitch ldx
+ *   W13        2I x H in fmt, pitch ldw: I gate rows, then I up rows
+ *   b13        2I values in fmt, or NULL
+ *   C          M x I in fmt, pitch ldc
+ *   GU, ldgu   M x 2I in fmt: g and u rounded, what gated_linear_backward needs; or NULL
+ * The activations are those of gemm_bias_act_bt.  Rows may start at any address; any H runs, one that is no
+ * multiple of 32 on copies of X and W13 in the workspace.  Pitches of X and W13 above
+ * 2^22 are GR_ERR_TOO_LARGE.
+ */
+int gated_linear_workspace_size(int64_t M, int64_t I, int64_t H, int64_t* bytes);
+
+int gated_linear_bt(int64_t M, int64_t I, int64_t H,
+                    const uint16_t* X, int64_t ldx,
+                    const uint16_t* W13, int64_t ldw, const uint16_t* b13, int act,
+                    uint16_t* C, int64_t ldc, uint16_t* GU, int64_t ldgu, int fmt,
+                    void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * linear_backward -- the gradients of Y = X * W^T + b:
+ *   dX := dY * W (M x K),  dW := dY^T * X (N x K),  dB[n] := sum over m of dY[m][n]
+ * in fp32, each rounded once to fmt.  dX, dW, dB: NULL for one that is not wanted (W
+ * is read for dX only, X for dW only).  With M = 0, dW and dB are zeros.  The sums over the
+ * tokens run in a fixed order.  The size depends on which gradients are asked for and on the
+ * addresses' alignment: give the pointers of the call.  M above 2^22 - 64 is
+ * GR_ERR_TOO_LARGE.
+ */
+int linear_backward_workspace_size(int64_t M, int64_t N, int64_t K,
+                                   const uint16_t* dY, int64_t lddy,
+                                   const uint16_t* X, int64_t ldx,
+                                   const uint16_t* W, int64_t ldw,
+                                   const uint16_t* dX, int64_t lddx,
+                                   const uint16_t* dW, int64_t lddw, const uint16_t* dB, int64_t* bytes);
+
+int linear_backward(int64_t M, int64_t N, int64_t K,
+                    const uint16_t* dY, int64_t lddy,
+                    const uint16_t* X, int64_t ldx,
+                    const uint16_t* W, int64_t ldw,
+                    uint16_t* dX, int64_t lddx,
+                    uint16_t* dW, int64_t lddw, uint16_t* dB, int fmt,
+                    void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * gated_linear_backward -- the gradients of gated_linear_bt from dH (M x I) and what it kept
+ * in GU (M x 2I):
+ *   dg = dH * u * act'(g),  du = dH * act(g)      (fp32, rounded to fmt)
+ *   dX := (dg, du) * W13 (M x H),  dW13 := (dg, du)^T * X (2I x H),  dB13 := the sums of (dg, du)
+ * as in linear_backward.  The derivative of GR_ACT_RELU at 0 is 0.
+ */
+int gated_linear_backward_workspace_size(int64_t M, int64_t I, int64_t H,
+                                         const uint16_t* W13, int64_t ldw,
+                                         const uint16_t* dX, int64_t lddx,
+                                         const uint16_t* dW13, const uint16_t* dB13, int64_t* bytes);
+
+int gated_linear_backward(int64_t M, int64_t I, int64_t H,
+                          const uint16_t* dH, int64_t lddh,
+                          const uint16_t* X, int64_t ldx,
+                          const uint16_t* W13, int64_t ldw,
+                          const uint16_t* GU, int64_t ldgu, int act,
+                          uint16_t* dX, int64_t lddx,
+                          uint16_t* dW13, int64_t lddw, uint16_t* dB13, int fmt,
+                          void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * sandwich_norm_fwd -- the norm after a block, its gate and scale, the residual's
+ * addition and the norm before the next block, in one pass:
+ *   total  = round16(R + scale * gate * norm(Y) * w)
+ *   normed = norm(total) * next_w                   (NULL: not wanted)
+ * with norm(v) = v / sqrt(mean over the row of v^2 + eps), in fp32 from 16-bit values, each
+ * rounded once.
+ *   Y, R, total, normed   M x N in fmt
+ *   w, next_w  N values in fmt, NULL for ones
+ *   gate       G x N in fmt (pitch ld_gate), one row for every M / G consecutive rows, G a
+ *              divisor of M (GR_ERR_INVALID_DIM); NULL with G = 0 for ones
+ * total and normed may each be Y or R itself (same pitch), but not the same.  N up to 32768
+ * (GR_ERR_TOO_LARGE); scale and eps finite, eps not negative (GR_ERR_INVALID_ARG).
+ */
+int sandwich_norm_fwd(int64_t M, int64_t N,
+                      const uint16_t* Y, int64_t ldy,
+                      const uint16_t* R, int64_t ldr,
+                      const uint16_t* w, const uint16_t* next_w,
+                      const uint16_t* gate, int64_t G, int64_t ld_gate, float scale, float eps,
+                      uint16_t* total, int64_t ldt,
+                      uint16_t* normed, int64_t ldn, int fmt, void* stream);
+
+/*
+ * sandwich_norm_bwd -- its gradients from dT and dN, those of total and normed (NULL:
+ * zeros, one of them at least is there): dY, dR (M x N), and where they are not NULL dw,
+ * dnext_w (N values; dnext_w needs dN), dgate (G x N; needs gate).  Y and T are the
+ * forward pass's Y and total.  Sums over rows are fp32 in a fixed order.  The workspace holds their partial
+ * sums; a call that asks for none of the three needs none.
+ */
+int sandwich_norm_bwd_workspace_size(int64_t M, int64_t N, int64_t G, int64_t* bytes);
+
+int sandwich_norm_bwd(int64_t M, int64_t N,
+                      const uint16_t* dT, int64_t ld_dt,
+                      const uint16_t* dN, int64_t ld_dn,
+                      const uint16_t* Y, int64_t ldy,
+                      const uint16_t* T, int64_t ldt,
+                      const uint16_t* w, const uint16_t* next_w,
+                      const uint16_t* gate, int64_t G, int64_t ld_gate, float scale, float eps,
+                      uint16_t* dY, int64_t ld_dy,
+                      uint16_t* dR, int64_t ld_dr,
+                      uint16_t* dw, uint16_t* dnext_w, uint16_t* dgate, int64_t ld_dgate, int fmt,
+                      void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * orthogonalize_update -- out := scale * X after `steps` of
+ *   A = X X^T,  X <- a X + (b A + c A A) X,   from X = G / (Frobenius norm of G + eps),
+ * for each of B matrices: singular values go through a s + b s^3 + c s^5 each step, and with
+ * the usual coefficients (3.4445, -4.7750, 2.0315) all but the smallest end near 1.
+ *   G          B x rows x cols in g_fmt (GR_FMT_F16, GR_FMT_BF16 or GR_FMT_F32), pitch ldg and
+ *              batch_g elements from one matrix to the next (of no meaning for B = 1)
+ *   coefficients  a, b, c: host memory
+ *   out        B x rows x cols bfloat16
+ * Products are fp16 x fp16 with fp32 sums, X, A and b A + c A A rounded to 11 bits each step
+ * (scaled by powers of two; singular values up to 8 stay finite).  Sides up to 65536, B up to
+ * 65535 (GR_ERR_TOO_LARGE), 1 to 64 steps (GR_ERR_INVALID_ARG).  A zero matrix gives zeros, one with an infinity or
+ * a NaN gives NaN.
+ */
+#define GR_FMT_F32 2
+int orthogonalize_workspace_size(int64_t B, int64_t rows, int64_t cols, int64_t* bytes);
+
+int orthogonalize_update(int64_t B, int64_t rows, int64_t cols,
+                         const void* G, int64_t ldg, int64_t batch_g, int g_fmt,
+                         const float* coefficients, int steps, float scale, float eps,
+                         uint16_t* out, int64_t ldo, int64_t batch_o,
+                         void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Static, NUL-terminated name of a status code ("GR_OK", "GR_ERR_ALIAS", ...),
  * so that a refused call can be reported with its cause (the fail-loudly
  * behaviour cited at the status codes above).  Unknown codes give
