@@ -297,34 +297,58 @@ struct Poly : Own<In> {
         // (a tile on the diagonal holds its own transpose)
         const bool both = ep.ct != nullptr && !(TRI && row_min == col0 / TILE_COLS<Acc> * TILE_COLS<Acc>);
         uint16_t* const ct = both ? ep.ct + blockIdx.y * ep.batch_ct : nullptr;
-        __syncthreads();
-        by_rows<COLS>(acc, region, lane, [&](int i, uint32_t row, uint32_t c) {
-            const int64_t m = row0 + 32 * i + row, n = col0 + 8 * c;
-            const bool mine = !EDGE || (m >= row_min && m < M && n < N);
-            float v[8];
-            staged8<CHUNKS>(region, row, 2 * c, v);
+        const uint32_t c = lane % LPR;
+        const int64_t n = col0 + 8 * c;
+        // D of 32 rows is fetched before the 32 rows in front of them are worked on: a load
+        // where it is needed would cost every one of them its latency (4096 x 8192 x 4096:
+        // 275 -> 226 us)
+        constexpr int IT = 32 / RPI;
+        u32x4 next[IT];
+        auto fetch = [&](int i) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(v[e], ep.alpha, m == n + e ? ep.diag : 0.0f);
-            if (d != nullptr && mine) {
+            for (int k = 0; k < IT; ++k) {
+                const int64_t m = row0 + 32 * i + RPI * k + lane / LPR;
+                next[k] = u32x4{0u, 0u, 0u, 0u};
+                if (EDGE && (m < row_min || m >= M || n >= N)) continue;
                 const uint16_t* const src = d + m * ep.ldd + n;
                 if (!EDGE || n + 8 <= N) {
-                    const u32x4 w = *reinterpret_cast<const u32x4_any*>(src);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(ep.beta, widen8<In>(w, e), v[e]);
+                    next[k] = *reinterpret_cast<const u32x4_any*>(src);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        if (n + e < N) v[e] = __builtin_fmaf(ep.beta, In::widen(src[e]), v[e]);
+                        if (n + e < N) next[k][e / 2] |= (uint32_t)src[e] << (16 * (e % 2));
                 }
             }
-            if (mine) put8<EDGE, false>(C + m * ldc + n, round8<Out>(v), n, 0, N);
-            if (ct == nullptr) return;
-            *reinterpret_cast<f32x4*>(region + stage_off<CHUNKS>(row, 2 * c)) = f32x4{v[0], v[1], v[2], v[3]};
-            *reinterpret_cast<f32x4*>(region + stage_off<CHUNKS>(row, 2 * c + 1)) = f32x4{v[4], v[5], v[6], v[7]};
-            if (row / RPI != 32 / RPI - 1) return;
-            // all 32 rows are there: columns of 8 rows each, four lanes to a column
+        };
+        if (d != nullptr) fetch(0);
+        __syncthreads();
+#pragma unroll 1
+        for (int i = 0; i < epi::AccTile<Acc>::FM; ++i) {
+            epi::stage_fp32_rows(acc, region, lane,
+                                 [](uint32_t row, uint32_t chunk) { return stage_off<CHUNKS>(row, chunk); });
+            u32x4 now[IT];
+#pragma unroll
+            for (int k = 0; k < IT; ++k) now[k] = d != nullptr ? next[k] : u32x4{0u, 0u, 0u, 0u};
+            if (d != nullptr && i + 1 < epi::AccTile<Acc>::FM) fetch(i + 1);
+#pragma unroll
+            for (int k = 0; k < IT; ++k) {
+                const uint32_t row = RPI * k + lane / LPR;
+                const int64_t m = row0 + 32 * i + row;
+                float v[8];
+                staged8<CHUNKS>(region, row, 2 * c, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = __builtin_fmaf(ep.beta, widen8<In>(now[k], e),
+                                          __builtin_fmaf(v[e], ep.alpha, m == n + e ? ep.diag : 0.0f));
+                if (!EDGE || (m >= row_min && m < M)) put8<EDGE, false>(C + m * ldc + n, round8<Out>(v), n, 0, N);
+                if (ct != nullptr) {
+                    *reinterpret_cast<f32x4*>(region + stage_off<CHUNKS>(row, 2 * c)) = f32x4{v[0], v[1], v[2], v[3]};
+                    *reinterpret_cast<f32x4*>(region + stage_off<CHUNKS>(row, 2 * c + 1)) = f32x4{v[4], v[5], v[6], v[7]};
+                }
+            }
             const int64_t mr = row0 + 32 * i;
-            if (EDGE && (mr < row_min || mr >= M)) return;
+            if (ct == nullptr || (EDGE && (mr < row_min || mr >= M))) continue;
+            // columns of 8 rows each, four lanes to a column
 #pragma unroll 1
             for (uint32_t k = 0; k < COLS / 16; ++k) {
                 const uint32_t col = 16 * k + lane / 4, oct = lane % 4;
@@ -335,7 +359,7 @@ struct Poly : Own<In> {
                 if (!EDGE || col0 + col < N)
                     *reinterpret_cast<u32x4_any*>(ct + (col0 + col) * ep.ldct + mr + 8 * oct) = round8<Out>(t);
             }
-        });
+        }
     }
 
     template <int ROWS, int ON, int T, typename S, typename K>

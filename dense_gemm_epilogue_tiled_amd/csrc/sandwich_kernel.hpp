@@ -283,49 +283,59 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) backward_kernel(BwdArgs
             }
 }
 
-// The sums of the slots' partial sums, a workgroup for 32 columns: 8 threads of a column
-// take every 8th slot and meet in LDS in order.
-constexpr int REDUCE_COLS = 32;
+// The sums of the slots' partial sums: a workgroup of 256 threads for 32 columns, 32 threads
+// for each 4 of them, which take every 32nd slot and meet in LDS in order.  blockIdx.y 0: the
+// first sums, 1: the second.
+constexpr int REDUCE_COLS = 32, REDUCE_PARTS = 32;
 template <typename E>
 __global__ void __launch_bounds__(256) reduce_kernel(BwdArgs a) {
-    __shared__ float red[8][REDUCE_COLS];
-    const int lane = threadIdx.x % REDUCE_COLS, part = threadIdx.x / REDUCE_COLS;  // 8 parts
-    const int64_t n = (int64_t)blockIdx.x * REDUCE_COLS + lane;
-    const bool in = n < a.N;
-    // Each part takes every 8th slot of [first, end); which: the first or second sums.
-    auto total = [&](int64_t first, int64_t end, int which) {
-        float s = 0.0f;
+    __shared__ __attribute__((aligned(16))) float red[REDUCE_PARTS][REDUCE_COLS];
+    const int lane = threadIdx.x % 8, part = threadIdx.x / 8;
+    const int64_t n0 = (int64_t)blockIdx.x * REDUCE_COLS, n = n0 + threadIdx.x;
+    const bool second = blockIdx.y != 0, mine = threadIdx.x < REDUCE_COLS && n < a.N;
+    if (second ? a.dnext_w == nullptr : (a.dw == nullptr && (a.split == 0 || a.dgate == nullptr))) return;
+    typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+    const int64_t c = n0 + 4 * lane;
+    const float* const src = a.part + (second ? a.N : 0) + c;
+    // The sum over the slots [first, end) of column n, for the first 32 threads.
+    auto total = [&](int64_t first, int64_t end) {
         if (end > a.slots) end = a.slots;  // no rows: no slots
-        if (in)
-            for (int64_t k = first + part; k < end; k += 8) s += a.part[(k * 2 + which) * a.N + n];
+        f32x4 s = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (c + 4 <= a.N) {
+#pragma unroll 4
+            for (int64_t k = first + part; k < end; k += REDUCE_PARTS) {
+                const f32x4 v = *reinterpret_cast<const f32x4_any*>(src + k * 2 * a.N);
+                s = f32x4{s[0] + v[0], s[1] + v[1], s[2] + v[2], s[3] + v[3]};
+            }
+        } else {
+            for (int64_t k = first + part; k < end; k += REDUCE_PARTS)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c + i < a.N) s[i] += src[k * 2 * a.N + i];
+        }
         __syncthreads();
-        red[part][lane] = s;
+        *reinterpret_cast<f32x4*>(&red[part][4 * lane]) = s;
         __syncthreads();
         float t = 0.0f;
+        if (threadIdx.x < REDUCE_COLS) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t += red[i][lane];
+            for (int i = 0; i < REDUCE_PARTS; ++i) t += red[i][threadIdx.x];
+        }
         return t;
     };
-    if (a.dnext_w != nullptr) {
-        const float s = total(0, a.slots, 1);
-        if (in && part == 0) a.dnext_w[n] = E::round(s);
-    }
-    if (a.split == 0) {
-        if (a.dw != nullptr) {
-            const float s = total(0, a.slots, 0);
-            if (in && part == 0) a.dw[n] = E::round(s);
-        }
+    if (second || a.split == 0) {
+        const float s = total(0, a.slots);
+        if (mine) (second ? a.dnext_w : a.dw)[n] = E::round(s);
         return;
     }
-    if (a.dw == nullptr && a.dgate == nullptr) return;
-    const float w = in && a.w != nullptr ? E::widen(a.w[n]) : 1.0f;
+    const float w = mine && a.w != nullptr ? E::widen(a.w[n]) : 1.0f;
     float dw = 0.0f;
     for (int64_t g = 0; g < a.groups; ++g) {
-        const float s = total(g * a.split, (g + 1) * a.split, 0);
-        dw = __builtin_fmaf(in && a.gate != nullptr ? E::widen(a.gate[g * a.ld_gate + n]) : 1.0f, s, dw);
-        if (a.dgate != nullptr && in && part == 0) a.dgate[g * a.ld_dgate + n] = E::round(s * w);
+        const float s = total(g * a.split, (g + 1) * a.split);
+        dw = __builtin_fmaf(mine && a.gate != nullptr ? E::widen(a.gate[g * a.ld_gate + n]) : 1.0f, s, dw);
+        if (a.dgate != nullptr && mine) a.dgate[g * a.ld_dgate + n] = E::round(s * w);
     }
-    if (a.dw != nullptr && in && part == 0) a.dw[n] = E::round(dw);
+    if (a.dw != nullptr && mine) a.dw[n] = E::round(dw);
 }
 
 }  // namespace sandwich

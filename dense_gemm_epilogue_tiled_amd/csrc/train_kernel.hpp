@@ -37,20 +37,34 @@ __device__ __forceinline__ u32x4 column8(const uint8_t* tile, uint32_t c, uint32
     return v;
 }
 
-// dst[c][r] = src[r][c] (TRANSPOSED) or dst[r][c] = src[r][c], 0 outside
-// src's rows x cols.  dst has 16-byte rows; it gets rows_pad columns (cols rows) if
-// transposed, else cols_pad columns (rows rows), both multiples of 8.
+// dst[c][r] = src[r][c] (transposed) or dst[r][c] = src[r][c], 0 outside src's rows x
+// cols.  dst has 16-byte rows; it gets `pad` columns, a multiple of 8.
 struct Job {
     const uint16_t* src;
     uint16_t* dst;
     int64_t rows, cols, lds, ldd;
-    int64_t pad;           // rows_pad or cols_pad
-    uint32_t tiles_c;      // tiles across the columns
-    uint32_t tiles;        // all of them
+    int64_t pad;
+    uint32_t tiles_c;  // tiles across the columns
+    uint32_t tiles;    // all of them; 0: nothing to do
+    int transposed;
 };
 
-template <bool TRANSPOSED>
-__device__ __forceinline__ void relayout_tile(const Job& j, uint32_t tile, uint8_t* lds) {
+// Several jobs in one launch: a workgroup per tile, the first job's first.
+constexpr int JOBS = 4;
+struct Jobs {
+    Job job[JOBS];
+};
+
+__global__ void __launch_bounds__(THREADS) relayout_kernel(Jobs jobs) {
+    __shared__ __attribute__((aligned(16))) uint8_t lds[TILE * TILE * 2];
+    uint32_t tile = blockIdx.x;
+    Job j = jobs.job[0];
+#pragma unroll
+    for (int i = 1; i < JOBS; ++i)
+        if (tile >= j.tiles) {
+            tile -= j.tiles;
+            j = jobs.job[i];
+        }
     const int64_t r0 = (int64_t)(tile / j.tiles_c) * TILE, c0 = (int64_t)(tile % j.tiles_c) * TILE;
     u32x4 v[2];
     uint32_t row[2], chunk[2];
@@ -64,31 +78,23 @@ __device__ __forceinline__ void relayout_tile(const Job& j, uint32_t tile, uint8
         const int n = r < j.rows && left > 0 ? (left < 8 ? (int)left : 8) : 0;
         v[i] = n > 0 ? mx::load8(j.src + r * j.lds + c, n, j.cols >= 8) : u32x4{0u, 0u, 0u, 0u};
     }
-    if constexpr (TRANSPOSED) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(lds + tile_off(row[i], chunk[i])) = v[i];
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t o = threadIdx.x + THREADS * i;
-            const uint32_t c = o / 8, oct = o % 8;
-            if (c0 + c < j.cols && r0 + 8 * oct < j.pad)
-                *reinterpret_cast<u32x4*>(j.dst + (c0 + c) * j.ldd + r0 + 8 * oct) = column8(lds, c, oct);
-        }
-    } else {
+    if (!j.transposed) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             if (r0 + row[i] < j.rows && c0 + 8 * chunk[i] < j.pad)
                 *reinterpret_cast<u32x4*>(j.dst + (r0 + row[i]) * j.ldd + c0 + 8 * chunk[i]) = v[i];
+        return;
     }
-}
-
-// Two jobs in one launch: a workgroup per tile, the first job's first.
-template <bool TRANSPOSED>
-__global__ void __launch_bounds__(THREADS) relayout_kernel(Job a, Job b) {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[TILE * TILE * 2];
-    if (blockIdx.x < a.tiles) relayout_tile<TRANSPOSED>(a, blockIdx.x, lds);
-    else relayout_tile<TRANSPOSED>(b, blockIdx.x - a.tiles, lds);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(lds + tile_off(row[i], chunk[i])) = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t o = threadIdx.x + THREADS * i;
+        const uint32_t c = o / 8, oct = o % 8;
+        if (c0 + c < j.cols && r0 + 8 * oct < j.pad)
+            *reinterpret_cast<u32x4*>(j.dst + (c0 + c) * j.ldd + r0 + 8 * oct) = column8(lds, c, oct);
+    }
 }
 
 // ---- the gated activation's backward pass -----------------------------------------------
@@ -131,7 +137,7 @@ __device__ __forceinline__ void value_and_slope(float x, float& a, float& d) {
 struct GatedBwdArgs {
     const uint16_t* dh;  // M x I
     const uint16_t* gu;  // M x 2 I: gates, then ups
-    uint16_t* dgu;       // M x 2 I
+    uint16_t* dgu;       // M x 2 I, zeros from there to the pitch
     uint16_t* dgu_t;     // 2 I x Mp, zeros for the tokens from M on; nullptr: not wanted
     int64_t M, I, ld_dh, ld_gu, ld_dgu, ld_t;
     int act;
@@ -182,6 +188,11 @@ __global__ void __launch_bounds__(THREADS) gated_backward_kernel(GatedBwdArgs a,
         }
         *reinterpret_cast<u32x4*>(lds[0] + tile_off(o / 8, o % 8)) = dg;
         *reinterpret_cast<u32x4*>(lds[1] + tile_off(o / 8, o % 8)) = du;
+    }
+    if (c0 + TILE >= a.I) {
+        const int64_t r = r0 + threadIdx.x / 4;
+        if (r < a.M)
+            for (int64_t c = 2 * a.I + threadIdx.x % 4; c < a.ld_dgu; c += 4) a.dgu[r * a.ld_dgu + c] = 0;
     }
     if (a.dgu_t == nullptr) return;
     __syncthreads();

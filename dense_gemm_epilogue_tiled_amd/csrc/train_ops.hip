@@ -12,19 +12,27 @@
 
 namespace {
 
-gr::train::Job job(const uint16_t* src, int64_t rows, int64_t cols, int64_t lds, uint16_t* dst, int64_t ldd, int64_t pad,
-                   bool transposed) {
-    using gr::train::TILE;
-    const int64_t tr = ceil_div(transposed ? pad : rows, TILE), tc = ceil_div(transposed ? cols : pad, TILE);
-    return {src, dst, rows, cols, lds, ldd, pad, (uint32_t)(tc > 0 ? tc : 1), (uint32_t)(tr * tc)};
-}
-const gr::train::Job kNoJob{nullptr, nullptr, 0, 0, 0, 0, 0, 1, 0};
+// Copies with padded or transposed rows, all of a call's in one launch.
+struct Relayouts {
+    gr::train::Jobs jobs{};
+    int count = 0;
+    int64_t tiles = 0;
 
-template <bool TRANSPOSED>
-int relayout(const gr::train::Job& a, const gr::train::Job& b, hipStream_t stream) {
-    if (a.tiles + b.tiles == 0) return GR_OK;
-    return launch(gr::train::relayout_kernel<TRANSPOSED>, (int64_t)a.tiles + b.tiles, gr::train::THREADS, stream, a, b);
-}
+    Relayouts() {
+        for (gr::train::Job& j : jobs.job) j.tiles_c = 1;
+    }
+    // dst: src (rows x cols, pitch lds) with rows of ldd = pad elements, or src's transpose.
+    void add(bool transposed, const uint16_t* src, int64_t rows, int64_t cols, int64_t lds, uint16_t* dst, int64_t pad) {
+        using gr::train::TILE;
+        const int64_t tr = ceil_div(transposed ? pad : rows, TILE), tc = ceil_div(transposed ? cols : pad, TILE);
+        if (tr * tc == 0) return;
+        jobs.job[count++] = {src, dst, rows, cols, lds, pad, pad, (uint32_t)tc, (uint32_t)(tr * tc), transposed ? 1 : 0};
+        tiles += tr * tc;
+    }
+    int run(hipStream_t stream) const {
+        return tiles == 0 ? GR_OK : launch(gr::train::relayout_kernel, tiles, gr::train::THREADS, stream, jobs);
+    }
+};
 
 // ---- the gated linear layer -----------------------------------------------------------
 
@@ -49,7 +57,10 @@ int run_gated(int64_t M, int64_t I, int64_t H, const uint16_t* X, int64_t ldx, c
         K = gated_pitch(H);
         uint16_t* const xp = reinterpret_cast<uint16_t*>(ws);
         uint16_t* const wp = reinterpret_cast<uint16_t*>(ws + aligned(M * K * 2));
-        const int st = relayout<false>(job(X, M, H, ldx, xp, K, K, false), job(W, 2 * I, H, ldw, wp, K, K, false), stream);
+        Relayouts copies;
+        copies.add(false, X, M, H, ldx, xp, K);
+        copies.add(false, W, 2 * I, H, ldw, wp, K);
+        const int st = copies.run(stream);
         if (st != GR_OK) return st;
         X = xp;
         W = wp;
@@ -59,9 +70,9 @@ int run_gated(int64_t M, int64_t I, int64_t H, const uint16_t* X, int64_t ldx, c
         using namespace gr::smallm;
         constexpr int W4 = 4, cols = 8 * W4;
         const gr::own::GatedArgs args = ep;
-        if (I % cols == 0)
-            return launch(gemm_relu_smallm_bt_stream_kernel<false, E, W4, 16>, ceil_div(I, cols), 64 * W4, stream, X, W, C,
-                          M, I, K, ldx, ldw, ldc, args);
+        if (M <= 4)
+            return launch(gemm_relu_smallm_bt_stream_kernel<true, E, W4, 4>, ceil_div(I, cols), 64 * W4, stream, X, W, C, M,
+                          I, K, ldx, ldw, ldc, args);
         return launch(gemm_relu_smallm_bt_stream_kernel<true, E, W4, 16>, ceil_div(I, cols), 64 * W4, stream, X, W, C, M, I,
                       K, ldx, ldw, ldc, args);
     }
@@ -70,30 +81,67 @@ int run_gated(int64_t M, int64_t I, int64_t H, const uint16_t* X, int64_t ldx, c
 
 // ---- gradients ------------------------------------------------------------------------
 
-// dX = dY W with 256 x 256 tiles and no epilogue but the rounding; other shapes take
-// gemm_bias_act's paths.
+// How dX = dY W (M x K, sums over N) is computed: 256 x 256 tiles with no epilogue but the
+// rounding where they are many; on W transposed, with N padded to whole strips by
+// zeros, where the product of row-major operands would have misaligned rows or a ragged
+// depth (333 x 2080 x 1001: 41 us in place, 13 with the copies) and the copies are not most
+// of the work; else gemm_bias_act's paths.
+enum InputGrad { kTiles, kTransposed, kPaths };
+
 template <typename Base>
 struct Bare : Base {
     static __device__ __forceinline__ uint16_t relu_round(float x) { return (uint16_t)gr::own::round2<Base>(x, x); }
 };
 
-bool input_grad_tiles(int64_t M, int64_t K, int64_t N, const uint16_t* dY, int64_t lddy, const uint16_t* W, int64_t ldw) {
+int64_t padded_depth(int64_t N) { return round_up(N, 64); }
+
+InputGrad input_grad_kind(int64_t M, int64_t K, int64_t N, const uint16_t* dY, int64_t lddy, const uint16_t* W, int64_t ldw) {
     using namespace gr::tile3;
-    return M >= BM && N > 0 && N % BKA == 0 && rows16(dY, lddy) && rows16(W, ldw) && lddy <= gr::tile2::MAX_LDA &&
-           ldw <= gr::tile2::MAX_LDB && ceil_div(M, BM) * ceil_div(K, BN) > 128;
+    const bool whole = rows16(dY, lddy) && rows16(W, ldw) && N > 0;
+    if (whole && M >= BM && N % BKA == 0 && lddy <= gr::tile2::MAX_LDA && ldw <= gr::tile2::MAX_LDB &&
+        ceil_div(M, BM) * ceil_div(K, BN) > 128)
+        return kTiles;
+    if (M > kStreamRows && N > 0 && padded_depth(N) <= kMaxPitch && !(whole && N % 32 == 0)) return kTransposed;
+    return kPaths;
 }
 
-int input_grad_need(int64_t M, int64_t K, int64_t N, const uint16_t* dY, int64_t lddy, const uint16_t* W, int64_t ldw,
-                    const uint16_t* dX, int64_t lddx, int64_t* bytes) {
-    *bytes = 0;
-    if (M == 0 || K == 0 || input_grad_tiles(M, K, N, dY, lddy, W, ldw)) return GR_OK;
-    return gemm_relu_f16_workspace_size(M, K, N, dY, lddy, W, ldw, dX, lddx, bytes);
+// Bytes for W^T, for dY with N padded (not for one that comes padded, `padded`), and for the
+// paths of gemm_bias_act.
+struct InputGradLayout {
+    InputGrad kind = kPaths;
+    int64_t wt = 0, dy = 0, paths = 0;
+    int64_t total() const { return wt + dy + paths; }
+};
+
+int input_grad_layout(int64_t M, int64_t K, int64_t N, const uint16_t* dY, int64_t lddy, bool padded, const uint16_t* W,
+                      int64_t ldw, const uint16_t* dX, int64_t lddx, InputGradLayout* l) {
+    *l = InputGradLayout{};
+    if (M == 0 || K == 0) return GR_OK;
+    l->kind = input_grad_kind(M, K, N, dY, lddy, W, ldw);
+    if (l->kind == kTransposed) {
+        l->wt = aligned(2 * K * padded_depth(N));
+        l->dy = padded ? 0 : aligned(2 * M * padded_depth(N));
+    } else if (l->kind == kPaths) {
+        const int st = gemm_relu_f16_workspace_size(M, K, N, dY, lddy, W, ldw, dX, lddx, &l->paths);
+        l->paths = aligned(l->paths);
+        return st;
+    }
+    return GR_OK;
+}
+
+// The copies that it works on.
+void input_grad_copies(const InputGradLayout& l, int64_t M, int64_t K, int64_t N, const uint16_t* dY, int64_t lddy,
+                       const uint16_t* W, int64_t ldw, uint8_t* ws, Relayouts* copies) {
+    if (l.kind != kTransposed) return;
+    const int64_t Np = padded_depth(N);
+    copies->add(true, W, N, K, ldw, reinterpret_cast<uint16_t*>(ws), Np);
+    if (l.dy > 0) copies->add(false, dY, M, N, lddy, reinterpret_cast<uint16_t*>(ws + l.wt), Np);
 }
 
 template <typename Base>
-int input_grad(int64_t M, int64_t K, int64_t N, const uint16_t* dY, int64_t lddy, const uint16_t* W, int64_t ldw,
-               uint16_t* dX, int64_t lddx, uint8_t* ws, int64_t ws_bytes, hipStream_t stream) {
-    if (input_grad_tiles(M, K, N, dY, lddy, W, ldw)) {
+int input_grad(const InputGradLayout& l, int64_t M, int64_t K, int64_t N, const uint16_t* dY, int64_t lddy, const uint16_t* W,
+               int64_t ldw, uint16_t* dX, int64_t lddx, uint8_t* ws, hipStream_t stream) {
+    if (l.kind == kTiles) {
         using namespace gr::tile3;
         using E = Bare<Base>;
         const uint32_t tm = (uint32_t)ceil_div(M, BM), tn = (uint32_t)ceil_div(K, BN);
@@ -105,8 +153,14 @@ int input_grad(int64_t M, int64_t K, int64_t N, const uint16_t* dY, int64_t lddy
         return launch(gemm_relu_tile3_kernel<true, E>, (int64_t)tm * tn, THREADS, stream, dY, W, dX, M, K, N, lddy, ldw,
                       lddx, tm, tn, kGroupM, vec, ep);
     }
+    if (l.kind == kTransposed) {
+        const int64_t Np = padded_depth(N);
+        const uint16_t* const dyp = l.dy > 0 ? reinterpret_cast<const uint16_t*>(ws + l.wt) : dY;
+        return product<gr::own::Plain<Base>>(choose(1, M, K, Np, 1), 1, M, K, Np, dyp, Np, reinterpret_cast<const uint16_t*>(ws),
+                                             Np, dX, lddx, gr::own::PlainArgs{}, stream);
+    }
     return gemm_bias_act_ws(M, K, N, dY, lddy, W, ldw, nullptr, GR_ACT_NONE, dX, lddx,
-                            Base::kIsF16 ? GR_FMT_F16 : GR_FMT_BF16, ws_bytes > 0 ? ws : nullptr, ws_bytes, stream, -1);
+                            Base::kIsF16 ? GR_FMT_F16 : GR_FMT_BF16, l.paths > 0 ? ws : nullptr, l.paths, stream, -1);
 }
 
 // dW = dY^T X from the transposed operands (pitch Mp each).
@@ -126,8 +180,9 @@ int64_t padded_tokens(int64_t M) { return M > 0 ? round_up(M, gr::train::PAD) : 
 
 // The parts of the workspace, in order; only those of the gradients that are asked for.
 struct GradLayout {
-    int64_t dyt, xt, dy, product;  // bytes: dY^T, X^T, dY (of the gated layer), what dX's product takes
-    int64_t total() const { return dyt + xt + dy + product; }
+    int64_t dyt, xt, dy;    // bytes: dY^T, X^T, dY (of the gated layer)
+    InputGradLayout input;  // what dX's product takes
+    int64_t total() const { return dyt + xt + dy + input.total(); }
 };
 
 int linear_layout(int64_t M, int64_t N, int64_t K, const uint16_t* dY, int64_t lddy, const uint16_t* W, int64_t ldw,
@@ -136,11 +191,8 @@ int linear_layout(int64_t M, int64_t N, int64_t K, const uint16_t* dY, int64_t l
     l->dyt = (dW || dB) ? aligned(2 * N * Mp) : 0;
     l->xt = dW ? aligned(2 * K * Mp) : 0;
     l->dy = 0;
-    l->product = 0;
-    if (!dX) return GR_OK;
-    const int st = input_grad_need(M, K, N, dY, lddy, W, ldw, dX, lddx, &l->product);
-    l->product = aligned(l->product);
-    return st;
+    l->input = InputGradLayout{};
+    return dX ? input_grad_layout(M, K, N, dY, lddy, false, W, ldw, dX, lddx, &l->input) : GR_OK;
 }
 
 
@@ -164,31 +216,31 @@ int run_linear_backward(int64_t M, int64_t N, int64_t K, const uint16_t* dY, int
     const int64_t Mp = padded_tokens(M);
     uint16_t* const dyt = reinterpret_cast<uint16_t*>(ws);
     uint16_t* const xt = reinterpret_cast<uint16_t*>(ws + l.dyt);
-    int st = GR_OK;
-    if (N > 0 && (dB || (dW && K > 0)))
-        st = relayout<true>(job(dY, M, N, lddy, dyt, Mp, Mp, true), dW ? job(X, M, K, ldx, xt, Mp, Mp, true) : kNoJob,
-                            stream);
+    uint8_t* const rest = ws + l.dyt + l.xt;
+    Relayouts copies;
+    if (dB || (dW && K > 0)) copies.add(true, dY, M, N, lddy, dyt, Mp);
+    if (dW && N > 0) copies.add(true, X, M, K, ldx, xt, Mp);
+    if (dX && M > 0 && K > 0) input_grad_copies(l.input, M, K, N, dY, lddy, W, ldw, rest, &copies);
+    int st = copies.run(stream);
     if (st == GR_OK && dW && N > 0 && K > 0) st = weight_grad<Base>(N, K, Mp, dyt, xt, dW, lddw, stream);
     if (st == GR_OK && dB && N > 0) st = bias_grad<Base>(N, Mp, dyt, dB, stream);
     if (st == GR_OK && dX && M > 0 && K > 0)
-        st = input_grad<Base>(M, K, N, dY, lddy, W, ldw, dX, lddx, ws + l.dyt + l.xt, l.product, stream);
+        st = input_grad<Base>(l.input, M, K, N, dY, lddy, W, ldw, dX, lddx, rest, stream);
     return st;
 }
 
 int gated_layout(int64_t M, int64_t I, int64_t H, const uint16_t* W, int64_t ldw, const uint16_t* dX, int64_t lddx,
                  const uint16_t* dW, const uint16_t* dB, GradLayout* l) {
-    const int64_t Mp = padded_tokens(M), ld = round_up(2 * I, 8);
+    const int64_t Mp = padded_tokens(M), ld = padded_depth(2 * I);
     l->dyt = (dW || dB) ? aligned(4 * I * Mp) : 0;
     l->xt = dW ? aligned(2 * H * Mp) : 0;
     l->dy = aligned(2 * M * ld);
-    l->product = 0;
+    l->input = InputGradLayout{};
     if (!dX) return GR_OK;
     // the gradient of the products lies in the workspace: an aligned address that is
     // nobody's stands for it
     const uint16_t* const place = reinterpret_cast<const uint16_t*>(uintptr_t(1) << 62);
-    const int st = input_grad_need(M, H, 2 * I, place, ld, W, ldw, dX, lddx, &l->product);
-    l->product = aligned(l->product);
-    return st;
+    return input_grad_layout(M, H, 2 * I, place, least(ld), true, W, ldw, dX, lddx, &l->input);
 }
 
 int validate_gated_backward(int64_t M, int64_t I, int64_t H, const uint16_t* dH, int64_t lddh, const uint16_t* X,
@@ -201,7 +253,7 @@ int validate_gated_backward(int64_t M, int64_t I, int64_t H, const uint16_t* dH,
     const bool any = dX || dW || dB;
     if (any && M > 0 && I > 0 && (!dH || !GU)) return GR_ERR_NULL_PTR;
     if (M > 0 && I > 0 && H > 0 && ((dX && !W) || (dW && !X))) return GR_ERR_NULL_PTR;
-    if (padded_tokens(M) > kMaxPitch || 2 * I + 8 > kMaxPitch) return GR_ERR_TOO_LARGE;
+    if (padded_tokens(M) > kMaxPitch || 2 * I + 64 > kMaxPitch) return GR_ERR_TOO_LARGE;
     return GR_OK;
 }
 
@@ -210,23 +262,24 @@ int run_gated_backward(int64_t M, int64_t I, int64_t H, const uint16_t* dH, int6
                        const uint16_t* W, int64_t ldw, const uint16_t* GU, int64_t ldgu, int act, uint16_t* dX, int64_t lddx,
                        uint16_t* dW, int64_t lddw, uint16_t* dB, uint8_t* ws, const GradLayout& l, hipStream_t stream) {
     using namespace gr::train;
-    const int64_t Mp = padded_tokens(M), ld = round_up(2 * I, 8);
+    const int64_t Mp = padded_tokens(M), ld = padded_depth(2 * I);
     uint16_t* const dyt = reinterpret_cast<uint16_t*>(ws);
     uint16_t* const xt = reinterpret_cast<uint16_t*>(ws + l.dyt);
     uint16_t* const dgu = reinterpret_cast<uint16_t*>(ws + l.dyt + l.xt);
-    int st = GR_OK;
-    if (I > 0) {
+    uint8_t* const rest = ws + l.dyt + l.xt + l.dy;
+    Relayouts copies;
+    if (dW && I > 0) copies.add(true, X, M, H, ldx, xt, Mp);
+    if (dX && M > 0 && H > 0) input_grad_copies(l.input, M, H, 2 * I, dgu, least(ld), W, ldw, rest, &copies);
+    int st = copies.run(stream);
+    if (st == GR_OK && I > 0) {
         const GatedBwdArgs a{dH, GU, dgu, l.dyt > 0 ? dyt : nullptr, M, I, lddh, ldgu, ld, Mp, act};
         const uint32_t tc = (uint32_t)ceil_div(I, TILE);
         st = launch(gated_backward_kernel<Base>, Mp / TILE * tc, THREADS, stream, a, tc);
     }
-    if (st == GR_OK && dW && I > 0 && H > 0) {
-        st = relayout<true>(job(X, M, H, ldx, xt, Mp, Mp, true), kNoJob, stream);
-        if (st == GR_OK) st = weight_grad<Base>(2 * I, H, Mp, dyt, xt, dW, lddw, stream);
-    }
+    if (st == GR_OK && dW && I > 0 && H > 0) st = weight_grad<Base>(2 * I, H, Mp, dyt, xt, dW, lddw, stream);
     if (st == GR_OK && dB && I > 0) st = bias_grad<Base>(2 * I, Mp, dyt, dB, stream);
     if (st == GR_OK && dX && M > 0 && H > 0)
-        st = input_grad<Base>(M, H, 2 * I, dgu, ld, W, ldw, dX, lddx, ws + l.dyt + l.xt + l.dy, l.product, stream);
+        st = input_grad<Base>(l.input, M, H, 2 * I, dgu, least(ld), W, ldw, dX, lddx, rest, stream);
     return st;
 }
 

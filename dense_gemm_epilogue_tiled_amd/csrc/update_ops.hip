@@ -87,7 +87,7 @@ int run_sandwich_backward(const gr::sandwich::BwdArgs& a, hipStream_t stream) {
                                : launch(backward_kernel<E, TPR, C, false>, grid, threads, stream, a);
         });
     if (st != GR_OK || a.part == nullptr) return st;
-    return launch(reduce_kernel<E>, ceil_div(a.N, REDUCE_COLS), 256, stream, a);
+    return launch_grid(reduce_kernel<E>, dim3((uint32_t)ceil_div(a.N, REDUCE_COLS), 2), 256, stream, a);
 }
 
 // ---- orthogonalised update ----------------------------------------------------------------
