@@ -23,7 +23,7 @@
 
 #include "norm_kernel.hpp"
 #include "own_epilogue.hpp"
-#include "train_kernel.hpp"
+#include "transpose.hpp"
 
 namespace gr {
 namespace ortho {

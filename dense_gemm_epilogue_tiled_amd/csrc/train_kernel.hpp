@@ -6,36 +6,17 @@
 // written per element, nothing next to the product's 2 M operations per element), with
 // the tokens padded by zeros to whole strips of 64, and the product is then the one of two
 // k-contiguous operands.  All of these kernels are bound by memory: every element is
-// read once and written once, in 16-byte pieces; a tile passes through LDS for the
-// transposition, 16-byte chunk c of row r at slot c XOR (r / 8) mod 8, so that the
-// eight lanes that gather a column's octets of rows meet eight distinct groups of banks.
+// read once and written once, in 16-byte pieces.
 #pragma once
 
 #include "norm_kernel.hpp"
 #include "own_epilogue.hpp"
+#include "transpose.hpp"
 
 namespace gr {
 namespace train {
 
-constexpr int THREADS = 256;
-constexpr int TILE = 64;     // rows and columns of a tile
-constexpr int PAD = 64;      // tokens of a transposed operand: whole strips of this
-
-__device__ __forceinline__ uint32_t tile_off(uint32_t r, uint32_t chunk) {
-    return r * (TILE * 2) + ((chunk ^ ((r >> 3) & 7u)) << 4);
-}
-
-// Eight rows 8 oct .. of column c of a staged tile.
-__device__ __forceinline__ u32x4 column8(const uint8_t* tile, uint32_t c, uint32_t oct) {
-    u32x4 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = *reinterpret_cast<const uint16_t*>(tile + tile_off(8 * oct + 2 * i, c >> 3) + 2 * (c & 7u));
-        const uint32_t hi = *reinterpret_cast<const uint16_t*>(tile + tile_off(8 * oct + 2 * i + 1, c >> 3) + 2 * (c & 7u));
-        v[i] = lo | (hi << 16);
-    }
-    return v;
-}
+constexpr int PAD = 64;  // tokens of a transposed operand: whole strips of this
 
 // dst[c][r] = src[r][c] (transposed) or dst[r][c] = src[r][c], 0 outside src's rows x
 // cols.  dst has 16-byte rows; it gets `pad` columns, a multiple of 8.
