@@ -8,7 +8,7 @@
 
 #include "../../include/gemm_relu.h"
 #include "own_products.hpp"
-#include "ortho_kernel.hpp"
+#include "ortho_small_kernel.hpp"
 #include "sandwich_kernel.hpp"
 
 namespace {
@@ -97,7 +97,8 @@ struct OrthoLayout {
     int64_t r, c;    // narrow and wide side
     int64_t rp, cp;  // padded
     int64_t parts, x, a;  // bytes: partial sums, one of the four X buffers, one of A and B
-    int64_t total() const { return parts + 4 * x + 2 * a; }
+    bool small;           // in one workgroup's LDS, without a workspace
+    int64_t total() const { return small ? 0 : parts + 4 * x + 2 * a; }
 };
 
 OrthoLayout ortho_layout(int64_t B, int64_t rows, int64_t cols) {
@@ -110,6 +111,7 @@ OrthoLayout ortho_layout(int64_t B, int64_t rows, int64_t cols) {
     l.parts = aligned(B * gr::ortho::PARTS * 8);
     l.x = aligned(B * l.rp * l.cp * 2);
     l.a = aligned(B * l.rp * l.rp * 2);
+    l.small = l.rp <= gr::ortho::SMALL_R && 2 * l.rp * (l.rp + l.cp) <= gr::ortho::SMALL_LDS;
     return l;
 }
 
@@ -121,6 +123,13 @@ int ortho_prepare(const gr::ortho::PrepArgs& a, int64_t B, hipStream_t stream) {
     const uint32_t tc = (uint32_t)(a.cols_pad / gr::train::TILE);
     return launch_grid(normalise_kernel<In>, dim3((uint32_t)(a.rows_pad / gr::train::TILE) * tc, (uint32_t)B), 256, stream, a,
                        tc);
+}
+
+template <typename In>
+int run_small(const OrthoLayout& l, int64_t B, const gr::ortho::SmallArgs& a, hipStream_t stream) {
+    using namespace gr::ortho;
+    return l.rp <= 64 ? launch(small_kernel<In, 64>, B, SMALL_THREADS, stream, a)
+                      : launch(small_kernel<In, 128>, B, SMALL_THREADS, stream, a);
 }
 
 template <typename Out>
@@ -267,6 +276,15 @@ int orthogonalize_update(int64_t B, int64_t rows, int64_t cols, const void* G, i
     st = check_regions(written, read);
     if (st == GR_OK) st = check_device();
     if (st != GR_OK) return st;
+    hipStream_t h = static_cast<hipStream_t>(stream);
+    const float k[3] = {coefficients[0], coefficients[1], coefficients[2]};
+    if (l.small) {
+        const gr::ortho::SmallArgs a{G, out, rows, cols, ldg, batch_g, ldo, batch_o, (uint32_t)l.cp, l.tall ? 1 : 0, steps,
+                                     k[1], k[2], k[0] + k[1] + k[2], scale, eps};
+        return g_fmt == GR_FMT_F32    ? run_small<gr::ortho::ElemF32>(l, B, a, h)
+               : g_fmt == GR_FMT_BF16 ? run_small<ElemBF16>(l, B, a, h)
+                                      : run_small<ElemF16>(l, B, a, h);
+    }
     uint8_t* at = static_cast<uint8_t*>(workspace);
     auto take = [&](int64_t bytes) {
         uint16_t* const p = reinterpret_cast<uint16_t*>(at);
@@ -278,7 +296,6 @@ int orthogonalize_update(int64_t B, int64_t rows, int64_t cols, const void* G, i
     uint16_t* const xt[2] = {take(l.x), take(l.x)};
     uint16_t* const a = take(l.a);
     uint16_t* const b = take(l.a);
-    hipStream_t h = static_cast<hipStream_t>(stream);
     const int64_t rows_pad = l.tall ? l.cp : l.rp, cols_pad = l.tall ? l.rp : l.cp;
     const gr::ortho::PrepArgs prep{G,        rows,     cols,         ldg, batch_g, part, l.tall ? xt[0] : x[0], l.tall ? x[0] : xt[0],
                                    rows_pad, cols_pad, l.rp * l.cp, eps};
@@ -286,7 +303,6 @@ int orthogonalize_update(int64_t B, int64_t rows, int64_t cols, const void* G, i
          : g_fmt == GR_FMT_BF16 ? ortho_prepare<ElemBF16>(prep, B, h)
                                 : ortho_prepare<ElemF16>(prep, B, h);
     if (st != GR_OK) return st;
-    const float k[3] = {coefficients[0], coefficients[1], coefficients[2]};
     return run_ortho<ElemBF16>(l, B, k, steps, scale, out, ldo, batch_o, x, xt, a, b, h);
 }
 
