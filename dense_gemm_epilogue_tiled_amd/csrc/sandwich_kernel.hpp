@@ -18,7 +18,9 @@
 // memory: a row is held in registers, every input is read once and every output
 // written once (forward 4, backward 6 matrices of M x N).  TPR threads hold a row, at
 // most C chunks of 8 columns each.  Backward, a thread keeps its columns' sums in
-// registers over the rows of its workgroup, so that only one partial sum per workgroup (or wave,
+// registers over the rows of its workgroup (one chunk per thread up to 8192 columns: with two, half
+// as many waves find room, 8192 x 8192 201 us against 190; beyond that the sums do not all
+// fit and some are spilled), so that only one partial sum per workgroup (or wave,
 // where a wave holds a row) and column goes through memory; a second kernel adds
 // those in a fixed order.
 #pragma once
@@ -31,6 +33,11 @@ namespace sandwich {
 
 constexpr int64_t MAX_N = 32768;
 
+// Rows that the threads of a workgroup hold at once (a wave each, or all of them one), and
+// the threads.
+constexpr int rows_at_once(int tpr) { return tpr == 64 ? 4 : 1; }
+constexpr int threads_for(int tpr) { return tpr == 64 ? 256 : tpr; }
+
 struct Args {
     const uint16_t *y, *residual, *w, *next_w, *gate;  // w, next_w, gate: nullptr for ones
     uint16_t *total, *normed;                          // normed: nullptr if not wanted
@@ -39,23 +46,43 @@ struct Args {
     float scale, eps;
 };
 
-// The chunks of 8 columns that thread t of TPR has of rows of N: how many columns
-// each holds.
-template <int TPR, int C>
+// The chunks of 8 columns that thread t of TPR has of rows of N: how many columns each
+// holds.  WHOLE: N is a multiple of 8, so that a chunk holds 8 or none; a thread then loads
+// without a branch (where it has none, the row's last chunk, for zeros), and all of its loads
+// are in flight at once.
+template <int TPR, int C, bool WHOLE>
 struct Columns {
     int n[C];
     bool more;  // 8 columns or more: a short chunk has 8 - n before it
-    int64_t at[C];
+    uint32_t at[C];
     __device__ __forceinline__ Columns(int t, int64_t N) : more(N > 8) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            at[c] = 8 * (t + (int64_t)c * TPR);
-            n[c] = at[c] < N ? (N - at[c] < 8 ? (int)(N - at[c]) : 8) : 0;
+            const uint32_t first = 8u * (uint32_t)(t + c * TPR);
+            n[c] = first < N ? (N - first < 8 ? (int)(N - first) : 8) : 0;
+            at[c] = WHOLE && n[c] == 0 ? (uint32_t)N - 8u : first;
         }
     }
     __device__ __forceinline__ void load(const uint16_t* row, u32x4 (&v)[C]) const {
 #pragma unroll
-        for (int c = 0; c < C; ++c) v[c] = n[c] > 0 ? mx::load8(row + at[c], n[c], more) : u32x4{0u, 0u, 0u, 0u};
+        for (int c = 0; c < C; ++c) {
+            if constexpr (WHOLE) v[c] = *reinterpret_cast<const own::u32x4_any*>(row + at[c]);
+            else v[c] = n[c] > 0 ? mx::load8(row + at[c], n[c], more) : u32x4{0u, 0u, 0u, 0u};
+        }
+    }
+    // Zeros where there are no columns.
+    __device__ __forceinline__ void clear(u32x4 (&v)[C]) const {
+        if constexpr (WHOLE) {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[c][i] = n[c] > 0 ? v[c][i] : 0u;
+        }
+    }
+    __device__ __forceinline__ void store(uint16_t* row, int c, const u32x4& v) const {
+        if (n[c] == 0) return;
+        if constexpr (WHOLE) *reinterpret_cast<own::u32x4_any*>(row + at[c]) = v;
+        else own::put8<true, false>(row + at[c], v, 0, 0, n[c]);
     }
 };
 
@@ -74,29 +101,26 @@ __device__ __forceinline__ void row_sums(float (&v)[K], float* red) {
             for (int k = 0; k < K; ++k) red[k * W + threadIdx.x / 64] = v[k];
         }
         __syncthreads();
+        const int lane = threadIdx.x % 64;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            float t = 0.0f;
-#pragma unroll
-            for (int i = 0; i < W; ++i) t += red[k * W + i];
-            v[k] = t;
-        }
+        for (int k = 0; k < K; ++k) v[k] = mx::wave_sum(lane < W ? red[k * W + lane] : 0.0f);
     }
 }
 
-template <typename E, int TPR, int C>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) forward_kernel(Args a) {
-    constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
+template <typename E, int TPR, int C, bool WHOLE>
+__global__ void __launch_bounds__(threads_for(TPR)) forward_kernel(Args a) {
+    constexpr int kRows = rows_at_once(TPR);
     __shared__ float red[2][TPR > 64 ? TPR / 64 : 1];
     const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
     if (row >= a.M) return;  // whole waves, and no barrier where TPR is 64
-    const Columns<TPR, C> col(threadIdx.x % TPR, a.N);
+    const Columns<TPR, C, WHOLE> col(threadIdx.x % TPR, a.N);
     u32x4 y[C], s[C], w[C], g[C], w2[C];
     col.load(a.y + row * a.ldy, y);
     col.load(a.residual + row * a.ldr, s);
     if (a.w != nullptr) col.load(a.w, w);
     if (a.gate != nullptr) col.load(a.gate + row / a.group * a.ld_gate, g);
     if (a.next_w != nullptr) col.load(a.next_w, w2);
+    col.clear(y);
     float sum[1] = {0.0f};
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -120,7 +144,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) forward_kernel(Args a) 
         }
         s[c] = own::round8<E>(v);
         if (col.n[c] > 0) {
-            own::put8<true, false>(a.total + row * a.ldt + col.at[c], s[c], 0, 0, col.n[c]);
+            col.store(a.total + row * a.ldt, c, s[c]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float z = i < col.n[c] ? own::widen8<E>(s[c], i) : 0.0f;
@@ -140,7 +164,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) forward_kernel(Args a) 
             v[i] = own::widen8<E>(s[c], i) * r2;
             if (a.next_w != nullptr) v[i] *= own::widen8<E>(w2[c], i);
         }
-        own::put8<true, false>(a.normed + row * a.ldn + col.at[c], own::round8<E>(v), 0, 0, col.n[c]);
+        col.store(a.normed + row * a.ldn, c, own::round8<E>(v));
     }
 }
 
@@ -169,18 +193,31 @@ __device__ __forceinline__ Rows rows_of(const BwdArgs& a, int64_t slot) {
     return {a.groups * slot / a.slots * a.group, a.groups * (slot + 1) / a.slots * a.group};
 }
 
+template <int C>
+__device__ __forceinline__ void packed(u32x4 (&v)[C]) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) asm volatile("" : "+v"(v[c]));
+}
+
 // SPLIT: a slot's rows have one gate, and its first partial sum is that of d scale
 // p; else that times the gate, and dgate is written here.
-template <typename E, int TPR, int C, bool SPLIT>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) backward_kernel(BwdArgs a) {
-    constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
+template <typename E, int TPR, int C, bool SPLIT, bool WHOLE>
+__global__ void __launch_bounds__(threads_for(TPR)) backward_kernel(BwdArgs a) {
+    constexpr int kRows = rows_at_once(TPR);
     constexpr int W = TPR > 64 ? TPR / 64 : 1;
     __shared__ float red[2][4 * W];
     const int64_t slot = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
     if (slot >= a.slots) return;  // whole waves, and no barrier where TPR is 64
-    const Columns<TPR, C> col(threadIdx.x % TPR, a.N);
+    const Columns<TPR, C, WHOLE> col(threadIdx.x % TPR, a.N);
     const Rows rows = rows_of(a, slot);
-    u32x4 w[C], w2[C], g[C];
+    // what is absent counts as ones, and as zeros among the gradients
+    u32x4 w[C], w2[C], g[C], y[C], z[C], dt[C], dn[C], next[4][C];
+    constexpr uint32_t one = E::kIsF16 ? 0x3C003C00u : 0x3F803F80u;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        w[c] = w2[c] = g[c] = u32x4{one, one, one, one};
+        next[0][c] = next[1][c] = next[2][c] = next[3][c] = u32x4{0u, 0u, 0u, 0u};
+    }
     if (a.w != nullptr) col.load(a.w, w);
     if (a.next_w != nullptr) col.load(a.next_w, w2);
     if (SPLIT && a.gate != nullptr) col.load(a.gate + rows.first / a.group * a.ld_gate, g);
@@ -192,13 +229,33 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) backward_kernel(BwdArgs
             s1[c][i] = s2[c][i] = 0.0f;
             if constexpr (!SPLIT) sw[c][i] = 0.0f;
         }
+    // A row is fetched while the one in front of it is worked on, where the registers are
+    // there (8192 x 8192: 190 -> 185 us).
+    constexpr bool kAhead = C == 1;
+    auto fetch = [&](int64_t row) {
+        col.load(a.y + row * a.ldy, next[0]);
+        col.load(a.total + row * a.ldt, next[1]);
+        if (a.dtotal != nullptr) col.load(a.dtotal + row * a.ld_dt, next[2]);
+        if (a.dnormed != nullptr) col.load(a.dnormed + row * a.ld_dn, next[3]);
+    };
+    if (kAhead && rows.first < rows.end) fetch(rows.first);
     for (int64_t row = rows.first; row < rows.end; ++row) {
-        u32x4 y[C], z[C], dt[C], dn[C];
-        col.load(a.y + row * a.ldy, y);
-        col.load(a.total + row * a.ldt, z);
-        if (a.dtotal != nullptr) col.load(a.dtotal + row * a.ld_dt, dt);
-        if (a.dnormed != nullptr) col.load(a.dnormed + row * a.ld_dn, dn);
-        if (!SPLIT && a.gate != nullptr && row % a.group == 0) col.load(a.gate + row / a.group * a.ld_gate, g);
+        if (!kAhead) fetch(row);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            y[c] = next[0][c];
+            z[c] = next[1][c];
+            dt[c] = next[2][c];
+            dn[c] = next[3][c];
+        }
+        if (kAhead && row + 1 < rows.end) fetch(row + 1);
+        if (!SPLIT && row % a.group == 0) col.load(a.gate + row / a.group * a.ld_gate, g);
+        col.clear(y);
+        col.clear(z);
+        col.clear(dn);
+        col.clear(dt);
+        // packed(): values wait for their next use in 16 bits, not widened
+        packed(w2);
         float sum[3] = {0.0f, 0.0f, 0.0f};  // of y^2, total^2, dq total
 #pragma unroll
         for (int c = 0; c < C; ++c)
@@ -207,13 +264,15 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) backward_kernel(BwdArgs
                 const float yv = own::widen8<E>(y[c], i), zv = own::widen8<E>(z[c], i);
                 sum[0] = __builtin_fmaf(yv, yv, sum[0]);
                 sum[1] = __builtin_fmaf(zv, zv, sum[1]);
-                if (a.dnormed != nullptr) {
-                    float v = own::widen8<E>(dn[c], i);
-                    if (a.next_w != nullptr) v *= own::widen8<E>(w2[c], i);
-                    sum[2] = __builtin_fmaf(v, zv, sum[2]);
-                }
+                sum[2] = __builtin_fmaf(own::widen8<E>(dn[c], i) * own::widen8<E>(w2[c], i), zv, sum[2]);
             }
         row_sums<TPR>(sum, red[0]);
+        packed(y);
+        packed(z);
+        packed(dn);
+        packed(w2);
+        packed(w);
+        packed(g);
         const float r1 = half_up(sum[0], a.N, a.eps), r2 = half_up(sum[1], a.N, a.eps);
         const float mean2 = sum[2] * r2 / (float)a.N;
         float d[C][8], dot[1] = {0.0f};
@@ -221,37 +280,29 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) backward_kernel(BwdArgs
         for (int c = 0; c < C; ++c) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                float v = a.dtotal != nullptr ? own::widen8<E>(dt[c], i) : 0.0f;
-                if (a.dnormed != nullptr) {
-                    const float dnv = own::widen8<E>(dn[c], i), q = own::widen8<E>(z[c], i) * r2;
-                    const float dq = a.next_w != nullptr ? dnv * own::widen8<E>(w2[c], i) : dnv;
-                    v = __builtin_fmaf(r2, __builtin_fmaf(-q, mean2, dq), v);
-                    s2[c][i] = __builtin_fmaf(dnv, q, s2[c][i]);
-                }
-                d[c][i] = v;
+                const float dnv = own::widen8<E>(dn[c], i), q = own::widen8<E>(z[c], i) * r2;
+                const float dq = dnv * own::widen8<E>(w2[c], i);
+                d[c][i] = __builtin_fmaf(r2, __builtin_fmaf(-q, mean2, dq), own::widen8<E>(dt[c], i));
+                s2[c][i] = __builtin_fmaf(dnv, q, s2[c][i]);
             }
-            if (col.n[c] > 0)
-                own::put8<true, false>(a.dresidual + row * a.ld_dr + col.at[c], own::round8<E>(d[c]), 0, 0, col.n[c]);
+            col.store(a.dresidual + row * a.ld_dr, c, own::round8<E>(d[c]));
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float p = own::widen8<E>(y[c], i) * r1;
-                float v = d[c][i] * a.scale;
+                const float p = own::widen8<E>(y[c], i) * r1, v = d[c][i] * a.scale;
                 s1[c][i] = __builtin_fmaf(v, p, s1[c][i]);
-                if (a.gate != nullptr) v *= own::widen8<E>(g[c], i);
-                if (a.w != nullptr) v *= own::widen8<E>(w[c], i);
-                d[c][i] = v;  // dp from here on
-                dot[0] = __builtin_fmaf(v, p, dot[0]);
+                d[c][i] = v * own::widen8<E>(g[c], i) * own::widen8<E>(w[c], i);  // dp from here on
+                dot[0] = __builtin_fmaf(d[c][i], p, dot[0]);
             }
         }
         row_sums<TPR>(dot, red[1]);
+        packed(y);
         const float mean1 = dot[0] / (float)a.N;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            if (col.n[c] == 0) continue;
             float v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = r1 * __builtin_fmaf(-(own::widen8<E>(y[c], i) * r1), mean1, d[c][i]);
-            own::put8<true, false>(a.dy + row * a.ld_dy + col.at[c], own::round8<E>(v), 0, 0, col.n[c]);
+            col.store(a.dy + row * a.ld_dy, c, own::round8<E>(v));
         }
         if constexpr (!SPLIT) {
             if ((row + 1) % a.group == 0) {  // the gate's last row
@@ -260,13 +311,11 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) backward_kernel(BwdArgs
                     float v[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        v[i] = a.w != nullptr ? s1[c][i] * own::widen8<E>(w[c], i) : s1[c][i];
+                        v[i] = s1[c][i] * own::widen8<E>(w[c], i);
                         sw[c][i] = __builtin_fmaf(own::widen8<E>(g[c], i), s1[c][i], sw[c][i]);
                         s1[c][i] = 0.0f;
                     }
-                    if (col.n[c] > 0 && a.dgate != nullptr)
-                        own::put8<true, false>(a.dgate + row / a.group * a.ld_dgate + col.at[c], own::round8<E>(v), 0, 0,
-                                               col.n[c]);
+                    if (a.dgate != nullptr) col.store(a.dgate + row / a.group * a.ld_dgate, c, own::round8<E>(v));
                 }
             }
         }

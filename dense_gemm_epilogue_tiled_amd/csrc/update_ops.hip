@@ -19,27 +19,23 @@ constexpr int64_t kOrthoMax = 65536;  // either side of an update
 // ---- sandwich norm ----------------------------------------------------------------------
 
 // f<TPR, C>() for rows of N columns: threads per row and chunks of 8 columns per thread.
-// A wave holds a row of up to 1024 columns, then a workgroup does.  Forward with few
-// rows the chip is empty either way and more threads per row take fewer steps each.
+// `wide`: one chunk per thread as far as it goes, for the backward pass, which needs the
+// registers, and for few rows, where more threads per row take fewer steps each.
 template <typename F>
-int by_width(int64_t N, bool few, F&& f) {
+int by_width(int64_t N, bool wide, F&& f) {
     using std::integral_constant;
 #define GR_CASE(TPR, C) return f(integral_constant<int, TPR>{}, integral_constant<int, C>{})
     if (N <= 512) GR_CASE(64, 1);
-    if (N <= 1024 && !few) GR_CASE(64, 2);
+    if (N <= 1024) GR_CASE(128, 1);
     if (N <= 2048) GR_CASE(256, 1);
-    if (N <= 4096 && !few) GR_CASE(256, 2);
+    if (N <= 4096 && !wide) GR_CASE(256, 2);
     if (N <= 4096) GR_CASE(512, 1);
-    if (N <= 8192 && !few) GR_CASE(512, 2);
+    if (N <= 8192 && !wide) GR_CASE(512, 2);
     if (N <= 8192) GR_CASE(1024, 1);
     if (N <= 16384) GR_CASE(1024, 2);
     GR_CASE(1024, 4);
 #undef GR_CASE
 }
-
-// Rows that the threads of a workgroup hold at once.
-constexpr int rows_at_once(int tpr) { return tpr < 256 ? 256 / tpr : 1; }
-int64_t rows_at_once_for(int64_t N) { return N <= 1024 ? 4 : 1; }
 
 int check_sandwich(int64_t M, int64_t N, int64_t G, bool gate, float scale, float eps, int fmt) {
     if (!dim_ok(M) || !dim_ok(N) || !dim_ok(G)) return GR_ERR_INVALID_DIM;
@@ -52,20 +48,24 @@ template <typename E>
 int run_sandwich(const gr::sandwich::Args& a, hipStream_t stream) {
     return by_width(a.N, a.M <= kCus, [&](auto tpr, auto c) {
         constexpr int TPR = decltype(tpr)::value, C = decltype(c)::value;
-        return launch(gr::sandwich::forward_kernel<E, TPR, C>, ceil_div(a.M, rows_at_once(TPR)), TPR < 256 ? 256 : TPR,
-                      stream, a);
+        using namespace gr::sandwich;
+        const int64_t grid = ceil_div(a.M, rows_at_once(TPR));
+        const int threads = threads_for(TPR);
+        return a.N % 8 == 0 ? launch(gr::sandwich::forward_kernel<E, TPR, C, true>, grid, threads, stream, a)
+                            : launch(gr::sandwich::forward_kernel<E, TPR, C, false>, grid, threads, stream, a);
     });
 }
 
 // How the rows are dealt out: slots (each with a partial sum of every column), and
-// how many of them share a gate's rows (0: a slot has whole gates).  Two workgroups per
-// CU, four rows or more to a slot where there are that many.
+// how many of them share a gate's rows (0: a slot has whole gates).  As many workgroups as
+// the chip holds of 512 threads (of 1024: half as many), four rows or more to a slot where there are that
+// many.
 struct Deal {
     int64_t slots, split;
 };
 Deal deal(int64_t M, int64_t N, int64_t groups) {
     if (M == 0) return {0, 1};
-    const int64_t rows = M / groups, most = 2 * kCus * rows_at_once_for(N);
+    const int64_t rows = M / groups, most = N <= 512 ? 8 * kCus : N <= 4096 ? 2 * kCus : kCus;
     if (groups > most) return {most, 0};
     int64_t split = most / groups;
     if (split > ceil_div(rows, 4)) split = ceil_div(rows, 4);
@@ -79,12 +79,15 @@ int run_sandwich_backward(const gr::sandwich::BwdArgs& a, hipStream_t stream) {
     using namespace gr::sandwich;
     int st = GR_OK;
     if (a.slots > 0)
-        st = by_width(a.N, false, [&](auto tpr, auto c) {
+        st = by_width(a.N, true, [&](auto tpr, auto c) {
             constexpr int TPR = decltype(tpr)::value, C = decltype(c)::value;
             const int64_t grid = ceil_div(a.slots, rows_at_once(TPR));
-            const int threads = TPR < 256 ? 256 : TPR;
-            return a.split > 0 ? launch(backward_kernel<E, TPR, C, true>, grid, threads, stream, a)
-                               : launch(backward_kernel<E, TPR, C, false>, grid, threads, stream, a);
+            const int threads = threads_for(TPR);
+            if (a.N % 8 == 0)
+                return a.split > 0 ? launch(backward_kernel<E, TPR, C, true, true>, grid, threads, stream, a)
+                                   : launch(backward_kernel<E, TPR, C, false, true>, grid, threads, stream, a);
+            return a.split > 0 ? launch(backward_kernel<E, TPR, C, true, false>, grid, threads, stream, a)
+                               : launch(backward_kernel<E, TPR, C, false, false>, grid, threads, stream, a);
         });
     if (st != GR_OK || a.part == nullptr) return st;
     return launch_grid(reduce_kernel<E>, dim3((uint32_t)ceil_div(a.N, REDUCE_COLS), 2), 256, stream, a);
