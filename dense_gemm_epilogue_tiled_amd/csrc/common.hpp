@@ -66,13 +66,14 @@ struct EpiArgs;
 // depend on the type.  Accumulation is fp32 for both.  kGeneral selects the
 // epilogue: false is the fused ReLU; true (the Epi<> wrapper below) is bias
 // plus a run-time activation.  kOwn: the type brings an epilogue of its own with
-// arguments of its own, and may pair rows of Bt (kPairs) or map workgroups to
-// tiles in its own way (own_epilogue.hpp).
+// arguments of its own, and may pair rows of Bt (kPairs), map workgroups to tiles in its
+// own way or bring a second product (kTwo; own_epilogue.hpp).
 struct ElemF16 {
     static constexpr bool kIsF16 = true;
     static constexpr bool kGeneral = false;
     static constexpr bool kOwn = false;
     static constexpr bool kPairs = false;
+    static constexpr bool kTwo = false;
     using Args = EpiArgs;
     static __device__ __forceinline__ float widen(uint16_t h) {
         return (float)__builtin_bit_cast(_Float16, h);
@@ -94,6 +95,7 @@ struct ElemBF16 {
     static constexpr bool kGeneral = false;
     static constexpr bool kOwn = false;
     static constexpr bool kPairs = false;
+    static constexpr bool kTwo = false;
     using Args = EpiArgs;
     static __device__ __forceinline__ float widen(uint16_t h) {
         return __builtin_bit_cast(float, (uint32_t)h << 16);

@@ -3,6 +3,7 @@
 // of training.
 //
 //   Plain   C = round(acc)
+//   Two     the same for two products at once, and sums over rows
 //   Gated   rows n and n + half of Bt are a pair: C[m][n] = act(g + b) * (u + b'),
 //           with (g, u) the pair's sums in fp32; optionally g and u themselves, rounded,
 //           for a backward pass
@@ -17,7 +18,7 @@
 // order.
 #pragma once
 
-#include "common.hpp"
+#include "norm_kernel.hpp"
 
 namespace gr {
 namespace own {
@@ -150,6 +151,88 @@ struct Plain : Own<Base> {
             const float v[4] = {s[0], s[1], s[2], s[3]};
             put4<Base>(C + (int64_t)m * ldc + n0 + c, v, n0 + c, n_own, N);
         }
+    }
+};
+
+// ---- Two --------------------------------------------------------------------------
+
+// One of two products in a launch, and the workgroups behind them for sums over rows: for
+// small gradients, where a launch costs as much as a product.
+struct Product {
+    const uint16_t *A, *Bt;
+    uint16_t* C;
+    int64_t M, N, K, lda, ldb, ldc;
+    uint32_t n_blocks, blocks;  // blocks (tiles) across the columns, and all of them
+    uint32_t order;             // tile_of_workgroup's
+};
+struct TwoArgs {
+    Product product[2];
+    // sums[r] = the sum of row r of the first product's A, K values, for r < sum_rows
+    uint16_t* sums;
+    int64_t sum_rows;
+};
+
+// The sum of a row with a 16-byte start of `cols` (a multiple of 8) values over a wave, in
+// fp32 and a fixed order.
+template <typename E>
+__device__ __forceinline__ float row_sum(const uint16_t* row, int64_t cols) {
+    float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int64_t c = 8 * (threadIdx.x % 64); c < cols; c += 512) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(row + c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += widen8<E>(v, e);
+    }
+    return mx::wave_sum(((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7])));
+}
+
+template <typename Base>
+struct Two : Own<Base> {
+    static constexpr bool kTwo = true;
+    using Args = TwoArgs;
+
+    // Whether workgroup wg, of WAVES waves, is one for sums: then they are done.
+    template <int WAVES>
+    static __device__ __forceinline__ bool sums(const Args& ep, uint32_t wg) {
+        const uint32_t products = ep.product[0].blocks + ep.product[1].blocks;
+        if (wg < products) return false;
+        const int64_t r = (int64_t)(wg - products) * WAVES + threadIdx.x / 64;
+        if (r < ep.sum_rows) {
+            const float s = row_sum<Base>(ep.product[0].A + r * ep.product[0].lda, ep.product[0].K);
+            if (threadIdx.x % 64 == 0) ep.sums[r] = Base::round(s);
+        }
+        return true;
+    }
+    static __device__ __forceinline__ void select(const Args& ep, uint32_t& wg, uint32_t& n_wg, const uint16_t* __restrict__& A,
+                                                  const uint16_t* __restrict__& B, uint16_t* __restrict__& C, int64_t& M,
+                                                  int64_t& N, int64_t& K, int64_t& lda, int64_t& ldb, int64_t& ldc,
+                                                  uint32_t& n_blocks, uint32_t& order) {
+        const bool second = wg >= ep.product[0].blocks;
+        if (second) wg -= ep.product[0].blocks;
+        const Product p = second ? ep.product[1] : ep.product[0];
+        A = p.A;
+        B = p.Bt;
+        C = p.C;
+        M = p.M;
+        N = p.N;
+        K = p.K;
+        lda = p.lda;
+        ldb = p.ldb;
+        ldc = p.ldc;
+        n_wg = p.blocks;
+        n_blocks = p.n_blocks;
+        order = p.order;
+    }
+
+    template <bool EDGE, typename Acc>
+    static __device__ __forceinline__ void store_tile(Acc& acc, uint8_t* region, uint32_t lane, uint16_t* C, int64_t ldc,
+                                                      int64_t row0, int64_t col0, int64_t row_min, int64_t M, int64_t N,
+                                                      const Args&) {
+        Plain<Base>::template store_tile<EDGE>(acc, region, lane, C, ldc, row0, col0, row_min, M, N, PlainArgs{});
+    }
+    template <int ROWS, int ON, int T, typename S, typename K>
+    static __device__ __forceinline__ void store_block(S sum4, K keep4, uint16_t* C, int64_t ldc, int64_t row0, int64_t M,
+                                                       int64_t N, int64_t n0, int64_t n_own, const Args&) {
+        Plain<Base>::template store_block<ROWS, ON, T>(sum4, keep4, C, ldc, row0, M, N, n0, n_own, PlainArgs{});
     }
 };
 

@@ -125,6 +125,69 @@ int product(Kernel kernel, int64_t B, int64_t M, int64_t N, int64_t K, const uin
     }
 }
 
+// The kernel for two plain products (M x N x K each) in one launch, or kTile256 for none: the
+// stream while the blocks of both fit the chip, else 128 x 128 tiles where each alone would take
+// them.
+struct Shape {
+    int64_t M, N, K;
+};
+Kernel choose_small(const Shape (&products)[2]) {
+    int64_t blocks = 0;
+    bool streams = true, tiles = true;
+    for (const Shape& p : products) {
+        blocks += ceil_div(p.M, kStreamRows) * ceil_div(p.N, kStreamNB);
+        streams = streams && p.N >= kStreamNB;
+        tiles = tiles && choose(1, p.M, p.N, p.K, 1) == kTile128;
+    }
+    if (streams && blocks <= 512) return blocks <= 256 ? kStream8 : kStream4;
+    return tiles ? kTile128 : kTile256;
+}
+
+// Up to two plain products and the sums over the rows of the first one's A, in one launch
+// where they are small: then a launch takes longer than a product.
+template <typename Base>
+struct Small {
+    gr::own::TwoArgs args{};
+    int count = 0;
+
+    void add(int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, const uint16_t* Bt, int64_t ldb, uint16_t* C,
+             int64_t ldc) {
+        args.product[count++] = {A, Bt, C, M, N, K, lda, ldb, ldc, 1, 0, 0};
+    }
+    int run(Kernel kernel, hipStream_t stream) {
+        using E = gr::own::Two<Base>;
+        const int64_t side = kernel == kTile128 ? gr::tile128::BM : kStreamRows;
+        int64_t grid = 0;
+        for (int i = 0; i < count; ++i) {
+            gr::own::Product& p = args.product[i];
+            p.n_blocks = (uint32_t)ceil_div(p.N, side);
+            p.blocks = (uint32_t)ceil_div(p.M, side) * p.n_blocks;
+            p.order = kernel != kTile128 && p.n_blocks % 4 == 0 ? (gr::kNoXcdRemap | 1u) : kGroupM;
+            grid += p.blocks;
+        }
+        const gr::own::TwoArgs a = args;
+        const int64_t none = 0;
+        const uint16_t* const in = nullptr;
+        uint16_t* const out = nullptr;
+        float* const part = nullptr;
+        const uint32_t zero = 0;
+        if (kernel == kTile128) {
+            using namespace gr::tile128;
+            grid += ceil_div(a.sum_rows, THREADS / 64);
+            return launch(gemm_relu_tile128_kernel<true, false, true, E>, grid, THREADS, stream, in, in, out, none, none, none,
+                          none, none, none, zero, zero, zero, 8, part, none, a);
+        }
+        using namespace gr::smallm;
+        const int waves = kernel == kStream8 ? kStreamWOne : kStreamW;
+        grid += ceil_div(a.sum_rows, waves);
+        if (kernel == kStream8)
+            return launch(gemm_relu_smallm_stream_kernel<kStreamNB, kStreamWOne, kStreamR, stream::WHOLE, E, false, 4, true, true>,
+                          grid, 64 * waves, stream, in, in, out, part, none, none, none, none, none, none, none, zero, zero, a);
+        return launch(gemm_relu_smallm_stream_kernel<kStreamNB, kStreamW, kStreamR, stream::WHOLE, E, false, 4, true, true>, grid,
+                      64 * waves, stream, in, in, out, part, none, none, none, none, none, none, none, zero, zero, a);
+    }
+};
+
 // The same for B products of one shape (grid y), and for symmetric ones C = own
 // epilogue of A A^T, A N x K.
 template <typename E>

@@ -294,18 +294,24 @@ __global__ __launch_bounds__(64 * W, 1) void gemm_relu_smallm_stream_kernel(
 
     const uint32_t tid = threadIdx.x, lane = tid & 63u;
     const uint32_t w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    uint32_t wg = blockIdx.x, n_wg = gridDim.x;
+    if constexpr (E::kTwo) {
+        if (E::template sums<W>(ep, wg)) return;
+        E::select(ep, wg, n_wg, A, B, C, M, N, K, lda, ldb, ldc, n_blocks, order);
+        k_per_split = K;
+    }
     uint32_t cb;
     int64_t s;
     if (RBLK && order != (kNoXcdRemap | 1u)) {
         uint32_t rb, nb;
-        tile_of_workgroup(blockIdx.x, gridDim.x, gridDim.x / n_blocks, n_blocks, order, rb, nb);
+        tile_of_workgroup(wg, n_wg, n_wg / n_blocks, n_blocks, order, rb, nb);
         cb = nb;
         s = rb;
     } else {
         // plain row-major order without the general mapping's divisions
         // (they delay the first copies: 1024^3 8.70 -> 8.60 us)
-        cb = blockIdx.x % n_blocks;
-        s = blockIdx.x / n_blocks;
+        cb = wg % n_blocks;
+        s = wg / n_blocks;
     }
     // columns of C per block (half as many where rows of Bt are paired: blocks
     // 0 and 1 of 16 rows from Bt's first half, 2 and 3 the same rows of its second)

@@ -89,11 +89,19 @@ __global__ __launch_bounds__(THREADS, 2) void gemm_relu_tile128_kernel(
     const uint32_t wm = wave >> 1;
     const uint32_t wn = wave & 1u;
 
+    uint32_t first = blockIdx.x, n_wg = gridDim.x;
+    if constexpr (E::kTwo) {
+        if (E::template sums<THREADS / 64>(ep, first)) return;
+        E::select(ep, first, n_wg, A, B, C, M, N, K, lda, ldb, ldc, tiles_n, group_m);
+        tiles_m = n_wg / tiles_n;
+    }
     const uint32_t tiles = tiles_m * tiles_n;
-    const uint32_t wg = SPLIT ? blockIdx.x % tiles : blockIdx.x;
+    const uint32_t wg = SPLIT ? blockIdx.x % tiles : first;
     const int64_t split = SPLIT ? blockIdx.x / tiles : 0;
     uint32_t tm, tn;
-    if constexpr (E::kOwn) {
+    if constexpr (E::kTwo) {
+        tile_of_workgroup(wg, n_wg, tiles_m, tiles_n, group_m, tm, tn);
+    } else if constexpr (E::kOwn) {
         static_assert(BT && !SPLIT, "own epilogues: B transposed, all of K");
         E::tile(ep, tiles_m, tiles_n, group_m, tm, tn);
         E::batch(ep, A, B, C);

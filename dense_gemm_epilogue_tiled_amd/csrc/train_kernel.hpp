@@ -36,16 +36,30 @@ struct Jobs {
     Job job[JOBS];
 };
 
-__global__ void __launch_bounds__(THREADS) relayout_kernel(Jobs jobs) {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[TILE * TILE * 2];
-    uint32_t tile = blockIdx.x;
+// The job of a workgroup, field by field: an array indexed by a variable would go through scratch
+// memory.
+__device__ __forceinline__ Job job_of(const Jobs jobs, uint32_t& tile) {
     Job j = jobs.job[0];
 #pragma unroll
-    for (int i = 1; i < JOBS; ++i)
-        if (tile >= j.tiles) {
-            tile -= j.tiles;
-            j = jobs.job[i];
-        }
+    for (int i = 1; i < JOBS; ++i) {
+        const bool next = tile >= j.tiles;
+        const Job& n = jobs.job[i];
+        tile -= next ? j.tiles : 0;
+        j.src = next ? n.src : j.src;
+        j.dst = next ? n.dst : j.dst;
+        j.rows = next ? n.rows : j.rows;
+        j.cols = next ? n.cols : j.cols;
+        j.lds = next ? n.lds : j.lds;
+        j.ldd = next ? n.ldd : j.ldd;
+        j.pad = next ? n.pad : j.pad;
+        j.tiles_c = next ? n.tiles_c : j.tiles_c;
+        j.transposed = next ? n.transposed : j.transposed;
+        j.tiles = next ? n.tiles : j.tiles;
+    }
+    return j;
+}
+
+__device__ __forceinline__ void relayout(const Job j, uint32_t tile, uint8_t* lds) {
     const int64_t r0 = (int64_t)(tile / j.tiles_c) * TILE, c0 = (int64_t)(tile % j.tiles_c) * TILE;
     u32x4 v[2];
     uint32_t row[2], chunk[2];
@@ -76,6 +90,13 @@ __global__ void __launch_bounds__(THREADS) relayout_kernel(Jobs jobs) {
         if (c0 + c < j.cols && r0 + 8 * oct < j.pad)
             *reinterpret_cast<u32x4*>(j.dst + (c0 + c) * j.ldd + r0 + 8 * oct) = column8(lds, c, oct);
     }
+}
+
+__global__ void __launch_bounds__(THREADS) relayout_kernel(Jobs jobs) {
+    __shared__ __attribute__((aligned(16))) uint8_t lds[TILE * TILE * 2];
+    uint32_t tile = blockIdx.x;
+    const Job j = job_of(jobs, tile);
+    relayout(j, tile, lds);
 }
 
 // ---- the gated activation's backward pass -----------------------------------------------
@@ -125,10 +146,16 @@ struct GatedBwdArgs {
 };
 
 // dg = dh u act'(g), du = dh act(g) of a tile of 64 tokens x 64 columns, written
-// as they are and transposed.
+// as they are and transposed.  The workgroups behind the tiles do `jobs`.
 template <typename E>
-__global__ void __launch_bounds__(THREADS) gated_backward_kernel(GatedBwdArgs a, uint32_t tiles_c) {
+__global__ void __launch_bounds__(THREADS) gated_backward_kernel(GatedBwdArgs a, uint32_t tiles_c, uint32_t tiles, Jobs jobs) {
     __shared__ __attribute__((aligned(16))) uint8_t lds[2][TILE * TILE * 2];
+    if (blockIdx.x >= tiles) {
+        uint32_t tile = blockIdx.x - tiles;
+        const Job j = job_of(jobs, tile);
+        relayout(j, tile, lds[0]);
+        return;
+    }
     const int64_t r0 = (int64_t)(blockIdx.x / tiles_c) * TILE, c0 = (int64_t)(blockIdx.x % tiles_c) * TILE;
     u32x4 dh[2], g[2], u[2];
     int n[2];
@@ -187,20 +214,13 @@ __global__ void __launch_bounds__(THREADS) gated_backward_kernel(GatedBwdArgs a,
 }
 
 // out[r] = the sum of row r of a matrix with 16-byte rows of `cols` (a multiple of 8)
-// values, in fp32 and a fixed order: a bias's gradient from the transposed gradient.  A
-// wave per row.
+// values: a bias's gradient from the transposed gradient.  A wave per row.
 template <typename E>
 __global__ void __launch_bounds__(THREADS) row_sums_kernel(const uint16_t* src, int64_t rows, int64_t cols, int64_t ld,
                                                            uint16_t* out) {
     const int64_t r = (int64_t)blockIdx.x * (THREADS / 64) + threadIdx.x / 64;
     if (r >= rows) return;
-    float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t c = 8 * (threadIdx.x % 64); c < cols; c += 512) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(src + r * ld + c);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] += own::widen8<E>(v, e);
-    }
-    const float s = mx::wave_sum(((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7])));
+    const float s = own::row_sum<E>(src + r * ld, cols);
     if (threadIdx.x % 64 == 0) out[r] = E::round(s);
 }
 

@@ -93,7 +93,9 @@ int run_gated(int64_t M, int64_t I, int64_t H, const uint16_t* X, int64_t ldx, c
 // rounding where they are many; on W transposed, with N padded to whole strips by
 // zeros, where the product of row-major operands would have misaligned rows or a ragged
 // depth (333 x 2080 x 1001: 41 us in place, 13 with the copies) and the copies are not most
-// of the work; else gemm_bias_act's paths.
+// of the work, and where W is so small that its copy beside the other ones costs less than a
+// launch of the product's own; else gemm_bias_act's paths.
+constexpr int64_t kSmallWeight = int64_t(1) << 21;  // elements
 enum InputGrad { kTiles, kTransposed, kPaths };
 
 template <typename Base>
@@ -109,7 +111,8 @@ InputGrad input_grad_kind(int64_t M, int64_t K, int64_t N, const uint16_t* dY, i
     if (whole && M >= BM && N % BKA == 0 && lddy <= gr::tile2::MAX_LDA && ldw <= gr::tile2::MAX_LDB &&
         ceil_div(M, BM) * ceil_div(K, BN) > 128)
         return kTiles;
-    if (M > kStreamRows && N > 0 && padded_depth(N) <= kMaxPitch && !(whole && N % 32 == 0)) return kTransposed;
+    const bool ragged = M > kStreamRows && !(whole && N % 32 == 0);
+    if (N > 0 && padded_depth(N) <= kMaxPitch && (ragged || N <= kSmallWeight / K)) return kTransposed;
     return kPaths;
 }
 
@@ -171,17 +174,40 @@ int input_grad(const InputGradLayout& l, int64_t M, int64_t K, int64_t N, const 
                             Base::kIsF16 ? GR_FMT_F16 : GR_FMT_BF16, l.paths > 0 ? ws : nullptr, l.paths, stream, -1);
 }
 
-// dW = dY^T X from the transposed operands (pitch Mp each).
-template <typename Base>
-int weight_grad(int64_t N, int64_t K, int64_t Mp, const uint16_t* dYt, const uint16_t* Xt, uint16_t* dW, int64_t lddw,
-                hipStream_t stream) {
-    return product<gr::own::Plain<Base>>(choose(1, N, K, Mp, 1), 1, N, K, Mp, dYt, Mp, Xt, Mp, dW, lddw, gr::own::PlainArgs{},
-                                         stream);
-}
-
 template <typename Base>
 int bias_grad(int64_t N, int64_t Mp, const uint16_t* dYt, uint16_t* dB, hipStream_t stream) {
     return launch(gr::train::row_sums_kernel<Base>, ceil_div(N, 4), gr::train::THREADS, stream, dYt, N, Mp, Mp, dB);
+}
+
+// dX, dW (N x K) and dB from what the copies made ready; rest: input_grad's workspace.
+template <typename Base>
+int grad_products(const InputGradLayout& l, int64_t M, int64_t N, int64_t K, int64_t Mp, const uint16_t* dYt, const uint16_t* Xt,
+                  const uint16_t* dY, int64_t lddy, const uint16_t* W, int64_t ldw, uint16_t* dX, int64_t lddx, uint16_t* dW,
+                  int64_t lddw, uint16_t* dB, uint8_t* rest, hipStream_t stream) {
+    const bool weight = dW && N > 0 && K > 0, input = dX && M > 0 && K > 0, bias = dB && N > 0;
+    // by the shapes alone, so that a gradient has the same bits with and without the others
+    const int64_t Np = padded_depth(N);
+    const Kernel both = choose_small({{N, K, Mp}, {M, K, Np}});
+    const Kernel kernel = both != kTile256 ? both : choose(1, N, K, Mp, 1);  // dW's
+    const bool together = both != kTile256 && input && l.kind == kTransposed;
+    int st = GR_OK;
+    if (kernel != kTile256 && (weight || together)) {
+        Small<Base> small;
+        if (weight) small.add(N, K, Mp, dYt, Mp, Xt, Mp, dW, lddw);
+        if (together)
+            small.add(M, K, Np, l.dy > 0 ? reinterpret_cast<const uint16_t*>(rest + l.wt) : dY, Np,
+                      reinterpret_cast<const uint16_t*>(rest), Np, dX, lddx);
+        if (weight && bias) {
+            small.args.sums = dB;
+            small.args.sum_rows = N;
+        }
+        st = small.run(kernel, stream);
+    } else if (weight) {
+        st = product<gr::own::Plain<Base>>(kernel, 1, N, K, Mp, dYt, Mp, Xt, Mp, dW, lddw, gr::own::PlainArgs{}, stream);
+    }
+    if (st == GR_OK && bias && (kernel == kTile256 || !weight)) st = bias_grad<Base>(N, Mp, dYt, dB, stream);
+    if (st == GR_OK && input && !together) st = input_grad<Base>(l, M, K, N, dY, lddy, W, ldw, dX, lddx, rest, stream);
+    return st;
 }
 
 int64_t padded_tokens(int64_t M) { return M > 0 ? round_up(M, gr::train::PAD) : gr::train::PAD; }
@@ -229,12 +255,9 @@ int run_linear_backward(int64_t M, int64_t N, int64_t K, const uint16_t* dY, int
     if (dB || (dW && K > 0)) copies.add(true, dY, M, N, lddy, dyt, Mp);
     if (dW && N > 0) copies.add(true, X, M, K, ldx, xt, Mp);
     if (dX && M > 0 && K > 0) input_grad_copies(l.input, M, K, N, dY, lddy, W, ldw, rest, &copies);
-    int st = copies.run(stream);
-    if (st == GR_OK && dW && N > 0 && K > 0) st = weight_grad<Base>(N, K, Mp, dyt, xt, dW, lddw, stream);
-    if (st == GR_OK && dB && N > 0) st = bias_grad<Base>(N, Mp, dyt, dB, stream);
-    if (st == GR_OK && dX && M > 0 && K > 0)
-        st = input_grad<Base>(l.input, M, K, N, dY, lddy, W, ldw, dX, lddx, rest, stream);
-    return st;
+    const int st = copies.run(stream);
+    if (st != GR_OK) return st;
+    return grad_products<Base>(l.input, M, N, K, Mp, dyt, xt, dY, lddy, W, ldw, dX, lddx, dW, lddw, dB, rest, stream);
 }
 
 int gated_layout(int64_t M, int64_t I, int64_t H, const uint16_t* W, int64_t ldw, const uint16_t* dX, int64_t lddx,
@@ -278,17 +301,16 @@ int run_gated_backward(int64_t M, int64_t I, int64_t H, const uint16_t* dH, int6
     Relayouts copies;
     if (dW && I > 0) copies.add(true, X, M, H, ldx, xt, Mp);
     if (dX && M > 0 && H > 0) input_grad_copies(l.input, M, H, 2 * I, dgu, least(ld), W, ldw, rest, &copies);
-    int st = copies.run(stream);
-    if (st == GR_OK && I > 0) {
+    int st = GR_OK;
+    if (I > 0) {
         const GatedBwdArgs a{dH, GU, dgu, l.dyt > 0 ? dyt : nullptr, M, I, lddh, ldgu, ld, Mp, act};
-        const uint32_t tc = (uint32_t)ceil_div(I, TILE);
-        st = launch(gated_backward_kernel<Base>, Mp / TILE * tc, THREADS, stream, a, tc);
+        const uint32_t tc = (uint32_t)ceil_div(I, TILE), tiles = (uint32_t)(Mp / TILE) * tc;
+        st = launch(gated_backward_kernel<Base>, tiles + copies.tiles, THREADS, stream, a, tc, tiles, copies.jobs);
+    } else {
+        st = copies.run(stream);
     }
-    if (st == GR_OK && dW && I > 0 && H > 0) st = weight_grad<Base>(2 * I, H, Mp, dyt, xt, dW, lddw, stream);
-    if (st == GR_OK && dB && I > 0) st = bias_grad<Base>(2 * I, Mp, dyt, dB, stream);
-    if (st == GR_OK && dX && M > 0 && H > 0)
-        st = input_grad<Base>(l.input, M, H, 2 * I, dgu, least(ld), W, ldw, dX, lddx, rest, stream);
-    return st;
+    if (st != GR_OK) return st;
+    return grad_products<Base>(l.input, M, 2 * I, H, Mp, dyt, xt, dgu, least(ld), W, ldw, dX, lddx, dW, lddw, dB, rest, stream);
 }
 
 }  // namespace
