@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "../../include/gemm_relu.h"
+#include "gemv_kernel.hpp"
 #include "own_products.hpp"
 #include "tile3_kernel.hpp"
 #include "train_kernel.hpp"
@@ -37,29 +38,30 @@ struct Relayouts {
 // ---- the gated linear layer -----------------------------------------------------------
 
 constexpr int kSmallMRows = 16;
+constexpr int kGemvRows = 4;
 
-// K that is not a whole number of 32-deep steps (0 included): x and the weight are
-// copied into the workspace with K padded by zeros.
+// K that is not a whole number of 32-deep steps (0 included), with more tokens than the
+// kernel for few takes: x and the weight are copied into the workspace with K padded by zeros.
 bool gated_packs(int64_t H) { return H % 32 != 0 || H == 0; }
 int64_t gated_pitch(int64_t H) { return H > 0 ? round_up(H, 64) : 64; }
 
 int64_t gated_need(int64_t M, int64_t I, int64_t H) {
-    if (M == 0 || I == 0 || !gated_packs(H)) return 0;
+    if (M <= kGemvRows || I == 0 || !gated_packs(H)) return 0;
     return aligned(M * gated_pitch(H) * 2) + aligned(2 * I * gated_pitch(H) * 2);
-}
-
-template <typename E, int WAVES, int ROWS, int RING>
-int small_m(int64_t M, int64_t I, int64_t K, const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, uint16_t* C,
-            int64_t ldc, const gr::own::GatedArgs& ep, hipStream_t stream) {
-    const gr::own::GatedArgs args = ep;
-    return launch(gr::smallm::gemm_relu_smallm_bt_stream_kernel<true, E, WAVES, ROWS, RING>, ceil_div(I, 8 * WAVES),
-                  64 * WAVES, stream, X, W, C, M, I, K, ldx, ldw, ldc, args);
 }
 
 template <typename Base>
 int run_gated(int64_t M, int64_t I, int64_t H, const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
               const gr::own::GatedArgs& ep, uint16_t* C, int64_t ldc, uint8_t* ws, hipStream_t stream) {
     using E = gr::own::Gated<Base>;
+    if (M <= kGemvRows) {
+        using namespace gr::gemv;
+        const Args a{X, W, C, M, I, H, ldx, ldw, ldc, ep};
+        const int64_t grid = ceil_div(I, WAVES * COLS);
+        if (M == 1) return launch(gated_gemv_kernel<Base, 1>, grid, THREADS, stream, a);
+        if (M == 2) return launch(gated_gemv_kernel<Base, 2>, grid, THREADS, stream, a);
+        return launch(gated_gemv_kernel<Base, 4>, grid, THREADS, stream, a);
+    }
     int64_t K = H;
     if (gated_packs(H)) {
         K = gated_pitch(H);
@@ -75,14 +77,12 @@ int run_gated(int64_t M, int64_t I, int64_t H, const uint16_t* X, int64_t ldx, c
         ldx = ldw = K;
     }
     if (M <= kSmallMRows && K % gr::smallm::BTS_KC == 0) {
-        // Two waves to a workgroup, so that the last round of workgroups is a small part of
-        // all (2 x 11008 x 4096: 34.0 us, 38.9 with four waves), and four rows of x at most
-        // in the ring where there are no more; one wave with a longer ring where eight
-        // columns each do not fill the chip (1 x 4096 x 2048: 7.8 us against 10.3).
-        const int64_t waves = ceil_div(I, 8);
-        if (M <= 4 && waves <= 512) return small_m<E, 1, 4, 4>(M, I, K, X, ldx, W, ldw, C, ldc, ep, stream);
-        if (M <= 4) return small_m<E, 2, 4, 2>(M, I, K, X, ldx, W, ldw, C, ldc, ep, stream);
-        return small_m<E, 2, 16, 2>(M, I, K, X, ldx, W, ldw, C, ldc, ep, stream);
+        // two waves to a workgroup, so that the last round of workgroups is a small part of all
+        // (2 x 11008 x 4096: 34.0 us, 38.9 with four)
+        constexpr int W2 = 2;
+        const gr::own::GatedArgs args = ep;
+        return launch(gr::smallm::gemm_relu_smallm_bt_stream_kernel<true, E, W2, 16>, ceil_div(I, 8 * W2), 64 * W2, stream, X, W,
+                      C, M, I, K, ldx, ldw, ldc, args);
     }
     return product<E>(choose(1, M, I, K, 2), 1, M, I, K, X, ldx, W, ldw, C, ldc, ep, stream);
 }
