@@ -2,6 +2,8 @@
 // kernel and its launch.
 #pragma once
 
+#include <initializer_list>
+
 #include "host.hpp"
 #include "own_epilogue.hpp"
 #include "smallm_kernel.hpp"
@@ -18,7 +20,13 @@ constexpr int64_t kMaxPitch = gr::tile2::MAX_LDA;  // 32-bit copy offsets over 2
 
 bool known_fmt(int fmt) { return fmt == GR_FMT_F16 || fmt == GR_FMT_BF16; }
 bool known_act(int act) { return act >= 0 && act < gr::kActCount; }
-bool dim_ok(int64_t v) { return v >= 0 && v <= kMaxDim; }
+int check_dims(std::initializer_list<int64_t> dims) {
+    for (int64_t v : dims)
+        if (v < 0) return GR_ERR_INVALID_DIM;
+    for (int64_t v : dims)
+        if (v > kMaxDim) return GR_ERR_TOO_LARGE;
+    return GR_OK;
+}
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 int64_t aligned(int64_t bytes) { return round_up(bytes, kWorkspaceAlign); }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

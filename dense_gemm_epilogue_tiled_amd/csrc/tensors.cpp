@@ -495,8 +495,8 @@ PyObject* gated_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const uint16_t* bias = vector_of<uint16_t>(a[2], x.t, 2 * I, x.t.scalar_type(), "b13");
         const int act = (int)int_of(a[3]);
         const bool keep = int_of(a[4]) != 0;
-        on_gpu(x.t, "x");
         const Wanted c(a[5], true, x.t, x.rows, I, "out"), gu(a[6], keep, x.t, x.rows, 2 * I, "gu_out");
+        on_gpu(x.t, "x");
         int64_t need = 0;
         int st = gated_linear_workspace_size(x.rows, I, x.cols, &need);
         if (st != GR_OK) return failed(st);
@@ -518,8 +518,8 @@ PyObject* linear_backward_(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const bool bias = int_of(a[3]) != 0, want_x = int_of(a[4]) != 0, want_w = int_of(a[5]) != 0;
         if (want_w && a[1] == Py_None) bad_value("the weight's gradient needs x");
         const Maybe x(a[1], dy.t, M, K, "x");
-        on_gpu(dy.t, "dy");
         const Wanted dx(a[6], want_x, dy.t, M, K, "dx_out"), dw(a[7], want_w, dy.t, N, K, "dw_out");
+        on_gpu(dy.t, "dy");
         const Tensor db = vector_like(bias, dy.t, N);
         int64_t need = 0;
         int st = linear_backward_workspace_size(M, N, K, dy.data, dy.ld, x.data, x.ld, w.data, w.ld, dx.data, dx.ld, dw.data,
@@ -546,8 +546,8 @@ PyObject* gated_linear_backward_(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const bool bias = int_of(a[5]) != 0, want_x = int_of(a[6]) != 0, want_w = int_of(a[7]) != 0;
         if (want_w && a[1] == Py_None) bad_value("the weight's gradient needs x");
         const Maybe x(a[1], dh.t, M, H, "x");
-        on_gpu(dh.t, "dh");
         const Wanted dx(a[8], want_x, dh.t, M, H, "dx_out"), dw(a[9], want_w, dh.t, 2 * I, H, "dw_out");
+        on_gpu(dh.t, "dh");
         const Tensor db = vector_like(bias, dh.t, 2 * I);
         int64_t need = 0;
         int st = gated_linear_backward_workspace_size(M, I, H, w.data, w.ld, dx.data, dx.ld, dw.data, data_or_null(db), &need);
@@ -598,8 +598,8 @@ PyObject* sandwich_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const double scale = double_of(a[5]), eps = double_of(a[6]);
         const bool norm = int_of(a[7]) != 0;
         if (!norm && next) bad_value("next_weight is given for a norm that is not asked for");
-        on_gpu(y.t, "y");
         const Wanted total(a[8], true, y.t, M, N, "total_out"), normed(a[9], norm, y.t, M, N, "normed_out");
+        on_gpu(y.t, "y");
         const int st = sandwich_norm_fwd(M, N, y.data, y.ld, data_of<uint16_t>(res), ldr, w, next, gate.data, gate.count, gate.ld,
                                          (float)scale, (float)eps, total.data, total.ld, normed.data, normed.ld, y.fmt,
                                          stream_of(a[10]));
@@ -674,7 +674,6 @@ PyObject* orthogonalize(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t steps = int_of(a[1]);
         const float k[3] = {(float)double_of(a[2]), (float)double_of(a[3]), (float)double_of(a[4])};
         const double scale = double_of(a[5]), eps = double_of(a[6]);
-        on_gpu(g, "update");
         Tensor out;
         if (const Tensor* given = maybe_tensor(a[7], "out")) {
             check_kind(*given, g.sizes(), at::kBFloat16, "out");
@@ -684,6 +683,7 @@ PyObject* orthogonalize(PyObject*, PyObject* const* a, Py_ssize_t n) {
             out = empty_like(g, g.sizes(), at::kBFloat16);
         }
         const Batch to(out, "out");
+        on_gpu(g, "update");
         int64_t need = 0;
         int st = orthogonalize_workspace_size(in.count, in.rows, in.cols, &need);
         if (st != GR_OK) return failed(st);

@@ -233,7 +233,8 @@ int linear_layout(int64_t M, int64_t N, int64_t K, const uint16_t* dY, int64_t l
 int validate_linear_backward(int64_t M, int64_t N, int64_t K, const uint16_t* dY, int64_t lddy, const uint16_t* X, int64_t ldx,
                              const uint16_t* W, int64_t ldw, const uint16_t* dX, int64_t lddx, const uint16_t* dW,
                              int64_t lddw, const uint16_t* dB) {
-    if (!dim_ok(M) || !dim_ok(N) || !dim_ok(K)) return GR_ERR_INVALID_DIM;
+    const int dims = check_dims({M, N, K});
+    if (dims != GR_OK) return dims;
     if (lddy < least(N)) return GR_ERR_INVALID_LD;
     if (dX && (ldw < least(K) || lddx < least(K))) return GR_ERR_INVALID_LD;
     if (dW && (ldx < least(K) || lddw < least(K))) return GR_ERR_INVALID_LD;
@@ -277,7 +278,8 @@ int gated_layout(int64_t M, int64_t I, int64_t H, const uint16_t* W, int64_t ldw
 int validate_gated_backward(int64_t M, int64_t I, int64_t H, const uint16_t* dH, int64_t lddh, const uint16_t* X,
                             int64_t ldx, const uint16_t* W, int64_t ldw, const uint16_t* GU, int64_t ldgu,
                             const uint16_t* dX, int64_t lddx, const uint16_t* dW, int64_t lddw, const uint16_t* dB) {
-    if (!dim_ok(M) || !dim_ok(I) || !dim_ok(2 * I) || !dim_ok(H)) return GR_ERR_INVALID_DIM;
+    const int dims = check_dims({M, I, 2 * I, H});
+    if (dims != GR_OK) return dims;
     if (lddh < least(I) || ldgu < least(2 * I)) return GR_ERR_INVALID_LD;
     if (dX && (ldw < least(H) || lddx < least(H))) return GR_ERR_INVALID_LD;
     if (dW && (ldx < least(H) || lddw < least(H))) return GR_ERR_INVALID_LD;
@@ -319,7 +321,8 @@ extern "C" {
 
 int gated_linear_workspace_size(int64_t M, int64_t I, int64_t H, int64_t* bytes) {
     if (!bytes) return GR_ERR_INVALID_ARG;
-    if (!dim_ok(M) || !dim_ok(I) || !dim_ok(2 * I) || !dim_ok(H)) return GR_ERR_INVALID_DIM;
+    const int dims = check_dims({M, I, 2 * I, H});
+    if (dims != GR_OK) return dims;
     *bytes = gated_need(M, I, H);
     return GR_OK;
 }
@@ -327,7 +330,8 @@ int gated_linear_workspace_size(int64_t M, int64_t I, int64_t H, int64_t* bytes)
 int gated_linear_bt(int64_t M, int64_t I, int64_t H, const uint16_t* X, int64_t ldx, const uint16_t* W13, int64_t ldw,
                     const uint16_t* b13, int act, uint16_t* C, int64_t ldc, uint16_t* GU, int64_t ldgu, int fmt,
                     void* workspace, int64_t workspace_bytes, void* stream) {
-    if (!dim_ok(M) || !dim_ok(I) || !dim_ok(2 * I) || !dim_ok(H)) return GR_ERR_INVALID_DIM;
+    const int dims = check_dims({M, I, 2 * I, H});
+    if (dims != GR_OK) return dims;
     if (ldx < least(H) || ldw < least(H) || ldc < least(I) || (GU && ldgu < least(2 * I))) return GR_ERR_INVALID_LD;
     if (!known_act(act) || !known_fmt(fmt)) return GR_ERR_INVALID_ARG;
     if (M == 0 || I == 0) return GR_OK;
@@ -390,7 +394,8 @@ int gated_linear_backward_workspace_size(int64_t M, int64_t I, int64_t H, const 
                                          const uint16_t* dX, int64_t lddx, const uint16_t* dW13, const uint16_t* dB13,
                                          int64_t* bytes) {
     if (!bytes) return GR_ERR_INVALID_ARG;
-    if (!dim_ok(M) || !dim_ok(I) || !dim_ok(2 * I) || !dim_ok(H)) return GR_ERR_INVALID_DIM;
+    const int dims = check_dims({M, I, 2 * I, H});
+    if (dims != GR_OK) return dims;
     if (dX && (ldw < least(H) || lddx < least(H))) return GR_ERR_INVALID_LD;
     if (M > 0 && I > 0 && H > 0 && dX && !W13) return GR_ERR_NULL_PTR;
     GradLayout l;

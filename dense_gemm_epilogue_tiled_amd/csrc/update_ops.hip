@@ -38,7 +38,8 @@ int by_width(int64_t N, bool wide, F&& f) {
 }
 
 int check_sandwich(int64_t M, int64_t N, int64_t G, bool gate, float scale, float eps, int fmt) {
-    if (!dim_ok(M) || !dim_ok(N) || !dim_ok(G)) return GR_ERR_INVALID_DIM;
+    const int dims = check_dims({M, N, G});
+    if (dims != GR_OK) return dims;
     if (gate ? G < 1 || M % G != 0 : G != 0) return GR_ERR_INVALID_DIM;
     if (!known_fmt(fmt) || !std::isfinite(scale) || !std::isfinite(eps) || eps < 0.0f) return GR_ERR_INVALID_ARG;
     return N > gr::sandwich::MAX_N ? GR_ERR_TOO_LARGE : GR_OK;
@@ -201,7 +202,8 @@ int sandwich_norm_fwd(int64_t M, int64_t N, const uint16_t* Y, int64_t ldy, cons
 
 int sandwich_norm_bwd_workspace_size(int64_t M, int64_t N, int64_t G, int64_t* bytes) {
     if (!bytes) return GR_ERR_INVALID_ARG;
-    if (!dim_ok(M) || !dim_ok(N) || !dim_ok(G) || (G > 0 && M % G != 0)) return GR_ERR_INVALID_DIM;
+    const int st = check_sandwich(M, N, G, G > 0, 1.0f, 0.0f, GR_FMT_BF16);
+    if (st != GR_OK) return st;
     *bytes = sandwich_need(M, N, G);
     return GR_OK;
 }
@@ -244,7 +246,8 @@ int sandwich_norm_bwd(int64_t M, int64_t N, const uint16_t* dT, int64_t ld_dt, c
 
 int orthogonalize_workspace_size(int64_t B, int64_t rows, int64_t cols, int64_t* bytes) {
     if (!bytes) return GR_ERR_INVALID_ARG;
-    if (!dim_ok(B) || !dim_ok(rows) || !dim_ok(cols)) return GR_ERR_INVALID_DIM;
+    const int dims = check_dims({B, rows, cols});
+    if (dims != GR_OK) return dims;
     if (B > 65535 || rows > kOrthoMax || cols > kOrthoMax) return GR_ERR_TOO_LARGE;
     *bytes = B > 0 && rows > 0 && cols > 0 ? ortho_layout(B, rows, cols).total() : 0;
     return GR_OK;
@@ -253,7 +256,8 @@ int orthogonalize_workspace_size(int64_t B, int64_t rows, int64_t cols, int64_t*
 int orthogonalize_update(int64_t B, int64_t rows, int64_t cols, const void* G, int64_t ldg, int64_t batch_g, int g_fmt,
                          const float* coefficients, int steps, float scale, float eps, uint16_t* out, int64_t ldo,
                          int64_t batch_o, void* workspace, int64_t workspace_bytes, void* stream) {
-    if (!dim_ok(B) || !dim_ok(rows) || !dim_ok(cols)) return GR_ERR_INVALID_DIM;
+    const int dims = check_dims({B, rows, cols});
+    if (dims != GR_OK) return dims;
     if (B > 65535 || rows > kOrthoMax || cols > kOrthoMax) return GR_ERR_TOO_LARGE;
     if (ldg < least(cols) || ldo < least(cols)) return GR_ERR_INVALID_LD;
     if ((!known_fmt(g_fmt) && g_fmt != GR_FMT_F32) || !coefficients || steps < 1 || steps > 64 || !std::isfinite(scale) ||

@@ -1013,7 +1013,7 @@ int gated_linear_bt(int64_t M, int64_t I, int64_t H,
  * in fp32, each rounded once to fmt.  dX, dW, dB: NULL for one that is not wanted (W
  * is read for dX only, X for dW only).  With M = 0, dW and dB are zeros.  The sums over the
  * tokens run in a fixed order.  The size depends on which gradients are asked for and on the
- * addresses' alignment: give the pointers of the call.  M above 2^22 - 64 is
+ * addresses' alignment: give the pointers of the call.  M above 2^22 is
  * GR_ERR_TOO_LARGE.
  */
 int linear_backward_workspace_size(int64_t M, int64_t N, int64_t K,

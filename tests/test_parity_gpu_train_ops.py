@@ -520,3 +520,48 @@ def test_repeated_calls_give_the_same_bits():
     first = [t.clone() for t in training_step(*i)]
     for _ in range(4):
         assert all(torch.equal(a, b) for a, b in zip(training_step(*i), first))
+
+
+# ---- the block that is trained --------------------------------------------------------------------
+
+def test_trained_block_gradients():
+    """feed_forward's forward and backward passes against the fp64 form of the whole block: what is rounded in between
+    moves a gradient by a few roundings of 8 bits, in the 2-norm."""
+    from dense_gemm_epilogue_tiled_amd import feed_forward as ff
+    M, H, I = 96, 128, 200
+    x, res = make((M, H), "bf16", 900), make((M, H), "bf16", 901, 2.0)
+    weights = {"w13": make((2 * I, H), "bf16", 902, H ** -0.5), "w2": make((H, I), "bf16", 903, I ** -0.5),
+               "norm": (make((H,), torch.float64, 904, 0.2) + 1).bfloat16(), "next_norm": (make((H,), torch.float64, 905, 0.2) + 1).bfloat16(),
+               "gate": make((3, H), "bf16", 906)}
+    dt, dn = make((M, H), "bf16", 907), make((M, H), "bf16", 908)
+    on = {n: w.cuda() for n, w in weights.items()}
+    (total, normed), kept = ff.train_forward(x.cuda(), res.cuda(), **on, scale=0.5)
+    dx, dres, grads = ff.train_backward(dt.cuda(), dn.cuda(), kept, **on, scale=0.5)
+    leaves = {"x": x, "res": res, **weights}
+    leaves = {n: t.double().requires_grad_() for n, t in leaves.items()}
+    g, u = (leaves["x"] @ leaves["w13"].T).chunk(2, -1)
+    y = (train_ref.act(g, "silu") * u) @ leaves["w2"].T
+    ref_total, _, _ = train_ref.sandwich(y, leaves["res"], leaves["norm"], None, leaves["gate"], 0.5, 1e-6)
+    ref_normed = train_ref.next_norm(ref_total, leaves["next_norm"], 1e-6)
+    ref = torch.autograd.grad((ref_total * dt.double()).sum() + (ref_normed * dn.double()).sum(), list(leaves.values()))
+    got = [dx, dres, *grads.values()]
+    step = 2.0 ** -8
+    for name, a, b in [("total", total, ref_total), ("normed", normed, ref_normed), *zip(leaves, got, ref)]:
+        # gu, h, y, total, dy, dh, dgu and the result: 8 roundings of half a step at most each, as if all fell together
+        assert (a.double().cpu() - b.detach()).norm() <= 8 * step * b.detach().norm(), name
+
+
+def test_training_demo_runs():
+    from dense_gemm_epilogue_tiled_amd import feed_forward as ff
+    weights, grads = ff._train_demo(40, 96, 130, 3)
+    assert all(bool(t.isfinite().all()) for t in [*weights.values(), *grads.values()])
+
+
+def test_update_matrix_moves_along_the_orthogonalised_momentum():
+    from dense_gemm_epilogue_tiled_amd import feed_forward as ff
+    w, grad, m = make((130, 70), "bf16", 950).cuda(), make((130, 70), "bf16", 951).cuda(), make((130, 70), torch.float32, 952).cuda()
+    before, mom = w.clone(), m * 0.9 + grad
+    ff.update_matrix(w, grad, m, 0.5, 0.9)
+    assert torch.equal(m, mom)
+    want = before.add(gr.orthogonalize(mom * 0.9 + grad, scale=(130 / 70) ** 0.5), alpha=-0.5)
+    assert torch.equal(w, want)
