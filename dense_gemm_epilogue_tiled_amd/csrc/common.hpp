@@ -61,6 +61,14 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 struct EpiArgs;
 
+// What the row-blocked stream fetches for an epilogue before its operands: nothing, unless a
+// type with an epilogue of its own says otherwise.
+template <int N>
+struct NothingHeld {
+    template <typename A>
+    __device__ __forceinline__ void fetch(const A&, int, int, int64_t, int64_t, int64_t, int64_t) {}
+};
+
 // Element types of A, B and C.  Operands travel as 16-bit patterns (f16x8
 // registers); only the matrix-core instruction and the output rounding
 // depend on the type.  Accumulation is fp32 for both.  kGeneral selects the
@@ -75,6 +83,8 @@ struct ElemF16 {
     static constexpr bool kPairs = false;
     static constexpr bool kTwo = false;
     using Args = EpiArgs;
+    template <int N>
+    using Held = NothingHeld<N>;
     static __device__ __forceinline__ float widen(uint16_t h) {
         return (float)__builtin_bit_cast(_Float16, h);
     }
@@ -97,6 +107,8 @@ struct ElemBF16 {
     static constexpr bool kPairs = false;
     static constexpr bool kTwo = false;
     using Args = EpiArgs;
+    template <int N>
+    using Held = NothingHeld<N>;
     static __device__ __forceinline__ float widen(uint16_t h) {
         return __builtin_bit_cast(float, (uint32_t)h << 16);
     }

@@ -141,8 +141,8 @@ struct Plain : Own<Base> {
         });
     }
 
-    template <int ROWS, int ON, int T, typename S, typename K>
-    static __device__ __forceinline__ void store_block(S sum4, K, uint16_t* C, int64_t ldc, int64_t, int64_t M, int64_t N,
+    template <int ROWS, int ON, int T, typename S, typename K, typename H>
+    static __device__ __forceinline__ void store_block(S sum4, K, const H&, uint16_t* C, int64_t ldc, int64_t, int64_t M, int64_t N,
                                                        int64_t n0, int64_t n_own, const Args&) {
         for (uint32_t o = threadIdx.x; o < (uint32_t)(ROWS * ON / 4); o += T) {
             const uint32_t m = o / (ON / 4), c = 4 * (o % (ON / 4));
@@ -229,10 +229,10 @@ struct Two : Own<Base> {
                                                       const Args&) {
         Plain<Base>::template store_tile<EDGE>(acc, region, lane, C, ldc, row0, col0, row_min, M, N, PlainArgs{});
     }
-    template <int ROWS, int ON, int T, typename S, typename K>
-    static __device__ __forceinline__ void store_block(S sum4, K keep4, uint16_t* C, int64_t ldc, int64_t row0, int64_t M,
+    template <int ROWS, int ON, int T, typename S, typename K, typename H>
+    static __device__ __forceinline__ void store_block(S sum4, K keep4, const H& held, uint16_t* C, int64_t ldc, int64_t row0, int64_t M,
                                                        int64_t N, int64_t n0, int64_t n_own, const Args&) {
-        Plain<Base>::template store_block<ROWS, ON, T>(sum4, keep4, C, ldc, row0, M, N, n0, n_own, PlainArgs{});
+        Plain<Base>::template store_block<ROWS, ON, T>(sum4, keep4, held, C, ldc, row0, M, N, n0, n_own, PlainArgs{});
     }
 };
 
@@ -316,8 +316,8 @@ struct Gated : Own<Base> {
         }
     }
 
-    template <int ROWS, int ON, int T, typename S, typename K>
-    static __device__ __forceinline__ void store_block(S sum4, K, uint16_t* C, int64_t ldc, int64_t row0, int64_t M,
+    template <int ROWS, int ON, int T, typename S, typename K, typename H>
+    static __device__ __forceinline__ void store_block(S sum4, K, const H&, uint16_t* C, int64_t ldc, int64_t row0, int64_t M,
                                                        int64_t N, int64_t n0, int64_t n_own, const Args& ep) {
         // C is at the block's first row already, what is kept is not
         Args at = ep;
@@ -357,6 +357,23 @@ constexpr int64_t TILE_COLS = 64 * epi::AccTile<Acc>::FN;
 template <typename In, typename Out, bool TRI>
 struct Poly : Own<In> {
     using Args = PolyArgs;
+
+    // D of a thread's groups of four columns: its latency passes beside the operands'.
+    template <int N>
+    struct Held {
+        u32x2 d[N];
+        __device__ __forceinline__ void fetch(const Args& ep, int on, int threads, int64_t row0, int64_t M, int64_t, int64_t n0) {
+            const uint16_t* const src = ep.d != nullptr ? ep.d + blockIdx.y * ep.batch_d + row0 * ep.ldd + n0 : nullptr;
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const uint32_t o = threadIdx.x + threads * k;
+                const uint32_t m = o / (on / 4), c = 4 * (o % (on / 4));
+                typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+                d[k] = u32x2{0u, 0u};
+                if (src != nullptr && (int64_t)m < M) d[k] = *reinterpret_cast<const u32x2_any*>(src + (int64_t)m * ep.ldd + c);
+            }
+        }
+    };
 
     static __device__ __forceinline__ void tile(const Args&, uint32_t tiles_m, uint32_t tiles_n, uint32_t group_m,
                                                 uint32_t& tm, uint32_t& tn) {
@@ -445,21 +462,21 @@ struct Poly : Own<In> {
         }
     }
 
-    template <int ROWS, int ON, int T, typename S, typename K>
-    static __device__ __forceinline__ void store_block(S sum4, K keep4, uint16_t* C, int64_t ldc, int64_t row0, int64_t M,
+    template <int ROWS, int ON, int T, typename S, typename K, typename H>
+    static __device__ __forceinline__ void store_block(S sum4, K keep4, const H& held, uint16_t* C, int64_t ldc, int64_t row0, int64_t M,
                                                        int64_t N, int64_t n0, int64_t n_own, const Args& ep) {
-        const uint16_t* const d = ep.d != nullptr ? ep.d + blockIdx.y * ep.batch_d + row0 * ep.ldd : nullptr;
         uint16_t* const ct = ep.ct != nullptr ? ep.ct + blockIdx.y * ep.batch_ct + row0 : nullptr;
-        for (uint32_t o = threadIdx.x; o < (uint32_t)(ROWS * ON / 4); o += T) {
+#pragma unroll
+        for (int k = 0; k < ROWS * ON / 4 / T; ++k) {
+            const uint32_t o = threadIdx.x + T * k;
             const uint32_t m = o / (ON / 4), c = 4 * (o % (ON / 4));
             if ((int64_t)m >= M) continue;
             const f32x4 s = sum4(m, c);
             float v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] = __builtin_fmaf(s[e], ep.alpha, row0 + m == n0 + c + e ? ep.diag : 0.0f);
-                if (d != nullptr) v[e] = __builtin_fmaf(ep.beta, In::widen(d[(int64_t)m * ep.ldd + n0 + c + e]), v[e]);
-            }
+            for (int e = 0; e < 4; ++e)
+                v[e] = __builtin_fmaf(ep.beta, In::widen((uint16_t)(held.d[k][e / 2] >> (16 * (e % 2)))),
+                                      __builtin_fmaf(s[e], ep.alpha, row0 + m == n0 + c + e ? ep.diag : 0.0f));
             put4<Out>(C + (int64_t)m * ldc + n0 + c, v, n0 + c, n_own, N);
             if (ct != nullptr) *keep4(m, c) = f32x4{v[0], v[1], v[2], v[3]};
         }

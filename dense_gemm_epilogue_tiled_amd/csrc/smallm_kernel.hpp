@@ -401,6 +401,10 @@ __global__ __launch_bounds__(64 * W, 1) void gemm_relu_smallm_stream_kernel(
         }
     };
 
+    // what an epilogue of one's own reads, on its way before the operands
+    typename E::template Held<E::kOwn ? ROWS * ON / 4 / T : 1> held;
+    if constexpr (E::kOwn) held.fetch(ep, ON, T, row0, M, N, n0);
+
     // R - 1 slots ahead: slot q + R - 1 goes out (into the entry slot q - 1
     // used, whose reads its MFMAs consumed) before slot q is waited for.
     const int64_t ahead = nw < R - 1 ? nw : R - 1;
@@ -472,7 +476,7 @@ __global__ __launch_bounds__(64 * W, 1) void gemm_relu_smallm_stream_kernel(
             return v;
         };
         auto keep4 = [&](uint32_t m, uint32_t c) { return reinterpret_cast<f32x4*>(red + red_at(m, c)); };
-        E::template store_block<ROWS, ON, T>(sum4, keep4, C, ldc, row0, M, N, n0, n_own, ep);
+        E::template store_block<ROWS, ON, T>(sum4, keep4, held, C, ldc, row0, M, N, n0, n_own, ep);
     } else {
         for (uint32_t o = tid; o < (uint32_t)(ROWS * NB); o += T) {
             const uint32_t m = o / NB, nl = o % NB;
