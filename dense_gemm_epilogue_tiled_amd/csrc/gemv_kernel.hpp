@@ -5,9 +5,8 @@
 // Bound by the weight's way from memory.  With so few tokens a matrix instruction's rows stay
 // empty and the multiply-adds of ordinary lanes are few (a sixth of their rate at four
 // tokens), so that nothing asks for the weight in pieces of 16 rows: 1 x 4096 x 14336
-// (235 MB of weights) 43.5 us with the matrix instructions' stream,
-// 37.1 here (6.3 TB/s).  Any K and any
-// address: a ragged end is loaded element by element.
+// (235 MB of weights) 43.5 us with the matrix instructions' stream, 37.2 here (6.3 TB/s; a
+// plain read reaches 6.5).  Any K and any address: a ragged end is loaded element by element.
 #pragma once
 
 #include "norm_kernel.hpp"
@@ -28,12 +27,9 @@ struct Args {
 
 // MT: tokens, of which the last stands for missing ones.
 template <typename E, int MT>
-__global__ void __launch_bounds__(THREADS) gated_gemv_kernel(Args a) {
+__device__ __forceinline__ void columns(const Args& a, int64_t n0, int lane) {
     constexpr int ROWS = 2 * COLS;
     constexpr int UNROLL = MT == 4 ? 2 : 4;  // pieces of 512 values of each row in flight
-    const int lane = threadIdx.x % 64;
-    const int64_t n0 = ((int64_t)blockIdx.x * WAVES + threadIdx.x / 64) * COLS;
-    if (n0 >= a.I) return;
     const uint16_t* row[ROWS];  // gate rows, then up rows
 #pragma unroll
     for (int j = 0; j < COLS; ++j) {
@@ -104,6 +100,13 @@ __global__ void __launch_bounds__(THREADS) gated_gemv_kernel(Args a) {
         a.ep.kept[m * a.ep.ld_kept + n] = (uint16_t)own::round2<E>(g, g);
         a.ep.kept[m * a.ep.ld_kept + a.I + n] = (uint16_t)own::round2<E>(u, u);
     }
+}
+
+template <typename E, int MT>
+__global__ void __launch_bounds__(THREADS) gated_gemv_kernel(Args a) {
+    const int64_t step = (int64_t)gridDim.x * WAVES * COLS;
+    for (int64_t n0 = ((int64_t)blockIdx.x * WAVES + threadIdx.x / 64) * COLS; n0 < a.I; n0 += step)
+        columns<E, MT>(a, n0, threadIdx.x % 64);
 }
 
 }  // namespace gemv

@@ -31,6 +31,9 @@ int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 int64_t aligned(int64_t bytes) { return round_up(bytes, kWorkspaceAlign); }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t least(int64_t cols) { return cols > 1 ? cols : 1; }
+// Workgroups for kernels that go over their rows with the grid's stride: a launch takes less than
+// 2^32 threads.
+int64_t held_grid(int64_t workgroups) { return workgroups < (1 << 20) ? workgroups : 1 << 20; }
 bool rows16(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
 
 struct Region {

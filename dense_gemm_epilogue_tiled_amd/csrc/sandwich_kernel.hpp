@@ -44,6 +44,7 @@ struct Args {
     int64_t M, N, ldy, ldr, ldt, ldn, ld_gate;
     int64_t group;                                     // rows per gate
     float scale, eps;
+    int64_t first;                                     // row of the launch's first workgroup
 };
 
 // The chunks of 8 columns that thread t of TPR has of rows of N: how many columns each
@@ -111,7 +112,7 @@ template <typename E, int TPR, int C, bool WHOLE>
 __global__ void __launch_bounds__(threads_for(TPR)) forward_kernel(Args a) {
     constexpr int kRows = rows_at_once(TPR);
     __shared__ float red[2][TPR > 64 ? TPR / 64 : 1];
-    const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+    const int64_t row = a.first + (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
     if (row >= a.M) return;  // whole waves, and no barrier where TPR is 64
     const Columns<TPR, C, WHOLE> col(threadIdx.x % TPR, a.N);
     u32x4 y[C], s[C], w[C], g[C], w2[C];

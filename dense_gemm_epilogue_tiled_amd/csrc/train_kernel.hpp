@@ -218,10 +218,10 @@ __global__ void __launch_bounds__(THREADS) gated_backward_kernel(GatedBwdArgs a,
 template <typename E>
 __global__ void __launch_bounds__(THREADS) row_sums_kernel(const uint16_t* src, int64_t rows, int64_t cols, int64_t ld,
                                                            uint16_t* out) {
-    const int64_t r = (int64_t)blockIdx.x * (THREADS / 64) + threadIdx.x / 64;
-    if (r >= rows) return;
-    const float s = own::row_sum<E>(src + r * ld, cols);
-    if (threadIdx.x % 64 == 0) out[r] = E::round(s);
+    for (int64_t r = (int64_t)blockIdx.x * (THREADS / 64) + threadIdx.x / 64; r < rows; r += (int64_t)gridDim.x * (THREADS / 64)) {
+        const float s = own::row_sum<E>(src + r * ld, cols);
+        if (threadIdx.x % 64 == 0) out[r] = E::round(s);
+    }
 }
 
 }  // namespace train

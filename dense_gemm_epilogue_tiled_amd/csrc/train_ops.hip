@@ -57,7 +57,7 @@ int run_gated(int64_t M, int64_t I, int64_t H, const uint16_t* X, int64_t ldx, c
     if (M <= kGemvRows) {
         using namespace gr::gemv;
         const Args a{X, W, C, M, I, H, ldx, ldw, ldc, ep};
-        const int64_t grid = ceil_div(I, WAVES * COLS);
+        const int64_t grid = held_grid(ceil_div(I, WAVES * COLS));
         if (M == 1) return launch(gated_gemv_kernel<Base, 1>, grid, THREADS, stream, a);
         if (M == 2) return launch(gated_gemv_kernel<Base, 2>, grid, THREADS, stream, a);
         return launch(gated_gemv_kernel<Base, 4>, grid, THREADS, stream, a);
@@ -176,7 +176,7 @@ int input_grad(const InputGradLayout& l, int64_t M, int64_t K, int64_t N, const 
 
 template <typename Base>
 int bias_grad(int64_t N, int64_t Mp, const uint16_t* dYt, uint16_t* dB, hipStream_t stream) {
-    return launch(gr::train::row_sums_kernel<Base>, ceil_div(N, 4), gr::train::THREADS, stream, dYt, N, Mp, Mp, dB);
+    return launch(gr::train::row_sums_kernel<Base>, held_grid(ceil_div(N, 4)), gr::train::THREADS, stream, dYt, N, Mp, Mp, dB);
 }
 
 // dX, dW (N x K) and dB from what the copies made ready; rest: input_grad's workspace.

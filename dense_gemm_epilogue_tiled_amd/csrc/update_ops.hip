@@ -50,10 +50,18 @@ int run_sandwich(const gr::sandwich::Args& a, hipStream_t stream) {
     return by_width(a.N, a.M <= kCus, [&](auto tpr, auto c) {
         constexpr int TPR = decltype(tpr)::value, C = decltype(c)::value;
         using namespace gr::sandwich;
-        const int64_t grid = ceil_div(a.M, rows_at_once(TPR));
+        // (a launch takes less than 2^32 threads)
+        constexpr int64_t most = (int64_t(1) << 20) * rows_at_once(TPR);
         const int threads = threads_for(TPR);
-        return a.N % 8 == 0 ? launch(gr::sandwich::forward_kernel<E, TPR, C, true>, grid, threads, stream, a)
-                            : launch(gr::sandwich::forward_kernel<E, TPR, C, false>, grid, threads, stream, a);
+        int st = GR_OK;
+        for (int64_t first = 0; st == GR_OK && first < a.M; first += most) {
+            Args part = a;
+            part.first = first;
+            const int64_t rows = a.M - first < most ? a.M - first : most, grid = ceil_div(rows, rows_at_once(TPR));
+            st = a.N % 8 == 0 ? launch(forward_kernel<E, TPR, C, true>, grid, threads, stream, part)
+                              : launch(forward_kernel<E, TPR, C, false>, grid, threads, stream, part);
+        }
+        return st;
     });
 }
 
@@ -195,7 +203,7 @@ int sandwich_norm_fwd(int64_t M, int64_t N, const uint16_t* Y, int64_t ldy, cons
     if (st == GR_OK) st = check_regions(n_only, n_read);
     if (st == GR_OK) st = check_device();
     if (st != GR_OK) return st;
-    const gr::sandwich::Args a{Y, R, w, next_w, gate, total, normed, M, N, ldy, ldr, ldt, ldn, ld_gate, gate ? M / G : 1, scale, eps};
+    const gr::sandwich::Args a{Y, R, w, next_w, gate, total, normed, M, N, ldy, ldr, ldt, ldn, ld_gate, gate ? M / G : 1, scale, eps, 0};
     hipStream_t h = static_cast<hipStream_t>(stream);
     return fmt == GR_FMT_BF16 ? run_sandwich<ElemBF16>(a, h) : run_sandwich<ElemF16>(a, h);
 }

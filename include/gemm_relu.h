@@ -1012,7 +1012,9 @@ int gated_linear_bt(int64_t M, int64_t I, int64_t H,
  *   dX := dY * W (M x K),  dW := dY^T * X (N x K),  dB[n] := sum over m of dY[m][n]
  * in fp32, each rounded once to fmt.  dX, dW, dB: NULL for one that is not wanted (W
  * is read for dX only, X for dW only).  With M = 0, dW and dB are zeros.  The sums over the
- * tokens run in a fixed order.  The size depends on which gradients are asked for and on the
+ * tokens run in a fixed order, the same with and without the other gradients.  The workspace
+ * holds dY and X transposed, with the tokens padded to multiples of 64, and where dX needs it W
+ * transposed (gated_linear_backward: dg and du as well).  The size depends on which gradients are asked for and on the
  * addresses' alignment: give the pointers of the call.  M above 2^22 is
  * GR_ERR_TOO_LARGE.
  */
@@ -1034,7 +1036,8 @@ int linear_backward(int64_t M, int64_t N, int64_t K,
 /*
  * gated_linear_backward -- the gradients of gated_linear_bt from dH (M x I) and what it kept
  * in GU (M x 2I):
- *   dg = dH * u * act'(g),  du = dH * act(g)      (fp32, rounded to fmt)
+ *   dg = dH * u * act'(g),  du = dH * act(g)      (fp32, rounded to fmt: infinite
+ *                                                  beyond its range)
  *   dX := (dg, du) * W13 (M x H),  dW13 := (dg, du)^T * X (2I x H),  dB13 := the sums of (dg, du)
  * as in linear_backward.  The derivative of GR_ACT_RELU at 0 is 0.
  */
@@ -1058,7 +1061,8 @@ int gated_linear_backward(int64_t M, int64_t I, int64_t H,
  *   total  = round16(R + scale * gate * norm(Y) * w)
  *   normed = norm(total) * next_w                   (NULL: not wanted)
  * with norm(v) = v / sqrt(mean over the row of v^2 + eps), in fp32 from 16-bit values, each
- * rounded once.
+ * rounded once.  Squares are summed in fp32: a row whose sum passes 3.4e38 counts as of
+ * infinite length.
  *   Y, R, total, normed   M x N in fmt
  *   w, next_w  N values in fmt, NULL for ones
  *   gate       G x N in fmt (pitch ld_gate), one row for every M / G consecutive rows, G a
@@ -1104,8 +1108,10 @@ int sandwich_norm_bwd(int64_t M, int64_t N,
  *              batch_g elements from one matrix to the next (of no meaning for B = 1)
  *   coefficients  a, b, c: host memory
  *   out        B x rows x cols bfloat16
- * Products are fp16 x fp16 with fp32 sums, X, A and b A + c A A rounded to 11 bits each step
- * (scaled by powers of two; singular values up to 8 stay finite).  Sides up to 65536, B up to
+ * Products are fp16 x fp16 with fp32 sums; X times 2^13, A times 2^10 and B = b A + c A A - (b +
+ * c) I times 2^10 are rounded to fp16 each step.  They stay finite while X's singular values,
+ * which begin at 1 at most, are below 8 and B's elements below 64 (with the usual coefficients:
+ * singular values below 2.6; they stay below 1.3).  Sides up to 65536, B up to
  * 65535 (GR_ERR_TOO_LARGE), 1 to 64 steps (GR_ERR_INVALID_ARG).  A zero matrix gives zeros, one with an infinity or
  * a NaN gives NaN.
  */

@@ -565,3 +565,69 @@ def test_update_matrix_moves_along_the_orthogonalised_momentum():
     assert torch.equal(m, mom)
     want = before.add(gr.orthogonalize(mom * 0.9 + grad, scale=(130 / 70) ** 0.5), alpha=-0.5)
     assert torch.equal(w, want)
+
+
+# ---- corners ---------------------------------------------------------------------------------------
+
+def test_gated_gradients_of_empty_sides():
+    dh, x = torch.empty(5, 0, dtype=torch.bfloat16, device="cuda"), make((5, 32), "bf16", 970).cuda()
+    w = torch.empty(0, 32, dtype=torch.bfloat16, device="cuda")
+    dx, dw, db = gr.gated_linear_backward(dh, x, w, dh, bias=True)
+    assert dx.shape == (5, 32) and not dx.any() and dw.shape == (0, 32) and db.shape == (0,)
+    h, gu = gr.gated_linear(x, w, keep=True)
+    assert h.shape == (5, 0) and gu.shape == (5, 0)
+    dh, gu = make((70, 8), "bf16", 971), make((70, 16), "bf16", 972)
+    no_x, no_w = torch.empty(70, 0, dtype=torch.bfloat16, device="cuda"), torch.empty(16, 0, dtype=torch.bfloat16, device="cuda")
+    dx, dw, db = gr.gated_linear_backward(dh.cuda(), no_x, no_w, gu.cuda(), bias=True)
+    assert dx.shape == (70, 0) and dw.shape == (16, 0)
+    refs, bounds = train_ref.gated_backward(dh, torch.zeros(70, 1), torch.zeros(16, 1), gu, "silu")
+    check16(db.cpu(), refs[2], db.dtype, bounds[2])
+
+
+def far(t, pitch):
+    """t's rows `pitch` elements apart, past 2^32 bytes in all."""
+    buf = torch.empty(t.shape[0] * pitch, dtype=t.dtype, device="cuda")
+    v = torch.as_strided(buf, t.shape, (pitch, 1))
+    v.copy_(t)
+    return v
+
+
+def test_far_rows():
+    """Rows 4 MB apart: offsets beyond 32 bits in every operand and output, on each kernel's tiles."""
+    pitch = 1 << 21
+    M, H, I = 1100, 64, 72
+    x, w, dh = make((M, H), "bf16", 980).cuda(), make((2 * I, H), "bf16", 981, H ** -0.5).cuda(), make((M, I), "bf16", 982).cuda()
+    want, want_gu = gr.gated_linear(x, w, keep=True)
+    out = far(torch.zeros_like(want), pitch)
+    got, gu = gr.gated_linear(far(x, pitch), w, keep=True, out=out, gu_out=far(torch.zeros_like(want_gu), pitch))
+    assert torch.equal(got, want) and torch.equal(gu, want_gu)
+    dx, dw, _ = gr.gated_linear_backward(dh, x, w, want_gu)
+    a, b, _ = gr.gated_linear_backward(far(dh, pitch), far(x, pitch), w, gu, dx_out=out.as_strided((M, H), (pitch, 1)))
+    assert torch.equal(a, dx) and torch.equal(b, dw)
+    del out, got, gu
+    y, res = make((M, I), "bf16", 983).cuda(), make((M, I), "bf16", 984).cuda()
+    total, normed = gr.sandwich_norm(y, res)
+    a, b = gr.sandwich_norm(far(y, pitch), far(res, pitch), total_out=far(torch.zeros_like(y), pitch))
+    assert torch.equal(a, total) and torch.equal(b, normed)
+
+
+def test_rows_beyond_one_launch():
+    """More rows than one launch's threads: the last ones are computed too."""
+    M, N = (1 << 22) + 5, 8
+    y, res = torch.randn(M, N, device="cuda").bfloat16(), torch.randn(M, N, device="cuda").bfloat16()
+    gate = torch.randn(3, N, device="cuda").bfloat16()
+    assert M % 3 == 0
+    total, normed = gr.sandwich_norm(y, res, gate=gate)
+    tail = slice(M - 9, M)
+    a, b = gr.sandwich_norm(y[tail], res[tail], gate=gate[2])
+    assert torch.equal(total[tail], a) and torch.equal(normed[tail], b)
+
+
+def test_wide_gates_of_few_tokens():
+    """More columns than one pass of the kernel for few tokens takes."""
+    M, I, H = 2, (1 << 23) + 77, 8
+    x, w = make((M, H), "bf16", 990).cuda(), torch.randn(2 * I, H, device="cuda").bfloat16()
+    h, _ = gr.gated_linear(x, w)
+    at = torch.tensor([0, 1, 4095, (1 << 23) - 1, 1 << 23, (1 << 23) + 1, I - 1], device="cuda")
+    some, _ = gr.gated_linear(x, torch.cat((w[at], w[I + at])))
+    assert torch.equal(h[:, at], some)
