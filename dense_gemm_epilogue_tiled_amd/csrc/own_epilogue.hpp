@@ -164,6 +164,11 @@ struct Product {
     int64_t M, N, K, lda, ldb, ldc;
     uint32_t n_blocks, blocks;  // blocks (tiles) across the columns, and all of them
     uint32_t order;             // tile_of_workgroup's
+    // K cut into `splits` ranges of k_per, whose fp32 sums go to part[split][m][n] for a second
+    // pass (row-blocked stream only); part nullptr: whole
+    uint32_t splits;
+    int64_t k_per;
+    float* part;
 };
 struct TwoArgs {
     Product product[2];
@@ -193,7 +198,7 @@ struct Two : Own<Base> {
     // Whether workgroup wg, of WAVES waves, is one for sums: then they are done.
     template <int WAVES>
     static __device__ __forceinline__ bool sums(const Args& ep, uint32_t wg) {
-        const uint32_t products = ep.product[0].blocks + ep.product[1].blocks;
+        const uint32_t products = ep.product[0].blocks * ep.product[0].splits + ep.product[1].blocks * ep.product[1].splits;
         if (wg < products) return false;
         const int64_t r = (int64_t)(wg - products) * WAVES + threadIdx.x / 64;
         if (r < ep.sum_rows) {
@@ -202,26 +207,38 @@ struct Two : Own<Base> {
         }
         return true;
     }
-    static __device__ __forceinline__ void select(const Args& ep, uint32_t& wg, uint32_t& n_wg, const uint16_t* __restrict__& A,
+    // Sets a workgroup's product and its number among that product's; returns where its sums go
+    // (nullptr: rounded to C).
+    static __device__ __forceinline__ float* select(const Args& ep, uint32_t& wg, uint32_t& n_wg, const uint16_t* __restrict__& A,
                                                   const uint16_t* __restrict__& B, uint16_t* __restrict__& C, int64_t& M,
                                                   int64_t& N, int64_t& K, int64_t& lda, int64_t& ldb, int64_t& ldc,
                                                   uint32_t& n_blocks, uint32_t& order) {
-        const bool second = wg >= ep.product[0].blocks;
-        if (second) wg -= ep.product[0].blocks;
+        const uint32_t first = ep.product[0].blocks * ep.product[0].splits;
+        const bool second = wg >= first;
+        if (second) wg -= first;
         const Product p = second ? ep.product[1] : ep.product[0];
-        A = p.A;
-        B = p.Bt;
+        const uint32_t split = p.splits > 1 ? wg / p.blocks : 0;
+        wg -= split * p.blocks;
+        const int64_t k0 = split * p.k_per;
+        A = p.A + k0;
+        B = p.Bt + k0;
         C = p.C;
         M = p.M;
         N = p.N;
-        K = p.K;
+        K = p.K - k0 < p.k_per ? p.K - k0 : p.k_per;
         lda = p.lda;
         ldb = p.ldb;
         ldc = p.ldc;
         n_wg = p.blocks;
         n_blocks = p.n_blocks;
         order = p.order;
+        return p.part != nullptr ? p.part + split * p.M * p.N : nullptr;
     }
+
+    template <int N>
+    struct Held : NothingHeld<N> {
+        float* part;
+    };
 
     template <bool EDGE, typename Acc>
     static __device__ __forceinline__ void store_tile(Acc& acc, uint8_t* region, uint32_t lane, uint16_t* C, int64_t ldc,
@@ -230,9 +247,26 @@ struct Two : Own<Base> {
         Plain<Base>::template store_tile<EDGE>(acc, region, lane, C, ldc, row0, col0, row_min, M, N, PlainArgs{});
     }
     template <int ROWS, int ON, int T, typename S, typename K, typename H>
-    static __device__ __forceinline__ void store_block(S sum4, K keep4, const H& held, uint16_t* C, int64_t ldc, int64_t row0, int64_t M,
-                                                       int64_t N, int64_t n0, int64_t n_own, const Args&) {
-        Plain<Base>::template store_block<ROWS, ON, T>(sum4, keep4, held, C, ldc, row0, M, N, n0, n_own, PlainArgs{});
+    static __device__ __forceinline__ void store_block(S sum4, K keep4, const H& held, uint16_t* C, int64_t ldc, int64_t row0,
+                                                       int64_t M, int64_t N, int64_t n0, int64_t n_own, const Args&) {
+        if (held.part == nullptr) {
+            Plain<Base>::template store_block<ROWS, ON, T>(sum4, keep4, held, C, ldc, row0, M, N, n0, n_own, PlainArgs{});
+            return;
+        }
+        typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+        for (uint32_t o = threadIdx.x; o < (uint32_t)(ROWS * ON / 4); o += T) {
+            const uint32_t m = o / (ON / 4), c = 4 * (o % (ON / 4));
+            if ((int64_t)m >= M) continue;
+            const f32x4 s = sum4(m, c);
+            float* const to = held.part + (row0 + m) * N + n0 + c;
+            if (n0 + c >= n_own) {
+                *reinterpret_cast<f32x4_any*>(to) = s;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n0 + c + e >= n_own) to[e] = s[e];
+            }
+        }
     }
 };
 

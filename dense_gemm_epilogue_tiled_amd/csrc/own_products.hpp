@@ -2,6 +2,7 @@
 // kernel and its launch.
 #pragma once
 
+#include <algorithm>
 #include <initializer_list>
 
 #include "host.hpp"
@@ -136,22 +137,54 @@ int product(Kernel kernel, int64_t B, int64_t M, int64_t N, int64_t K, const uin
     }
 }
 
-// The kernel for two plain products (M x N x K each) in one launch, or kTile256 for none: the
-// stream while the blocks of both fit the chip, else 128 x 128 tiles where each alone would take
-// them.
+// How a weight's gradient, a plain product whose K are the tokens, is computed beside an
+// input's.  Streamed, where the blocks (of both, if `together`: one launch) fit the chip; its K
+// is then cut into `splits` ranges for blocks that would stay empty otherwise, if that saves a
+// wave kPassSteps steps of 32, which take about as long as the second pass over the ranges'
+// sums (whole and cut, all of linear_backward in bf16: 8192 tokens x 256 x 256 47 and 25 us,
+// 6061 x 320 x 222 40 and 22, 4096 x 64 x 64 23 and 11; 2048 x 768 x 768 saves too little: 30
+// whole).  8 or 4 waves to a block, whichever leaves the longer product fewer steps per wave.
+// Else 128 x 128 tiles together where each alone would take them, or by itself by the rule
+// above.
 struct Shape {
     int64_t M, N, K;
 };
-Kernel choose_small(const Shape (&products)[2]) {
-    int64_t blocks = 0;
-    bool streams = true, tiles = true;
-    for (const Shape& p : products) {
-        blocks += ceil_div(p.M, kStreamRows) * ceil_div(p.N, kStreamNB);
-        streams = streams && p.N >= kStreamNB;
-        tiles = tiles && choose(1, p.M, p.N, p.K, 1) == kTile128;
+struct WeightPlan {
+    Kernel kernel;
+    bool together;
+    int64_t splits, k_per;
+};
+
+// `other` blocks of a product with `other_steps` of 32 run beside; false: more than fit.
+constexpr int64_t kPassSteps = 10;
+bool plan_stream(const Shape& p, int64_t other, int64_t other_steps, WeightPlan* plan) {
+    const int64_t blocks = ceil_div(p.M, kStreamRows) * ceil_div(p.N, kStreamNB);
+    int64_t least_steps = 0;
+    for (const Kernel kernel : {kStream8, kStream4}) {
+        const int64_t waves = kernel == kStream8 ? kStreamWOne : kStreamW, most = kernel == kStream8 ? 256 : 512;
+        if (blocks == 0 || blocks + other > most) continue;
+        int64_t k_per = p.K, splits = (most - other) / blocks;
+        splits = std::min<int64_t>(splits, 32);
+        const int64_t whole = p.K / 32 / waves, cut = round_up(ceil_div(p.K, splits), 32 * waves);
+        if (whole - cut / 32 / waves >= kPassSteps) k_per = cut;
+        splits = ceil_div(p.K, k_per);
+        const int64_t steps = std::max(k_per / 32 / waves + (splits > 1 ? kPassSteps : 0), other_steps / waves);
+        if (least_steps == 0 || steps < least_steps) {
+            *plan = {kernel, other > 0, splits, k_per};
+            least_steps = steps > 0 ? steps : 1;
+        }
     }
-    if (streams && blocks <= 512) return blocks <= 256 ? kStream8 : kStream4;
-    return tiles ? kTile128 : kTile256;
+    return least_steps > 0;
+}
+
+WeightPlan plan_weight(const Shape& weight, const Shape& input) {
+    WeightPlan plan{choose(1, weight.M, weight.N, weight.K, 1), false, 1, weight.K};
+    const int64_t beside = ceil_div(input.M, kStreamRows) * ceil_div(input.N, kStreamNB);
+    if (weight.N >= kStreamNB && input.N >= kStreamNB && beside > 0 && plan_stream(weight, beside, input.K / 32, &plan)) return plan;
+    plan.together = plan.kernel == kTile128 && choose(1, input.M, input.N, input.K, 1) == kTile128;
+    WeightPlan cut = plan;
+    if (!plan.together && weight.N >= kStreamNB && plan_stream(weight, 0, 0, &cut) && cut.splits > 1) return cut;
+    return plan;
 }
 
 // Up to two plain products and the sums over the rows of the first one's A, in one launch
@@ -163,7 +196,7 @@ struct Small {
 
     void add(int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda, const uint16_t* Bt, int64_t ldb, uint16_t* C,
              int64_t ldc) {
-        args.product[count++] = {A, Bt, C, M, N, K, lda, ldb, ldc, 1, 0, 0};
+        args.product[count++] = {A, Bt, C, M, N, K, lda, ldb, ldc, 1, 0, 0, 1, K, nullptr};
     }
     int run(Kernel kernel, hipStream_t stream) {
         using E = gr::own::Two<Base>;
@@ -174,7 +207,7 @@ struct Small {
             p.n_blocks = (uint32_t)ceil_div(p.N, side);
             p.blocks = (uint32_t)ceil_div(p.M, side) * p.n_blocks;
             p.order = kernel != kTile128 && p.n_blocks % 4 == 0 ? (gr::kNoXcdRemap | 1u) : kGroupM;
-            grid += p.blocks;
+            grid += (int64_t)p.blocks * p.splits;
         }
         const gr::own::TwoArgs a = args;
         const int64_t none = 0;

@@ -295,9 +295,10 @@ __global__ __launch_bounds__(64 * W, 1) void gemm_relu_smallm_stream_kernel(
     const uint32_t tid = threadIdx.x, lane = tid & 63u;
     const uint32_t w = __builtin_amdgcn_readfirstlane(tid >> 6);
     uint32_t wg = blockIdx.x, n_wg = gridDim.x;
+    float* sums_to = nullptr;  // where a second pass takes the fp32 sums from, if one does
     if constexpr (E::kTwo) {
         if (E::template sums<W>(ep, wg)) return;
-        E::select(ep, wg, n_wg, A, B, C, M, N, K, lda, ldb, ldc, n_blocks, order);
+        sums_to = E::select(ep, wg, n_wg, A, B, C, M, N, K, lda, ldb, ldc, n_blocks, order);
         k_per_split = K;
     }
     uint32_t cb;
@@ -403,6 +404,7 @@ __global__ __launch_bounds__(64 * W, 1) void gemm_relu_smallm_stream_kernel(
 
     // what an epilogue of one's own reads, on its way before the operands
     typename E::template Held<E::kOwn ? ROWS * ON / 4 / T : 1> held;
+    if constexpr (E::kTwo) held.part = sums_to;
     if constexpr (E::kOwn) held.fetch(ep, ON, T, row0, M, N, n0);
 
     // R - 1 slots ahead: slot q + R - 1 goes out (into the entry slot q - 1

@@ -224,5 +224,31 @@ __global__ void __launch_bounds__(THREADS) row_sums_kernel(const uint16_t* src, 
     }
 }
 
+// C[m][n] = round(the sum over the splits, in order, of part[split][m][n]): the second pass of a
+// weight's gradient whose tokens were cut into ranges.  Four columns per thread where N allows.
+template <typename E, int VEC>
+__global__ void __launch_bounds__(THREADS) sum_splits_kernel(const float* part, int64_t splits, int64_t M, int64_t N, uint16_t* C,
+                                                             int64_t ldc) {
+    const int64_t total = M * N, step = (int64_t)gridDim.x * THREADS * VEC;
+    for (int64_t o = ((int64_t)blockIdx.x * THREADS + threadIdx.x) * VEC; o < total; o += step) {
+        float sum[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sum[e] = 0.0f;
+#pragma unroll 4
+        for (int64_t s = 0; s < splits; ++s) {
+            if constexpr (VEC == 4) {
+                const f32x4 v = *reinterpret_cast<const f32x4*>(part + s * total + o);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] += v[e];
+            } else {
+                sum[0] += part[s * total + o];
+            }
+        }
+        const int64_t m = o / N, n = o - m * N;
+        if constexpr (VEC == 4) own::put4<E>(C + m * ldc + n, sum, n, 0, N);
+        else C[m * ldc + n] = E::round(sum[0]);
+    }
+}
+
 }  // namespace train
 }  // namespace gr

@@ -179,21 +179,40 @@ int bias_grad(int64_t N, int64_t Mp, const uint16_t* dYt, uint16_t* dB, hipStrea
     return launch(gr::train::row_sums_kernel<Base>, held_grid(ceil_div(N, 4)), gr::train::THREADS, stream, dYt, N, Mp, Mp, dB);
 }
 
+int64_t padded_tokens(int64_t M) { return M > 0 ? round_up(M, gr::train::PAD) : gr::train::PAD; }
+
+WeightPlan weight_plan(int64_t M, int64_t N, int64_t K) {
+    return plan_weight({N, K, padded_tokens(M)}, {M, K, padded_depth(N)});
+}
+// fp32 sums of the ranges of tokens.
+int64_t parts_need(int64_t M, int64_t N, int64_t K) {
+    const WeightPlan plan = weight_plan(M, N, K);
+    return plan.splits > 1 ? aligned(plan.splits * N * K * 4) : 0;
+}
+
 // dX, dW (N x K) and dB from what the copies made ready; rest: input_grad's workspace.
 template <typename Base>
 int grad_products(const InputGradLayout& l, int64_t M, int64_t N, int64_t K, int64_t Mp, const uint16_t* dYt, const uint16_t* Xt,
                   const uint16_t* dY, int64_t lddy, const uint16_t* W, int64_t ldw, uint16_t* dX, int64_t lddx, uint16_t* dW,
-                  int64_t lddw, uint16_t* dB, uint8_t* rest, hipStream_t stream) {
+                  int64_t lddw, uint16_t* dB, float* part, uint8_t* rest, hipStream_t stream) {
     const bool weight = dW && N > 0 && K > 0, input = dX && M > 0 && K > 0, bias = dB && N > 0;
     // by the shapes alone, so that a gradient has the same bits with and without the others
     const int64_t Np = padded_depth(N);
-    const Kernel both = choose_small({{N, K, Mp}, {M, K, Np}});
-    const Kernel kernel = both != kTile256 ? both : choose(1, N, K, Mp, 1);  // dW's
-    const bool together = both != kTile256 && input && l.kind == kTransposed;
+    const WeightPlan plan = weight_plan(M, N, K);
+    const Kernel kernel = plan.kernel;  // dW's
+    const bool together = plan.together && input && l.kind == kTransposed;
     int st = GR_OK;
     if (kernel != kTile256 && (weight || together)) {
         Small<Base> small;
-        if (weight) small.add(N, K, Mp, dYt, Mp, Xt, Mp, dW, lddw);
+        if (weight) {
+            small.add(N, K, Mp, dYt, Mp, Xt, Mp, dW, lddw);
+            if (plan.splits > 1) {
+                gr::own::Product& p = small.args.product[0];
+                p.splits = (uint32_t)plan.splits;
+                p.k_per = plan.k_per;
+                p.part = part;
+            }
+        }
         if (together)
             small.add(M, K, Np, l.dy > 0 ? reinterpret_cast<const uint16_t*>(rest + l.wt) : dY, Np,
                       reinterpret_cast<const uint16_t*>(rest), Np, dX, lddx);
@@ -202,6 +221,14 @@ int grad_products(const InputGradLayout& l, int64_t M, int64_t N, int64_t K, int
             small.args.sum_rows = N;
         }
         st = small.run(kernel, stream);
+        if (st == GR_OK && weight && plan.splits > 1) {
+            using namespace gr::train;
+            const float* const from = part;
+            const int vec = K % 4 == 0 ? 4 : 1;
+            const int64_t grid = ceil_div(N * K, THREADS * vec) < 2048 ? ceil_div(N * K, THREADS * vec) : 2048;
+            st = vec == 4 ? launch(sum_splits_kernel<Base, 4>, grid, THREADS, stream, from, plan.splits, N, K, dW, lddw)
+                          : launch(sum_splits_kernel<Base, 1>, grid, THREADS, stream, from, plan.splits, N, K, dW, lddw);
+        }
     } else if (weight) {
         st = product<gr::own::Plain<Base>>(kernel, 1, N, K, Mp, dYt, Mp, Xt, Mp, dW, lddw, gr::own::PlainArgs{}, stream);
     }
@@ -210,13 +237,11 @@ int grad_products(const InputGradLayout& l, int64_t M, int64_t N, int64_t K, int
     return st;
 }
 
-int64_t padded_tokens(int64_t M) { return M > 0 ? round_up(M, gr::train::PAD) : gr::train::PAD; }
-
 // The parts of the workspace, in order; only those of the gradients that are asked for.
 struct GradLayout {
-    int64_t dyt, xt, dy;    // bytes: dY^T, X^T, dY (of the gated layer)
-    InputGradLayout input;  // what dX's product takes
-    int64_t total() const { return dyt + xt + dy + input.total(); }
+    int64_t dyt, xt, dy, parts;  // bytes: dY^T, X^T, dY (of the gated layer), fp32 sums
+    InputGradLayout input;       // what dX's product takes
+    int64_t total() const { return dyt + xt + dy + parts + input.total(); }
 };
 
 int linear_layout(int64_t M, int64_t N, int64_t K, const uint16_t* dY, int64_t lddy, const uint16_t* W, int64_t ldw,
@@ -225,6 +250,7 @@ int linear_layout(int64_t M, int64_t N, int64_t K, const uint16_t* dY, int64_t l
     l->dyt = (dW || dB) ? aligned(2 * N * Mp) : 0;
     l->xt = dW ? aligned(2 * K * Mp) : 0;
     l->dy = 0;
+    l->parts = dW ? parts_need(M, N, K) : 0;
     l->input = InputGradLayout{};
     return dX ? input_grad_layout(M, K, N, dY, lddy, false, W, ldw, dX, lddx, &l->input) : GR_OK;
 }
@@ -251,14 +277,15 @@ int run_linear_backward(int64_t M, int64_t N, int64_t K, const uint16_t* dY, int
     const int64_t Mp = padded_tokens(M);
     uint16_t* const dyt = reinterpret_cast<uint16_t*>(ws);
     uint16_t* const xt = reinterpret_cast<uint16_t*>(ws + l.dyt);
-    uint8_t* const rest = ws + l.dyt + l.xt;
+    float* const part = reinterpret_cast<float*>(ws + l.dyt + l.xt);
+    uint8_t* const rest = ws + l.dyt + l.xt + l.parts;
     Relayouts copies;
     if (dB || (dW && K > 0)) copies.add(true, dY, M, N, lddy, dyt, Mp);
     if (dW && N > 0) copies.add(true, X, M, K, ldx, xt, Mp);
     if (dX && M > 0 && K > 0) input_grad_copies(l.input, M, K, N, dY, lddy, W, ldw, rest, &copies);
     const int st = copies.run(stream);
     if (st != GR_OK) return st;
-    return grad_products<Base>(l.input, M, N, K, Mp, dyt, xt, dY, lddy, W, ldw, dX, lddx, dW, lddw, dB, rest, stream);
+    return grad_products<Base>(l.input, M, N, K, Mp, dyt, xt, dY, lddy, W, ldw, dX, lddx, dW, lddw, dB, part, rest, stream);
 }
 
 int gated_layout(int64_t M, int64_t I, int64_t H, const uint16_t* W, int64_t ldw, const uint16_t* dX, int64_t lddx,
@@ -267,6 +294,7 @@ int gated_layout(int64_t M, int64_t I, int64_t H, const uint16_t* W, int64_t ldw
     l->dyt = (dW || dB) ? aligned(4 * I * Mp) : 0;
     l->xt = dW ? aligned(2 * H * Mp) : 0;
     l->dy = aligned(2 * M * ld);
+    l->parts = dW ? parts_need(M, 2 * I, H) : 0;
     l->input = InputGradLayout{};
     if (!dX) return GR_OK;
     // the gradient of the products lies in the workspace: an aligned address that is
@@ -299,7 +327,8 @@ int run_gated_backward(int64_t M, int64_t I, int64_t H, const uint16_t* dH, int6
     uint16_t* const dyt = reinterpret_cast<uint16_t*>(ws);
     uint16_t* const xt = reinterpret_cast<uint16_t*>(ws + l.dyt);
     uint16_t* const dgu = reinterpret_cast<uint16_t*>(ws + l.dyt + l.xt);
-    uint8_t* const rest = ws + l.dyt + l.xt + l.dy;
+    float* const part = reinterpret_cast<float*>(ws + l.dyt + l.xt + l.dy);
+    uint8_t* const rest = ws + l.dyt + l.xt + l.dy + l.parts;
     Relayouts copies;
     if (dW && I > 0) copies.add(true, X, M, H, ldx, xt, Mp);
     if (dX && M > 0 && H > 0) input_grad_copies(l.input, M, H, 2 * I, dgu, least(ld), W, ldw, rest, &copies);
@@ -312,7 +341,7 @@ int run_gated_backward(int64_t M, int64_t I, int64_t H, const uint16_t* dH, int6
         st = copies.run(stream);
     }
     if (st != GR_OK) return st;
-    return grad_products<Base>(l.input, M, 2 * I, H, Mp, dyt, xt, dgu, least(ld), W, ldw, dX, lddx, dW, lddw, dB, rest, stream);
+    return grad_products<Base>(l.input, M, 2 * I, H, Mp, dyt, xt, dgu, least(ld), W, ldw, dX, lddx, dW, lddw, dB, part, rest, stream);
 }
 
 }  // namespace

@@ -631,3 +631,17 @@ def test_wide_gates_of_few_tokens():
     at = torch.tensor([0, 1, 4095, (1 << 23) - 1, 1 << 23, (1 << 23) + 1, I - 1], device="cuda")
     some, _ = gr.gated_linear(x, torch.cat((w[at], w[I + at])))
     assert torch.equal(h[:, at], some)
+
+
+@pytest.mark.parametrize("M,N,K", [(6061, 320, 222), (8192, 70, 65), (5000, 128, 131), (20000, 64, 64)])
+def test_linear_backward_of_many_tokens(M, N, K):
+    """Few blocks and many tokens: the tokens are cut into ranges, whose sums a second pass adds."""
+    log("many tokens %dx%dx%d" % (M, N, K))
+    dy, x, w = make((M, N), "bf16", 1001), make((M, K), "bf16", 1002), make((N, K), "bf16", 1003, K ** -0.5)
+    dw, dw_buf = guarded(N, K, torch.bfloat16, 3)
+    got = gr.linear_backward(dy.cuda(), x.cuda(), w.cuda(), bias=True, dw_out=dw)
+    refs, bounds = train_ref.linear_backward(dy, x, w)
+    for g, r, b in zip(got, refs, bounds):
+        check16(g.cpu(), r, g.dtype, b)
+    untouched(dw_buf, N, K)
+    assert torch.equal(gr.linear_backward(dy.cuda(), x.cuda(), w.cuda(), input_grad=False)[1], dw)
