@@ -1,6 +1,6 @@
 // The whole orthogonalisation of a small matrix in one workgroup: X (r x c, fp16) and A (r x
 // r) stay in its LDS for all steps, where a step is otherwise three launches of a few
-// microseconds each (128 x 512: 93 us for five steps, 39 here; 64 x 64: 76 and 15).  r and c are
+// microseconds each (128 x 512: 93 us for five steps, 65 here; 64 x 64: 76 and 14).  r and c are
 // padded by zeros to multiples of 64, r to 64 or 128, and 2 r (c + r) bytes have to fit 160
 // KiB.
 //

@@ -435,7 +435,7 @@ struct Poly : Own<In> {
         const int64_t n = col0 + 8 * c;
         // D of 32 rows is fetched before the 32 rows in front of them are worked on: a load
         // where it is needed would cost every one of them its latency (4096 x 8192 x 4096:
-        // 275 -> 226 us)
+        // 275 -> 239 us)
         constexpr int IT = 32 / RPI;
         u32x4 next[IT];
         auto fetch = [&](int i) {

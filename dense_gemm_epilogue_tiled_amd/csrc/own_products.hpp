@@ -71,7 +71,7 @@ int check_workspace(const void* ws, int64_t bytes, int64_t need) {
 
 // The kernels of C (M x N) = own epilogue of A Bt^T, both operands k-contiguous, for a
 // type with an epilogue of its own.  `rows` of Bt make a column of C (2: paired).
-enum Kernel { kTile256, kTile128, kStream4, kStream8, kSmallM };
+enum Kernel { kTile256, kTile128, kStream4, kStream8 };
 
 // Which of them, for B products at once: up to 64 rows, and products of at most 512 blocks of 64 x 64 (sums of
 // N x rows) with a K long enough to fill them, are streamed; 256 x 256 tiles where there

@@ -19,19 +19,23 @@ constexpr int64_t kOrthoMax = 65536;  // either side of an update
 // ---- sandwich norm ----------------------------------------------------------------------
 
 // f<TPR, C>() for rows of N columns: threads per row and chunks of 8 columns per thread.
-// `wide`: one chunk per thread as far as it goes, for the backward pass, which needs the
-// registers, and for few rows, where more threads per row take fewer steps each.
-template <typename F>
-int by_width(int64_t N, bool wide, F&& f) {
+// `WIDE` (the backward pass, which needs the registers): one chunk as far as it goes.  Else two
+// from 2048 columns on and half as many threads, so that a CU holds more rows (forward, 8192 x 8192:
+// 93 us, 98 with one chunk; 64 x 8192 4.1 and 4.2, 1 x 4096 3.1 and 2.9).
+template <bool WIDE, typename F>
+int by_width(int64_t N, F&& f) {
     using std::integral_constant;
 #define GR_CASE(TPR, C) return f(integral_constant<int, TPR>{}, integral_constant<int, C>{})
     if (N <= 512) GR_CASE(64, 1);
     if (N <= 1024) GR_CASE(128, 1);
     if (N <= 2048) GR_CASE(256, 1);
-    if (N <= 4096 && !wide) GR_CASE(256, 2);
-    if (N <= 4096) GR_CASE(512, 1);
-    if (N <= 8192 && !wide) GR_CASE(512, 2);
-    if (N <= 8192) GR_CASE(1024, 1);
+    if constexpr (WIDE) {
+        if (N <= 4096) GR_CASE(512, 1);
+        if (N <= 8192) GR_CASE(1024, 1);
+    } else {
+        if (N <= 4096) GR_CASE(256, 2);
+        if (N <= 8192) GR_CASE(512, 2);
+    }
     if (N <= 16384) GR_CASE(1024, 2);
     GR_CASE(1024, 4);
 #undef GR_CASE
@@ -47,7 +51,7 @@ int check_sandwich(int64_t M, int64_t N, int64_t G, bool gate, float scale, floa
 
 template <typename E>
 int run_sandwich(const gr::sandwich::Args& a, hipStream_t stream) {
-    return by_width(a.N, a.M <= kCus, [&](auto tpr, auto c) {
+    return by_width<false>(a.N, [&](auto tpr, auto c) {
         constexpr int TPR = decltype(tpr)::value, C = decltype(c)::value;
         using namespace gr::sandwich;
         // (a launch takes less than 2^32 threads)
@@ -88,7 +92,7 @@ int run_sandwich_backward(const gr::sandwich::BwdArgs& a, hipStream_t stream) {
     using namespace gr::sandwich;
     int st = GR_OK;
     if (a.slots > 0)
-        st = by_width(a.N, true, [&](auto tpr, auto c) {
+        st = by_width<true>(a.N, [&](auto tpr, auto c) {
             constexpr int TPR = decltype(tpr)::value, C = decltype(c)::value;
             const int64_t grid = ceil_div(a.slots, rows_at_once(TPR));
             const int threads = threads_for(TPR);
