@@ -172,9 +172,10 @@ struct Product {
 };
 struct TwoArgs {
     Product product[2];
-    // sums[r] = the sum of row r of the first product's A, K values, for r < sum_rows
+    // sums[r] = the sum of row r of sum_of (sum_k values, rows like a product's A), for r < sum_rows
     uint16_t* sums;
-    int64_t sum_rows;
+    const uint16_t* sum_of;
+    int64_t sum_rows, sum_k;
 };
 
 // The sum of a row with a 16-byte start of `cols` (a multiple of 8) values over a wave, in
@@ -202,7 +203,7 @@ struct Two : Own<Base> {
         if (wg < products) return false;
         const int64_t r = (int64_t)(wg - products) * WAVES + threadIdx.x / 64;
         if (r < ep.sum_rows) {
-            const float s = row_sum<Base>(ep.product[0].A + r * ep.product[0].lda, ep.product[0].K);
+            const float s = row_sum<Base>(ep.sum_of + r * ep.sum_k, ep.sum_k);
             if (threadIdx.x % 64 == 0) ep.sums[r] = Base::round(s);
         }
         return true;

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <initializer_list>
+#include <utility>
 
 #include "host.hpp"
 #include "own_epilogue.hpp"
@@ -138,14 +139,17 @@ int product(Kernel kernel, int64_t B, int64_t M, int64_t N, int64_t K, const uin
 }
 
 // How a weight's gradient, a plain product whose K are the tokens, is computed beside an
-// input's.  Streamed, where the blocks (of both, if `together`: one launch) fit the chip; its K
-// is then cut into `splits` ranges for blocks that would stay empty otherwise, if that saves a
-// wave kPassSteps steps of 32, which take about as long as the second pass over the ranges'
-// sums (whole and cut, all of linear_backward in bf16: 8192 tokens x 256 x 256 47 and 25 us,
-// 6061 x 320 x 222 40 and 22, 4096 x 64 x 64 23 and 11; 2048 x 768 x 768 saves too little: 30
-// whole).  8 or 4 waves to a block, whichever leaves the longer product fewer steps per wave.
-// Else 128 x 128 tiles together where each alone would take them, or by itself by the rule
-// above.
+// input's.  Streamed, where the blocks (of both, if `together`: one launch) fit the chip, or
+// are half as many again and those of the longer product begin first (333 x 2080 x 1001, 528
+// and 96 blocks: 22 us, 28 as tiles and blocks of their own launches; 864 blocks would lose: 35 against 33).
+// Its K is then cut into `splits` ranges for blocks that would stay empty otherwise, if that
+// saves a wave kPassSteps steps of 32, which take about as long as the second pass over the
+// ranges' sums (whole and cut, all of linear_backward in bf16: 8192 tokens x 256 x 256 47 and
+// 23 us, 6061 x 320 x 222 40 and 22, 4096 x 64 x 64 23 and 11; 1024 x 1024 x 1024 saves too
+// little: 19 whole).  Of the
+// three ways to stream the one with the fewest steps per wave, where those of blocks that do
+// not all fit count one and a half.  Else 128 x 128 tiles together where each alone would
+// take them, or by itself by the rule above.
 struct Shape {
     int64_t M, N, K;
 };
@@ -159,22 +163,24 @@ struct WeightPlan {
 constexpr int64_t kPassSteps = 10;
 bool plan_stream(const Shape& p, int64_t other, int64_t other_steps, WeightPlan* plan) {
     const int64_t blocks = ceil_div(p.M, kStreamRows) * ceil_div(p.N, kStreamNB);
-    int64_t least_steps = 0;
-    for (const Kernel kernel : {kStream8, kStream4}) {
-        const int64_t waves = kernel == kStream8 ? kStreamWOne : kStreamW, most = kernel == kStream8 ? 256 : 512;
-        if (blocks == 0 || blocks + other > most) continue;
-        int64_t k_per = p.K, splits = (most - other) / blocks;
-        splits = std::min<int64_t>(splits, 32);
-        const int64_t whole = p.K / 32 / waves, cut = round_up(ceil_div(p.K, splits), 32 * waves);
-        if (whole - cut / 32 / waves >= kPassSteps) k_per = cut;
-        splits = ceil_div(p.K, k_per);
-        const int64_t steps = std::max(k_per / 32 / waves + (splits > 1 ? kPassSteps : 0), other_steps / waves);
-        if (least_steps == 0 || steps < least_steps) {
-            *plan = {kernel, other > 0, splits, k_per};
-            least_steps = steps > 0 ? steps : 1;
+    if (blocks == 0) return false;
+    struct Way {
+        Kernel kernel;
+        int64_t waves, most, cost;
+    };
+    int64_t least_cost = -1;
+    for (const Way& way : {Way{kStream8, kStreamWOne, 256, 2}, Way{kStream4, kStreamW, 512, 2}, Way{kStream4, kStreamW, 768, 3}}) {
+        if (blocks + other > way.most || (other == 0 && way.most > 512)) continue;
+        const int64_t step = 32 * way.waves, splits = std::min<int64_t>((way.most - other) / blocks, 32);
+        const int64_t cut = round_up(ceil_div(p.K, splits), step), k_per = p.K / step - cut / step >= kPassSteps ? cut : p.K;
+        const int64_t steps = k_per / step + (k_per < p.K ? kPassSteps : 0);
+        const int64_t cost = way.cost * std::max(steps, other_steps / way.waves);
+        if (least_cost < 0 || cost < least_cost) {
+            *plan = {way.kernel, other > 0, ceil_div(p.K, k_per), k_per};
+            least_cost = cost;
         }
     }
-    return least_steps > 0;
+    return least_cost >= 0;
 }
 
 WeightPlan plan_weight(const Shape& weight, const Shape& input) {
@@ -200,6 +206,8 @@ struct Small {
     }
     int run(Kernel kernel, hipStream_t stream) {
         using E = gr::own::Two<Base>;
+        // the longer blocks begin first
+        if (args.product[1].k_per > args.product[0].k_per) std::swap(args.product[0], args.product[1]);
         const int64_t side = kernel == kTile128 ? gr::tile128::BM : kStreamRows;
         int64_t grid = 0;
         for (int i = 0; i < count; ++i) {

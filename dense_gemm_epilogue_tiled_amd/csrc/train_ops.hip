@@ -218,7 +218,9 @@ int grad_products(const InputGradLayout& l, int64_t M, int64_t N, int64_t K, int
                       reinterpret_cast<const uint16_t*>(rest), Np, dX, lddx);
         if (weight && bias) {
             small.args.sums = dB;
+            small.args.sum_of = dYt;
             small.args.sum_rows = N;
+            small.args.sum_k = Mp;
         }
         st = small.run(kernel, stream);
         if (st == GR_OK && weight && plan.splits > 1) {

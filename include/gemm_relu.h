@@ -1014,7 +1014,7 @@ int gated_linear_bt(int64_t M, int64_t I, int64_t H,
  * is read for dX only, X for dW only).  With M = 0, dW and dB are zeros.  The sums over the
  * tokens run in a fixed order, the same with and without the other gradients.  The workspace
  * holds dY and X transposed, with the tokens padded to multiples of 64, where the tokens are
- * summed in ranges the ranges' fp32 sums (8 MiB at most), and where dX needs it W transposed
+ * summed in ranges the ranges' fp32 sums (12 MiB at most), and where dX needs it W transposed
  * (gated_linear_backward: dg and du as well).  The size depends on which gradients are asked
  * for and on the addresses' alignment: give the pointers of the call.  M above 2^22 is
  * GR_ERR_TOO_LARGE.
