@@ -63,7 +63,8 @@ struct PrepArgs {
     const void* src;
     int64_t rows, cols, ld, batch;  // of the update, batch: elements from one matrix to the next
     double* part;                   // PARTS per matrix
-    uint16_t *x, *xt;               // like the update, and transposed: zeros up to rows_pad, cols_pad
+    uint16_t *x, *xt;               // like the update, and transposed: zeros up to rows_pad, cols_pad; one
+                                    // may be nullptr
     int64_t rows_pad, cols_pad, batch_x;
     float eps;
 };
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(256) normalise_kernel(PrepArgs a, uint32_t til
     __syncthreads();
     sum = ((red[0] + red[1]) + red[2]) + red[3];
     const float f = (float)((double)SCALE_X / (__builtin_sqrt(sum) + (double)a.eps));
-    uint16_t* const x = a.x + blockIdx.y * a.batch_x;
+    uint16_t* const x = a.x + blockIdx.y * a.batch_x;  // (not used where there is none)
     uint16_t* const xt = a.xt + blockIdx.y * a.batch_x;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -124,9 +125,10 @@ __global__ void __launch_bounds__(256) normalise_kernel(PrepArgs a, uint32_t til
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[i][e] *= f;
         const u32x4 w = own::round8<ElemF16>(v[i]);
-        *reinterpret_cast<u32x4*>(x + (r0 + o / 8) * a.cols_pad + c0 + 8 * (o % 8)) = w;
+        if (a.x != nullptr) *reinterpret_cast<u32x4*>(x + (r0 + o / 8) * a.cols_pad + c0 + 8 * (o % 8)) = w;
         *reinterpret_cast<u32x4*>(lds + train::tile_off(o / 8, o % 8)) = w;
     }
+    if (a.xt == nullptr) return;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {

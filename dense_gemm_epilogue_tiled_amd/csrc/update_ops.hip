@@ -3,11 +3,13 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
 #include "../../include/gemm_relu.h"
 #include "own_products.hpp"
+#include "ortho_fold_kernel.hpp"
 #include "ortho_small_kernel.hpp"
 #include "sandwich_kernel.hpp"
 
@@ -114,7 +116,8 @@ struct OrthoLayout {
     int64_t rp, cp;  // padded
     int64_t parts, x, a;  // bytes: partial sums, one of the four X buffers, one of A and B
     bool small;           // in one workgroup's LDS, without a workspace
-    int64_t total() const { return small ? 0 : parts + 4 * x + 2 * a; }
+    bool fold;            // two launches a step: no X^T, no B
+    int64_t total() const { return small ? 0 : fold ? parts + 2 * x + a : parts + 4 * x + 2 * a; }
 };
 
 OrthoLayout ortho_layout(int64_t B, int64_t rows, int64_t cols) {
@@ -128,6 +131,7 @@ OrthoLayout ortho_layout(int64_t B, int64_t rows, int64_t cols) {
     l.x = aligned(B * l.rp * l.cp * 2);
     l.a = aligned(B * l.rp * l.rp * 2);
     l.small = l.rp <= gr::ortho::SMALL_R && 2 * l.rp * (l.rp + l.cp) <= gr::ortho::SMALL_LDS;
+    l.fold = !l.small && l.rp <= gr::ortho::FOLD_R;
     return l;
 }
 
@@ -146,6 +150,37 @@ int run_small(const OrthoLayout& l, int64_t B, const gr::ortho::SmallArgs& a, hi
     using namespace gr::ortho;
     return l.rp <= 64 ? launch(small_kernel<In, 64>, B, SMALL_THREADS, stream, a)
                       : launch(small_kernel<In, 128>, B, SMALL_THREADS, stream, a);
+}
+
+// Workgroups that walk over a matrix's blocks of columns: as many as the chip holds for all of the matrices.
+template <int RP>
+int run_fold_step(gr::ortho::FoldTo to, const OrthoLayout& l, int64_t B, const gr::ortho::FoldArgs& a, hipStream_t stream) {
+    using namespace gr::ortho;
+    const int64_t held = kCus * (FOLD_R / RP), blocks = l.cp / FOLD_COLS;
+    const dim3 grid((uint32_t)std::min(blocks, std::max<int64_t>(1, held / B)), (uint32_t)B);
+    if (to == kNextX) return launch_grid(fold_kernel<RP, kNextX>, grid, 2 * RP, stream, a);
+    if (to == kResult) return launch_grid(fold_kernel<RP, kResult>, grid, 2 * RP, stream, a);
+    return launch_grid(fold_kernel<RP, kResultTall>, grid, 2 * RP, stream, a);
+}
+
+int run_fold(const OrthoLayout& l, int64_t B, int64_t rows, int64_t cols, const float (&k)[3], int steps, float scale, uint16_t* out,
+             int64_t ldo, int64_t batch_o, uint16_t* const (&x)[2], uint16_t* d, hipStream_t stream) {
+    using namespace gr::ortho;
+    const int64_t rp = l.rp, cp = l.cp, bx = rp * cp, ba = rp * rp;
+    for (int s = 0; s < steps; ++s) {
+        const gr::own::PolyArgs p{nullptr, d, 0, rp, SCALE_A / (SCALE_X * SCALE_X), 0.0f, -SCALE_A, bx, bx, ba, 0, ba};
+        int st = symmetric<ElemF16>(B, rp, cp, x[s % 2], cp, d, rp, p, stream);
+        if (st != GR_OK) return st;
+        const FoldTo to = s + 1 < steps ? kNextX : l.tall ? kResultTall : kResult;
+        const FoldArgs a{x[s % 2], d, to == kNextX ? x[(s + 1) % 2] : out, rows, cols, ldo, batch_o, (uint32_t)cp, k[2],
+                         k[1] + 2.0f * k[2], k[0] + k[1] + k[2], scale};
+        st = rp <= 64    ? run_fold_step<64>(to, l, B, a, stream)
+             : rp <= 128 ? run_fold_step<128>(to, l, B, a, stream)
+             : rp <= 192 ? run_fold_step<192>(to, l, B, a, stream)
+                         : run_fold_step<256>(to, l, B, a, stream);
+        if (st != GR_OK) return st;
+    }
+    return GR_OK;
 }
 
 template <typename Out>
@@ -312,9 +347,10 @@ int orthogonalize_update(int64_t B, int64_t rows, int64_t cols, const void* G, i
     };
     double* const part = reinterpret_cast<double*>(take(l.parts));
     uint16_t* const x[2] = {take(l.x), take(l.x)};
-    uint16_t* const xt[2] = {take(l.x), take(l.x)};
     uint16_t* const a = take(l.a);
-    uint16_t* const b = take(l.a);
+    // (not there where the steps are folded)
+    uint16_t* const xt[2] = {l.fold ? nullptr : take(l.x), l.fold ? nullptr : take(l.x)};
+    uint16_t* const b = l.fold ? nullptr : take(l.a);
     const int64_t rows_pad = l.tall ? l.cp : l.rp, cols_pad = l.tall ? l.rp : l.cp;
     const gr::ortho::PrepArgs prep{G,        rows,     cols,         ldg, batch_g, part, l.tall ? xt[0] : x[0], l.tall ? x[0] : xt[0],
                                    rows_pad, cols_pad, l.rp * l.cp, eps};
@@ -322,6 +358,7 @@ int orthogonalize_update(int64_t B, int64_t rows, int64_t cols, const void* G, i
          : g_fmt == GR_FMT_BF16 ? ortho_prepare<ElemBF16>(prep, B, h)
                                 : ortho_prepare<ElemF16>(prep, B, h);
     if (st != GR_OK) return st;
+    if (l.fold) return run_fold(l, B, rows, cols, k, steps, scale, out, ldo, batch_o, x, a, h);
     return run_ortho<ElemBF16>(l, B, k, steps, scale, out, ldo, batch_o, x, xt, a, b, h);
 }
 

@@ -645,3 +645,23 @@ def test_linear_backward_of_many_tokens(M, N, K):
         check16(g.cpu(), r, g.dtype, b)
     untouched(dw_buf, N, K)
     assert torch.equal(gr.linear_backward(dy.cuda(), x.cuda(), w.cuda(), input_grad=False)[1], dw)
+
+
+@pytest.mark.parametrize("batch,rows,cols", [(1, 33, 4001), (3, 3000, 64), (2, 100, 1500), (2, 1501, 120), (3, 191, 257), (1, 2000, 193),
+                                             (40, 250, 300)])
+def test_orthogonalize_of_a_narrow_side_up_to_256(batch, rows, cols):
+    """Each of the kernel's widths, either way round, one and several blocks of columns to a workgroup; with the outputs
+    apart at odd addresses, and a matrix of NaN beside the others."""
+    log("ortho narrow %d %dx%d" % (batch, rows, cols))
+    g = make((batch, rows, cols), torch.float32, 21)
+    buf = torch.full((batch, rows + 1, cols + 3), 77.0, dtype=torch.bfloat16, device="cuda")
+    out = buf[:, :rows, 1:cols + 1]
+    gr.orthogonalize(g.cuda(), out=out)
+    for i in range(min(batch, 3)):
+        check_ortho(out[i], g[i])
+    want = out.clone()
+    out.fill_(77.0)
+    assert bool((buf == 77).all())
+    g[0, 1, 2] = float("nan")
+    got = gr.orthogonalize(g.cuda())
+    assert bool(got[0].isnan().all()) and torch.equal(got[1:], want[1:])
