@@ -73,20 +73,33 @@ int check_workspace(const void* ws, int64_t bytes, int64_t need) {
 // The kernels of C (M x N) = own epilogue of A Bt^T, both operands k-contiguous, for a
 // type with an epilogue of its own.  `rows` of Bt make a column of C (2: paired).
 enum Kernel { kTile256, kTile128, kStream4, kStream8 };
+static_assert(gr::tile3t::BM == 256 && gr::tile3t::BN == 256 && gr::tile128::BM == 128 && gr::tile128::BN == 128, "sides");
+
+// 256 x 256 tiles, a CU each, rather than 128 x 128, two to a CU: where the former are more
+// than half as many as CUs and, with a short K, their rounds do not take longer.  A round of
+// the latter takes about three quarters of the time, and the last one half of that on average
+// (sums over 64 and 512 of 9536 x 1546, 266 and 975 tiles: 27.5 and 50.8 us with the large ones,
+// 17.0 and 39.8 with the small; 8192 x 4096, 512 and 2048 tiles: 22.5 and 48.3, 28.8 and 58.5;
+// over 2048 of 9536 x 1546: 113 and 117).
+bool large_tiles(int64_t large, int64_t small, int64_t K) {
+    return large > 128 && (K >= 2048 || 6 * small + 1536 > 4096 * ceil_div(large, 256));
+}
 
 // Which of them, for B products at once: up to 64 rows, and products of at most 512 blocks of 64 x 64 (sums of
-// N x rows) with a K long enough to fill them, are streamed; 256 x 256 tiles where there
-// are more than half as many as CUs; else 128 x 128 tiles.  The borders between them are
-// those of the transposed-B ReLU kernels, whose main loops these are.
-Kernel choose(int64_t B, int64_t M, int64_t N, int64_t K, int rows) {
+// N x rows) with a K long enough to fill them, are streamed; else tiles.  The borders between
+// streams and tiles are those of the transposed-B ReLU kernels, whose main loops these are.
+// `triangle`: of N x N only the tiles on and below the diagonal (3000 x 3000 orthogonalised, 78
+// large and 300 small tiles: 1101 us with the large, 957).
+Kernel choose(int64_t B, int64_t M, int64_t N, int64_t K, int rows, bool triangle = false) {
     const int64_t on = kStreamNB / rows;
     const int64_t blocks = B * ceil_div(M, kStreamRows) * ceil_div(N, on);
     if (N >= on && (M <= kStreamRows || (blocks <= 256 && K >= 256) || (blocks <= 512 && K >= 1024)))
         return blocks <= 256 ? kStream8 : kStream4;
-    if (K % gr::tile3t::BKS == 0 && M >= gr::tile3t::BM &&
-        B * ceil_div(M, gr::tile3t::BM) * ceil_div(N, gr::tile3t::BN / rows) > 128)
-        return kTile256;
-    return kTile128;
+    auto tiles = [&](int64_t side) {
+        const int64_t m = ceil_div(M, side), n = ceil_div(N, side / rows);
+        return B * (triangle ? m * (m + 1) / 2 : m * n);
+    };
+    return K % gr::tile3t::BKS == 0 && M >= gr::tile3t::BM && large_tiles(tiles(256), tiles(128), K) ? kTile256 : kTile128;
 }
 
 constexpr uint32_t kGroupM = 4;  // tile rows that walk the columns together (see tile_of_workgroup)
@@ -263,7 +276,7 @@ template <typename In>
 int symmetric(int64_t B, int64_t N, int64_t K, const uint16_t* A, int64_t lda, uint16_t* C, int64_t ldc,
               gr::own::PolyArgs ep, hipStream_t stream) {
     using namespace gr::own;
-    const Kernel kernel = choose(B, N, N, K, 1);
+    const Kernel kernel = choose(B, N, N, K, 1, true);
     if (kernel == kStream4 || kernel == kStream8) {
         ep.ct = nullptr;
         return product<Poly<In, In, false>>(kernel, B, N, N, K, A, lda, A, lda, C, ldc, ep, stream);
