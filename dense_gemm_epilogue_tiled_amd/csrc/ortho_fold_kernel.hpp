@@ -5,7 +5,7 @@
 //   X <- (a + b + c) X + (b + 2 c) Y + c D Y
 //
 // which is a X + (b A + c A A) X.  B is never formed: two launches a step, not three (8 x
-// 256 x 1024, five steps: 96 us against 126), and X is kept in one layout, not in two.  D and Y,
+// 256 x 1024, five steps: 87 us against 126), and X is kept in one layout, not in two.  D and Y,
 // both small where the iteration ends, are rounded to fp16 (D times SCALE_A, Y times SCALE_Y);
 // Y's own multiple is added before its rounding.
 //

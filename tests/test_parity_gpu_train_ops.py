@@ -665,3 +665,38 @@ def test_orthogonalize_of_a_narrow_side_up_to_256(batch, rows, cols):
     g[0, 1, 2] = float("nan")
     got = gr.orthogonalize(g.cuda())
     assert bool(got[0].isnan().all()) and torch.equal(got[1:], want[1:])
+
+
+@pytest.mark.parametrize("rows,cols", [(200, 1300), (1300, 200)])
+def test_orthogonalize_of_a_narrow_side_arguments(rows, cols):
+    """One step, which is the last; other coefficients, steps and a scale."""
+    log("ortho narrow arguments %dx%d" % (rows, cols))
+    g = make((rows, cols), torch.float32, 22)
+    check_ortho(gr.orthogonalize(g.cuda(), steps=1), g, steps=1)
+    check_ortho(gr.orthogonalize(g.cuda(), steps=8, coefficients=(15 / 8, -10 / 8, 3 / 8), scale=0.25), g, 8,
+                (15 / 8, -10 / 8, 3 / 8), 0.25)
+
+
+def test_small_gradients_and_narrow_updates_in_a_graph():
+    """Ranges of tokens, two products in a launch, updates in two launches a step: replayed on new inputs, with eager
+    calls in between, and the same bits as eager calls."""
+    log("graph of small gradients and narrow updates")
+    M, N, K = 5000, 200, 131
+    dy, x = make((M, N), "bf16", 31).cuda(), make((M, K), "bf16", 32).cuda()
+    w, a = make((N, K), "bf16", 33).cuda(), make((2, 160, 500), torch.float32, 34).cuda()
+
+    def work():
+        return (*gr.linear_backward(dy, x, w, bias=True), gr.orthogonalize(a))
+
+    work()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = work()
+    for seed in range(4):
+        for t in (dy, x, w, a):
+            t.copy_(make(tuple(t.shape), t.dtype, 40 + seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, want in zip(held, work()):
+            assert torch.equal(got, want)
