@@ -104,7 +104,8 @@ int run_sandwich_backward(const gr::sandwich::BwdArgs& a, hipStream_t stream) {
             return a.split > 0 ? launch(backward_kernel<E, TPR, C, true, false>, grid, threads, stream, a)
                                : launch(backward_kernel<E, TPR, C, false, false>, grid, threads, stream, a);
         });
-    if (st != GR_OK || a.part == nullptr) return st;
+    // (not by the partial sums' address: without rows there are none, and the sums are zeros)
+    if (st != GR_OK || !(a.dw || a.dnext_w || a.dgate)) return st;
     return launch_grid(reduce_kernel<E>, dim3((uint32_t)ceil_div(a.N, REDUCE_COLS), 2), 256, stream, a);
 }
 

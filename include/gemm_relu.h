@@ -1083,8 +1083,9 @@ int sandwich_norm_fwd(int64_t M, int64_t N,
  * sandwich_norm_bwd -- its gradients from dT and dN, those of total and normed (NULL:
  * zeros, one of them at least is there): dY, dR (M x N), and where they are not NULL dw,
  * dnext_w (N values; dnext_w needs dN), dgate (G x N; needs gate).  Y and T are the
- * forward pass's Y and total.  Sums over rows are fp32 in a fixed order.  The workspace holds their partial
- * sums; a call that asks for none of the three needs none.
+ * forward pass's Y and total.  Sums over rows are fp32 in a fixed order; with M = 0 they are zeros.  The
+ * workspace holds their partial sums; a call that asks for none of the three needs none, nor does one
+ * with M = 0.
  */
 int sandwich_norm_bwd_workspace_size(int64_t M, int64_t N, int64_t G, int64_t* bytes);
 

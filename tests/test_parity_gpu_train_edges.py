@@ -1,0 +1,77 @@
+"""GPU tests of the training operators where a call has nothing to sum or leaves a type's range."""
+import pytest
+import torch
+
+import dense_gemm_epilogue_tiled_amd as gr
+from gpu_util import log
+from train_ref import TYPES
+
+pytestmark = pytest.mark.gpu
+
+
+def nans(*shape, dtype=torch.bfloat16):
+    return torch.full(shape, float("nan"), dtype=dtype, device="cuda")
+
+
+def norm_bwd_without_rows(N, w, gate, G, dw, dnext, dgate, fmt=gr.GR_FMT_BF16, ws=None):
+    at = [None if t is None else t.data_ptr() for t in (w, w, gate if G else None, dw, dnext, dgate if G else None, ws)]
+    return gr.sandwich_norm_bwd(0, N, None, N, None, N, None, N, None, N, *at[:3], G, N, 1.0, 1e-6, None, N, None, N, *at[3:6], N,
+                                fmt, at[6], 0 if ws is None else ws.numel(), torch.cuda.current_stream().cuda_stream)
+
+
+def used_memory():
+    """Leaves the allocator's small free blocks full of NaN: an output that nothing writes shows."""
+    blocks = [nans(n) for n in (64, 256, 2048, 20000) for _ in range(24)]
+    torch.cuda.synchronize()
+    del blocks
+
+
+# ---- no rows -----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("workspace", [False, True])
+@pytest.mark.parametrize("G", [0, 1, 3])
+@pytest.mark.parametrize("N", [1, 40, 1030])
+def test_norm_gradients_without_rows_are_written(N, G, workspace, dtype):
+    """Zeros, with a workspace and without: no rows need none."""
+    log("norm without rows N %d G %d %s" % (N, G, dtype))
+    kind = TYPES[dtype]
+    w, gate = torch.ones(N, dtype=kind, device="cuda"), torch.ones(max(G, 1), N, dtype=kind, device="cuda")
+    dw, dnext, dgate = nans(N, dtype=kind), nans(N, dtype=kind), nans(max(G, 1), N, dtype=kind)
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda") if workspace else None
+    assert gr.sandwich_norm_bwd_workspace_size(0, N, G) == (gr.GR_OK, 0)
+    st = norm_bwd_without_rows(N, w, gate, G, dw, dnext, dgate, gr.GR_FMT_BF16 if dtype == "bf16" else gr.GR_FMT_F16, ws)
+    assert st == gr.GR_OK
+    for g in (dw, dnext, dgate)[:3 if G else 2]:
+        assert bool((g == 0).all())
+
+
+@pytest.mark.parametrize("G", [0, 1, 3])
+def test_norm_gradients_without_rows_one_by_one(G):
+    """Each sum alone; the others' places stay as they are."""
+    N = 40
+    w, gate = torch.ones(N, dtype=torch.bfloat16, device="cuda"), torch.ones(max(G, 1), N, dtype=torch.bfloat16, device="cuda")
+    for wanted in range(3 if G else 2):
+        out = [nans(N), nans(N), nans(max(G, 1), N)]
+        given = [t if i == wanted else None for i, t in enumerate(out)]
+        st = norm_bwd_without_rows(N, w, gate, G, *given)
+        assert st == gr.GR_OK
+        for i, t in enumerate(out):
+            assert bool((t == 0).all() if i == wanted else t.isnan().all())
+
+
+def test_helpers_gradients_without_rows_are_written():
+    """Every gradient of a batch without tokens, in memory that held NaN."""
+    w, y = torch.ones(64, 32, dtype=torch.bfloat16, device="cuda"), torch.empty(0, 32, dtype=torch.bfloat16, device="cuda")
+    one, gates = torch.ones(32, dtype=torch.bfloat16, device="cuda"), torch.ones(5, 32, dtype=torch.bfloat16, device="cuda")
+    gu = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    for gate in (None, one, gates):
+        used_memory()
+        got = gr.sandwich_norm_backward(y, y, y, y, one, one, gate)[2:]
+        assert all(g is None if gate is None and i == 2 else bool((g == 0).all()) for i, g in enumerate(got))
+    for call in (lambda out: gr.linear_backward(gu, y, w, bias=True, dw_out=out),
+                 lambda out: gr.gated_linear_backward(y, y, w, gu, bias=True, dw_out=out)):
+        used_memory()
+        out = nans(64, 32)
+        _, dw, db = call(out)
+        assert dw.data_ptr() == out.data_ptr() and bool((dw == 0).all()) and bool((db == 0).all())
