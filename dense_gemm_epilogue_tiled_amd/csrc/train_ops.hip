@@ -305,6 +305,13 @@ int gated_layout(int64_t M, int64_t I, int64_t H, const uint16_t* W, int64_t ldw
     return input_grad_layout(M, H, 2 * I, place, least(ld), true, W, ldw, dX, lddx, &l->input);
 }
 
+// Sides that the size and the call take alike.
+int check_gated_backward(int64_t M, int64_t I, int64_t H) {
+    const int dims = check_dims({M, I, 2 * I, H});
+    if (dims != GR_OK) return dims;
+    return padded_tokens(M) > kMaxPitch || 2 * I + 64 > kMaxPitch ? GR_ERR_TOO_LARGE : GR_OK;
+}
+
 int validate_gated_backward(int64_t M, int64_t I, int64_t H, const uint16_t* dH, int64_t lddh, const uint16_t* X,
                             int64_t ldx, const uint16_t* W, int64_t ldw, const uint16_t* GU, int64_t ldgu,
                             const uint16_t* dX, int64_t lddx, const uint16_t* dW, int64_t lddw, const uint16_t* dB) {
@@ -316,8 +323,7 @@ int validate_gated_backward(int64_t M, int64_t I, int64_t H, const uint16_t* dH,
     const bool any = dX || dW || dB;
     if (any && M > 0 && I > 0 && (!dH || !GU)) return GR_ERR_NULL_PTR;
     if (M > 0 && I > 0 && H > 0 && ((dX && !W) || (dW && !X))) return GR_ERR_NULL_PTR;
-    if (padded_tokens(M) > kMaxPitch || 2 * I + 64 > kMaxPitch) return GR_ERR_TOO_LARGE;
-    return GR_OK;
+    return check_gated_backward(M, I, H);
 }
 
 template <typename Base>
@@ -354,6 +360,7 @@ int gated_linear_workspace_size(int64_t M, int64_t I, int64_t H, int64_t* bytes)
     if (!bytes) return GR_ERR_INVALID_ARG;
     const int dims = check_dims({M, I, 2 * I, H});
     if (dims != GR_OK) return dims;
+    if (M > 0 && I > 0 && H > kMaxPitch) return GR_ERR_TOO_LARGE;  // (no pitch fits: the call refuses it)
     *bytes = gated_need(M, I, H);
     return GR_OK;
 }
@@ -429,8 +436,10 @@ int gated_linear_backward_workspace_size(int64_t M, int64_t I, int64_t H, const 
     if (dims != GR_OK) return dims;
     if (dX && (ldw < least(H) || lddx < least(H))) return GR_ERR_INVALID_LD;
     if (M > 0 && I > 0 && H > 0 && dX && !W13) return GR_ERR_NULL_PTR;
+    int st = check_gated_backward(M, I, H);
+    if (st != GR_OK) return st;
     GradLayout l;
-    const int st = gated_layout(M, I, H, W13, ldw, dX, lddx, dW13, dB13, &l);
+    st = gated_layout(M, I, H, W13, ldw, dX, lddx, dW13, dB13, &l);
     *bytes = l.total();
     return st;
 }

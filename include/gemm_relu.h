@@ -997,7 +997,7 @@ int moe_w4(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk,
  *   GU, ldgu   M x 2I in fmt: g and u rounded, what gated_linear_backward needs; or NULL
  * The activations are those of gemm_bias_act_bt.  Rows may start at any address; any H runs, one that is no
  * multiple of 32 on copies of X and W13 in the workspace.  Pitches of X and W13 above
- * 2^22 are GR_ERR_TOO_LARGE.
+ * 2^22, and with them H, are GR_ERR_TOO_LARGE.
  */
 int gated_linear_workspace_size(int64_t M, int64_t I, int64_t H, int64_t* bytes);
 
@@ -1040,7 +1040,8 @@ int linear_backward(int64_t M, int64_t N, int64_t K,
  *   dg = dH * u * act'(g),  du = dH * act(g)      (fp32, rounded to fmt: infinite
  *                                                  beyond its range)
  *   dX := (dg, du) * W13 (M x H),  dW13 := (dg, du)^T * X (2I x H),  dB13 := the sums of (dg, du)
- * as in linear_backward.  The derivative of GR_ACT_RELU at 0 is 0.
+ * as in linear_backward.  The derivative of GR_ACT_RELU at 0 is 0.  M above 2^22 and 2I above
+ * 2^22 - 64 are GR_ERR_TOO_LARGE.
  */
 int gated_linear_backward_workspace_size(int64_t M, int64_t I, int64_t H,
                                          const uint16_t* W13, int64_t ldw,
