@@ -101,10 +101,10 @@ __global__ void __launch_bounds__(THREADS) relayout_kernel(Jobs jobs) {
 
 // ---- the gated activation's backward pass -----------------------------------------------
 
-// An activation's value and derivative.  Sigmoid's complement is taken as the sigmoid of
-// -x, so that neither side of 0 cancels.
+// An activation's value and derivative at a finite x.  Sigmoid's complement is taken as the
+// sigmoid of -x, so that neither side of 0 cancels.
 template <int A>
-__device__ __forceinline__ void value_and_slope(float x, float& a, float& d) {
+__device__ __forceinline__ void value_and_slope_within(float x, float& a, float& d) {
     if constexpr (A == kActRelu) {
         a = x > 0.0f ? x : 0.0f;
         d = x > 0.0f ? 1.0f : 0.0f;
@@ -133,6 +133,18 @@ __device__ __forceinline__ void value_and_slope(float x, float& a, float& d) {
     } else {
         a = x;
         d = 1.0f;
+    }
+}
+
+// The same at any x, with the limits at an infinity (not 0 times infinity): a gate beyond the
+// type's range is kept as one, where the forward pass had a finite sum.
+template <int A>
+__device__ __forceinline__ void value_and_slope(float x, float& a, float& d) {
+    if constexpr (A == kActGelu || A == kActGeluTanh || A == kActSilu) {
+        value_and_slope_within<A>(__builtin_isinf(x) ? __builtin_copysignf(__FLT_MAX__, x) : x, a, d);
+        if (x == __builtin_inff()) a = x;
+    } else {
+        value_and_slope_within<A>(x, a, d);
     }
 }
 

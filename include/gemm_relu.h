@@ -1040,8 +1040,9 @@ int linear_backward(int64_t M, int64_t N, int64_t K,
  *   dg = dH * u * act'(g),  du = dH * act(g)      (fp32, rounded to fmt: infinite
  *                                                  beyond its range)
  *   dX := (dg, du) * W13 (M x H),  dW13 := (dg, du)^T * X (2I x H),  dB13 := the sums of (dg, du)
- * as in linear_backward.  The derivative of GR_ACT_RELU at 0 is 0.  M above 2^22 and 2I above
- * 2^22 - 64 are GR_ERR_TOO_LARGE.
+ * as in linear_backward.  The derivative of GR_ACT_RELU at 0 is 0.  At a g that GU holds as an
+ * infinity (one beyond float16's range, say) act and act' are their limits there.  M above 2^22 and
+ * 2I above 2^22 - 64 are GR_ERR_TOO_LARGE.
  */
 int gated_linear_backward_workspace_size(int64_t M, int64_t I, int64_t H,
                                          const uint16_t* W13, int64_t ldw,

@@ -3,10 +3,14 @@ import pytest
 import torch
 
 import dense_gemm_epilogue_tiled_amd as gr
+import train_ref
 from gpu_util import log
-from train_ref import TYPES
+from mx_ref import check16
+from train_ref import TYPES, make
 
 pytestmark = pytest.mark.gpu
+
+INF = float("inf")
 
 
 def nans(*shape, dtype=torch.bfloat16):
@@ -75,3 +79,48 @@ def test_helpers_gradients_without_rows_are_written():
         out = nans(64, 32)
         _, dw, db = call(out)
         assert dw.data_ptr() == out.data_ptr() and bool((dw == 0).all()) and bool((db == 0).all())
+
+
+# ---- gates beyond the type's range ----------------------------------------------------------
+
+# value and slope at -infinity and at +infinity
+LIMITS = {"none": (-INF, 1, INF, 1), "relu": (0, 0, INF, 1), "gelu": (0, 0, INF, 1), "gelu_tanh": (0, 0, INF, 1), "silu": (0, 0, INF, 1),
+          "sigmoid": (0, 0, 1, 0), "tanh": (-1, 0, 1, 0)}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("name", LIMITS)
+def test_gated_backward_of_infinite_gates(name, dtype):
+    """The activation's limits, and NaN for NaN alone."""
+    low, low_slope, high, high_slope = LIMITS[name]
+    gu = torch.tensor([[-INF, INF, float("nan"), 0.5] + [2.0] * 4], dtype=TYPES[dtype])
+    dh, w = torch.full((1, 4), 0.5, dtype=TYPES[dtype]), torch.zeros(8, 32, dtype=TYPES[dtype])
+    db = gr.gated_linear_backward(dh.cuda(), None, w.cuda(), gu.cuda(), act=name, bias=True, input_grad=False, weight_grad=False)[2].tolist()
+    assert db[:2] == [low_slope * 1.0, high_slope * 1.0] and db[4:6] == [low * 0.5, high * 0.5], db
+    assert db[2] != db[2] or name in ("relu", "none")  # the slopes of these are constants
+    assert db[6] != db[6] or name == "relu" and db[6] == 0
+    assert all(v == v for v in (db[3], db[7]))
+
+
+@pytest.mark.parametrize("name", ["relu", "gelu", "gelu_tanh", "silu", "sigmoid"])
+def test_gradients_of_gates_far_below_float16(name):
+    """Gates whose sums are finite and beyond float16's range: the forward pass gives zeros there, and the gradients are
+    finite and those of the sums."""
+    M, I, H = 70, 40, 64
+    log("far gates %s" % name)
+    x, w, dh = make((M, H), "f16", 11), make((2 * I, H), "f16", 12, H ** -0.5), make((M, I), "f16", 13)
+    x[:, 0], w[3, 0], w[7, 0] = 60.0, -2000.0, -30000.0
+    h, gu = gr.gated_linear(x.cuda(), w.cuda(), act=name, keep=True)
+    sums = x.double() @ w.double().T
+    assert bool((gu[:, [3, 7]] == -INF).all()) and float(sums[:, [3, 7]].max()) < -65536
+    assert bool(gu[:, [c for c in range(2 * I) if c not in (3, 7)]].isfinite().all()) and not h[:, [3, 7]].any()
+    got = gr.gated_linear_backward(dh.cuda(), x.cuda(), w.cuda(), gu, act=name, bias=True)
+    # at -100 as at the sums every value and slope is below 1e-40
+    kept = gu.cpu().double()
+    kept[:, [3, 7]] = -100.0
+    refs, bounds = train_ref.gated_backward(dh, x, w, kept, name)
+    for g, r, b in zip(got, refs, bounds):
+        assert bool(r.isfinite().all())
+        check16(g.cpu(), r, g.dtype, b)
+    none = [3, 7, I + 3, I + 7]
+    assert not got[1][none].any() and not got[2][none].any()
