@@ -59,6 +59,19 @@ __device__ __forceinline__ void load8(const void* row, int64_t c, int n, float (
 template <typename In>
 constexpr int kBytes = __is_same(In, ElemF32) ? 4 : 2;
 
+// What a value is multiplied by to become one of X: SCALE_X / (norm + eps), as a factor of about
+// 1 and a power of two, since fp32 does not hold it where the norm is below 2.4e-35.  A zero
+// matrix without an eps stays zero.
+struct Factor {
+    float f;
+    int e;
+    __device__ __forceinline__ Factor(double squares, float eps) : f(0.0f), e(0) {
+        const double norm = __builtin_sqrt(squares) + (double)eps;
+        if (norm != 0.0) f = (float)frexp((double)SCALE_X / norm, &e);
+    }
+    __device__ __forceinline__ float operator()(float v) const { return ldexpf(v, e) * f; }
+};
+
 struct PrepArgs {
     const void* src;
     int64_t rows, cols, ld, batch;  // of the update, batch: elements from one matrix to the next
@@ -116,14 +129,14 @@ __global__ void __launch_bounds__(256) normalise_kernel(PrepArgs a, uint32_t til
     if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = sum;
     __syncthreads();
     sum = ((red[0] + red[1]) + red[2]) + red[3];
-    const float f = (float)((double)SCALE_X / (__builtin_sqrt(sum) + (double)a.eps));
+    const Factor scaled(sum, a.eps);
     uint16_t* const x = a.x + blockIdx.y * a.batch_x;  // (not used where there is none)
     uint16_t* const xt = a.xt + blockIdx.y * a.batch_x;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const uint32_t o = threadIdx.x + 256 * i;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] *= f;
+        for (int e = 0; e < 8; ++e) v[i][e] = scaled(v[i][e]);
         const u32x4 w = own::round8<ElemF16>(v[i]);
         if (a.x != nullptr) *reinterpret_cast<u32x4*>(x + (r0 + o / 8) * a.cols_pad + c0 + 8 * (o % 8)) = w;
         *reinterpret_cast<u32x4*>(lds + train::tile_off(o / 8, o % 8)) = w;

@@ -179,10 +179,10 @@ __global__ void __launch_bounds__(SMALL_THREADS) small_kernel(SmallArgs a) {
     sum = 0.0;
 #pragma unroll
     for (int i = 0; i < SMALL_WAVES; ++i) sum += red[i];
-    const float f = (float)((double)SCALE_X / (__builtin_sqrt(sum) + (double)a.eps));
+    const Factor scaled(sum, a.eps);
     each([&](uint32_t r, uint32_t c, int n, float (&v)[8]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= f;
+        for (int i = 0; i < 8; ++i) v[i] = scaled(v[i]);
         const u32x4 w = own::round8<ElemF16>(v);  // zeros behind the row's end
         if (!a.tall) {
             *(GR_LDS u32x4*)(x + xp.chunk(r, c >> 3)) = w;

@@ -1117,8 +1117,8 @@ int sandwich_norm_bwd(int64_t M, int64_t N,
  * rounded to fp16 each step.  They stay finite while X's singular values, which begin at 1 at
  * most, are below 4 and B's elements below 64 (with the usual coefficients: singular values
  * below 2.6; they stay below 1.3).  Sides up to 65536, B up to 65535 (GR_ERR_TOO_LARGE), 1 to
- * 64 steps (GR_ERR_INVALID_ARG).  A zero matrix gives zeros, one with an infinity or a NaN
- * gives NaN.
+ * 64 steps (GR_ERR_INVALID_ARG).  A zero matrix gives zeros, with an eps of 0 too, and one with an
+ * infinity or a NaN gives NaN.
  */
 #define GR_FMT_F32 2
 int orthogonalize_workspace_size(int64_t B, int64_t rows, int64_t cols, int64_t* bytes);

@@ -124,3 +124,33 @@ def test_gradients_of_gates_far_below_float16(name):
         check16(g.cpu(), r, g.dtype, b)
     none = [3, 7, I + 3, I + 7]
     assert not got[1][none].any() and not got[2][none].any()
+
+
+# ---- updates at the ends of the range without an eps ----------------------------------------
+
+# one workgroup's, two launches a step, three launches a step; wide and tall
+UPDATES = [(8, 8), (70, 70), (128, 500), (500, 100), (200, 1300), (1300, 150), (600, 700), (700, 600)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16], ids=["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,cols", UPDATES)
+def test_zero_update_without_eps(rows, cols, dtype):
+    """Zeros beside a matrix that is not: zeros, and the other's own result."""
+    g = torch.stack((torch.zeros(rows, cols), make((rows, cols), torch.float32, 21))).to(dtype)
+    got = gr.orthogonalize(g.cuda(), eps=0.0)
+    assert bool((got[0] == 0).all())
+    assert torch.equal(got[1], gr.orthogonalize(torch.stack((g[1], g[1])).cuda(), eps=0.0)[1])
+    assert bool((gr.orthogonalize(g[:1].cuda(), eps=0.0) == 0).all())
+
+
+@pytest.mark.parametrize("scale", [1e-44, 1e-41, 1e-37, 1e-36, 1e38])
+@pytest.mark.parametrize("rows,cols", UPDATES)
+def test_update_far_from_one_without_eps(rows, cols, scale):
+    """fp32's subnormal and largest numbers: the result of the same matrix anywhere else, to the operands' roundings in
+    fp16 (as if they fell at other places: twice) and the result's in bfloat16."""
+    log("ortho %dx%d times %g" % (rows, cols, scale))
+    g = (make((rows, cols), torch.float64, 22).clamp(-3, 3) * scale).float()
+    ref = train_ref.newton_schulz(g, 5, eps=0.0)
+    held = train_ref.newton_schulz(g, 5, eps=0.0, rounded=True)
+    got = gr.orthogonalize(g.cuda(), eps=0.0).cpu().double()
+    assert (got - ref).norm() <= 2 * (held - ref).norm() + 2.0 ** -8 * ref.norm()
