@@ -14,8 +14,10 @@
 // where the iteration ends (the result's error before its own rounding, 256 x 1024: 1.1e-3
 // against 1.5e-3 with a X + (b A + c A A) X).  The elements
 // are bounded by the singular values, and small by the matrix's size: X times
-// 2^13 and A and B times 2^10 keep singular values up to 8 finite and the elements
-// of a random 8192 x 8192 matrix (1e-4 in X, 4e-6 in A) normal numbers.
+// 2^13 and A and B times 2^10 keep the elements of a random 8192 x 8192 matrix (1e-4 in X,
+// 4e-6 in A) normal numbers.  Above, B's elements have to stay below 64 (with the usual
+// coefficients: singular values below 2.6), and singular values below 8 for A, or below 4
+// for the (A - I) X of the form with two launches.
 //
 // Rows and columns are padded by zeros to multiples of 64, which the iteration keeps:
 // the products see whole strips whatever the matrix.

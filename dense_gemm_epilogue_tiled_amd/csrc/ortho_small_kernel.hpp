@@ -1,8 +1,16 @@
 // The whole orthogonalisation of a small matrix in one workgroup: X (r x c, fp16) and A (r x
-// r) stay in its LDS for all steps, where a step is otherwise three launches of a few
-// microseconds each (128 x 512: 93 us for five steps, 65 here; 64 x 64: 76 and 14).  r and c are
-// padded by zeros to multiples of 64, r to 64 or 128, and 2 r (c + r) bytes have to fit 160
-// KiB.
+// r) stay in its LDS for all steps, where a step is otherwise two launches of a few
+// microseconds each.  r and c are padded by zeros to multiples of 64, r to 64 or 128, and 2 r (c + r)
+// bytes have to fit 160 KiB: the border is what fits.  Five steps in us, bfloat16, replayed in a
+// graph, as two launches a step and here:
+//
+//                64 x 64     64 x 640    128 x 128   128 x 256   128 x 512
+//   1 matrix     33   15     41   41     49   31     44   41     48   67
+//   8                        45   42                 48   41     55   68
+//   300          105  28                             196  82     295  147
+//
+// (1000 of 128 x 512: 757 and 309.)  So one workgroup a matrix is the faster form but for a few
+// matrices of the longest, whose columns one CU works off alone.
 //
 //   A = X X^T       32 x 32 tiles on and below the diagonal, a wave each; both operands are
 //                   rows of X, which the matrix instruction wants as they lie; a tile

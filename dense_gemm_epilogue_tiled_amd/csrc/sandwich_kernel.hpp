@@ -20,7 +20,8 @@
 // most C chunks of 8 columns each.  Backward, a thread keeps its columns' sums in
 // registers over the rows of its workgroup (one chunk per thread up to 8192 columns: with two, half
 // as many waves find room, 8192 x 8192 201 us against 190; beyond that the sums do not all
-// fit and some are spilled), so that only one partial sum per workgroup (or wave,
+// fit and some are spilled: of the same bytes 4096 x 16384 takes 384 us and 2048 x 32768 894, and
+// rows that are no multiples of 8, which load with branches, half as much again or more), so that only one partial sum per workgroup (or wave,
 // where a wave holds a row) and column goes through memory; a second kernel adds
 // those in a fixed order.
 #pragma once

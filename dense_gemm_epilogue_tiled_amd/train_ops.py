@@ -16,7 +16,9 @@ import ctypes
 from . import GR_FMT_BF16, _ptr, lib
 from .mx_ops import _act, _run, _workspace
 
-QUINTIC = (3.4445, -4.7750, 2.0315)  # Newton-Schulz coefficients: steep at 0, between 0.7 and 1.2 near 1
+# Newton-Schulz coefficients, steep at 0 and between 0.7 and 1.2 near 1; published in K. Jordan et al., "Muon: An optimizer
+# for hidden layers in neural networks", 2024
+QUINTIC = (3.4445, -4.7750, 2.0315)
 
 
 # ---- raw calls --------------------------------------------------------------------
@@ -149,7 +151,8 @@ def sandwich_norm(y, residual, weight=None, next_weight=None, gate=None, scale=1
 def sandwich_norm_backward(dtotal, dnormed, y, total, weight=None, next_weight=None, gate=None, scale=1.0, eps=1e-6,
                            workspace="auto", stream=None):
     """``(dy, dresidual, dweight, dnext_weight, dgate)`` of sandwich_norm from the gradients of total and normed
-    (None for zeros, not both), ``y`` and its ``total``.  The gradient of what is None is None."""
+    (None for zeros, not both), ``y`` and its ``total``.  The gradient of what is None is None, and without ``dnormed``
+    that of next_weight; with no rows those of the weights and gates are zeros."""
     return _run("sandwich_norm_backward", "sandwich_norm_bwd", stream, y, dtotal, dnormed, total, weight, next_weight, gate,
                 scale, eps, _workspace(workspace))
 

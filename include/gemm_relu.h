@@ -1107,7 +1107,8 @@ int sandwich_norm_bwd(int64_t M, int64_t N,
  * orthogonalize_update -- out := scale * X after `steps` of
  *   A = X X^T,  X <- a X + (b A + c A A) X,   from X = G / (Frobenius norm of G + eps),
  * for each of B matrices: singular values go through a s + b s^3 + c s^5 each step, and with
- * the usual coefficients (3.4445, -4.7750, 2.0315) all but the smallest end near 1.
+ * the usual coefficients (3.4445, -4.7750, 2.0315; K. Jordan et al., "Muon: An optimizer for hidden
+ * layers in neural networks", 2024) all but the smallest end near 1.
  *   G          B x rows x cols in g_fmt (GR_FMT_F16, GR_FMT_BF16 or GR_FMT_F32), pitch ldg and
  *              batch_g elements from one matrix to the next (of no meaning for B = 1)
  *   coefficients  a, b, c: host memory

@@ -41,7 +41,8 @@ def untouched(buf, rows, cols):
 
 # ---- gated linear ------------------------------------------------------------------------
 
-# M, I, H: the small-M stream (H % 256 == 0), the 64 x 64 stream, 128 and 256 tiles with ragged and whole edges, packed H
+# M, I, H: the kernel for up to 4 tokens, the small-M stream (H % 256 == 0), streamed blocks, 128 x 128 tiles with ragged
+# edges, 256 x 256 tiles of one strip, packed H (test_parity_gpu_train_paths.py has sizes for each kernel by name)
 GATED = [(1, 64, 256), (1, 33, 512), (16, 70, 256), (2, 5, 256), (3, 40, 288), (17, 33, 96), (64, 32, 32), (65, 100, 320),
          (130, 31, 64), (5, 1, 32), (200, 2100, 64), (129, 2049, 160), (257, 8200, 64), (512, 16384, 64), (300, 9000, 192),
          (1, 40, 7), (9, 70, 100), (70, 20, 33), (300, 8300, 90), (4, 8, 0)]
